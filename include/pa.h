@@ -375,6 +375,181 @@ int pa_copy_blocks(void *const *kv_caches, int num_layers,
                    int head_size, int dtype, pa_stream_t stream);
 
 /*
+ * pa_build_step — a serving step's index inputs, built on the GPU: from the
+ * sequences' lengths and each request's count of new tokens, the block tables
+ * are extended from a device free list and the positions, slots, offsets and
+ * lengths of the step are written, so that a whole step (this call,
+ * pa_rope_and_cache or pa_reshape_and_cache, pa_prefill or pa_decode) runs
+ * from a CUDA graph without the host knowing the tables. The bookkeeping is
+ * that of the host allocator below ([book] §4.4.1, §4.4.3; [codex] §4.3), for
+ * blocks that one sequence holds alone (no reference counts, no copy on
+ * write). With b(x) = ceil(x / block_size):
+ *   1. every row with query_lens[s] < 0 (a finished sequence), in row order,
+ *      returns its b(seq_lens[s]) blocks to the free list, the last logical
+ *      block first, as pa_alloc_free_seq does; its length becomes 0;
+ *   2. every row with query_lens[s] = q > 0, in row order, takes
+ *      b(seq_lens[s] + q) - b(seq_lens[s]) blocks from the free list for its
+ *      next logical blocks, as q pa_alloc_append_token calls do; its length
+ *      grows by q. Rows with query_lens[s] = 0 stay as they are.
+ * Rows are served in order until one needs more blocks than are left or more
+ * tokens than token_capacity leaves: that row and all later ones get nothing
+ * this step (as with query_lens 0; finished rows are still returned).
+ *
+ *   block_tables   device, [num_seqs][max_blocks_per_seq] int32, in and out:
+ *                  only the entries of newly taken blocks are written
+ *   seq_lens       device, [num_seqs] int32: tokens cached before the step
+ *   query_lens     device, [num_seqs] int32: new tokens; 0 idle; < 0 finished
+ *   free_list      device, [num_blocks] int32, in and out: a stack, the next
+ *                  block to hand out last. Entries [0, *num_free) are free;
+ *                  those behind the new count are left as they were. The
+ *                  order {b0, b1, ...} of pa_alloc_create is its reverse.
+ *   num_free       device, [1] int32
+ *   seq_lens_out, num_free_out: the new lengths and count; may be seq_lens and
+ *                  num_free themselves (in place). No other overlap of an
+ *                  input with an output, or of two outputs, is allowed.
+ *   cu_seqlens_q   device, [num_seqs + 1] int32 out: first token of each row
+ *   positions      device, [token_capacity] int32 out, or NULL: each token's
+ *                  position in its sequence; 0 behind the last token
+ *   slot_mapping   device, [token_capacity] int32 out: each token's slot; -1
+ *                  (skipped by the writes) behind the last token
+ *   num_admitted   device, [1] int32 out: the first row that got nothing for
+ *                  want of blocks or tokens, num_seqs if none
+ *   num_seqs <= 4096; num_blocks * block_size <= 2^31 - 1
+ * A row whose length is negative or would pass max_blocks_per_seq *
+ * block_size sets PA_DEVERR_SEQ_LEN, keeps its length and neither takes nor
+ * returns blocks. A block id outside the pool that is taken or found in a
+ * table sets PA_DEVERR_BLOCK_ID; its tokens' slots are -1. A free count
+ * outside [0, num_blocks], or blocks returned beyond num_blocks in all, set
+ * PA_DEVERR_BLOCK_ID too, and the count is held to that range. One launch;
+ * reads only what earlier work on the stream has written. Deterministic.
+ * Returns PA_OK or a PA_ERR_* code.
+ */
+int pa_build_step(int32_t *block_tables, int max_blocks_per_seq, const int32_t *seq_lens,
+                  const int32_t *query_lens, int num_seqs, int32_t *free_list,
+                  const int32_t *num_free, int32_t *seq_lens_out, int32_t *num_free_out,
+                  int32_t *cu_seqlens_q, int32_t *positions, int32_t *slot_mapping,
+                  int token_capacity, int32_t *num_admitted, int num_blocks, int block_size,
+                  pa_stream_t stream);
+
+/*
+ * pa_rope_plan — the rotary frequencies in the form pa_rope_and_cache reads
+ * (host to host; copy the plan to the device once). Pair i turns by
+ * inv_freq[i] radians per position of axis pair_axes[i] (NULL: axis 0 for
+ * all; else each in [0, 4)); inv_freq is within +-2^32 (scaled and
+ * extended-context variants included). plan receives num_pairs words: the
+ * turns per position as a 62-bit fraction of a turn, the axis in the low two
+ * bits. Returns PA_OK or a PA_ERR_* code.
+ */
+int pa_rope_plan(const double *inv_freq, const int32_t *pair_axes, int num_pairs,
+                 uint64_t *plan);
+
+/*
+ * pa_rope_and_cache — rotary positions on this step's queries and keys, and
+ * pa_reshape_and_cache of the rotated keys and the values, in one pass. With
+ * several axes (time, height, width) the pairs of a head are shared out among
+ * the axes by the plan, and a token has one position per axis.
+ *
+ *   query_out      device, [num_tokens] rows of [num_q_heads][head_size],
+ *                  query_out_stride elements apart; may be query itself (same
+ *                  stride: in place), else disjoint from every input
+ *   query, key, value  device, rows of [num_q_heads | num_kv_heads][head_size],
+ *                  their token strides (in elements) at least a row's length
+ *                  and multiples of 8: slices of one projection's output will do
+ *   kv_cache, slot_mapping  as for pa_reshape_and_cache. A token with a
+ *                  negative slot writes no K or V; its query is still rotated.
+ *   positions      device, [num_axes][position_stride] int32 (position_stride
+ *                  >= num_tokens; not read when num_axes is 1), any value
+ *   plan           device, [rot_dim / 2] words of pa_rope_plan. An axis that
+ *                  is not below num_axes reads as num_axes - 1.
+ *   rot_dim        a multiple of 16, <= head_size and <= 512: the leading
+ *                  dimensions that turn; the rest of a head passes unchanged
+ *   adjacent       0: pair i is dimensions (i, i + rot_dim / 2); else (2i, 2i + 1)
+ *   head_size      a multiple of 8, <= 1024
+ * Result: (x1, x2) becomes (x1 cos a - x2 sin a, x1 sin a + x2 cos a) in fp32,
+ * rounded once to dtype (values that pass are bit copies); a is reduced exactly
+ * (to 2^-31 turns) at any 32-bit position. Two tokens with the same slot race. Launched
+ * with programmatic dependent launch: it waits for the preceding kernel before
+ * it reads anything. Returns PA_OK or a PA_ERR_* code.
+ */
+int pa_rope_and_cache(void *query_out, const void *query, const void *key, const void *value,
+                      void *kv_cache, const int32_t *slot_mapping, const int32_t *positions,
+                      int num_axes, int64_t position_stride, const uint64_t *plan, int rot_dim,
+                      int adjacent, int num_tokens, int64_t query_out_stride, int64_t query_stride,
+                      int64_t key_stride, int64_t value_stride, int num_q_heads,
+                      int num_kv_heads, int head_size, int num_blocks, int block_size, int dtype,
+                      pa_stream_t stream);
+
+/*
+ * pa_rope_and_cache_fp8 — pa_rope_and_cache into an FP8 pool. A rotated key
+ * element goes from fp32 straight to the E4M3 value nearest to its quotient
+ * by k_scale (no rounding to dtype in between); the rest as in
+ * pa_reshape_and_cache_fp8. k_scale and v_scale finite and > 0.
+ */
+int pa_rope_and_cache_fp8(void *query_out, const void *query, const void *key, const void *value,
+                          void *kv_cache, const int32_t *slot_mapping, const int32_t *positions,
+                          int num_axes, int64_t position_stride, const uint64_t *plan, int rot_dim,
+                          int adjacent, int num_tokens, int64_t query_out_stride,
+                          int64_t query_stride, int64_t key_stride, int64_t value_stride,
+                          int num_q_heads, int num_kv_heads, int head_size, int num_blocks,
+                          int block_size, int dtype, float k_scale, float v_scale,
+                          pa_stream_t stream);
+
+/*
+ * pa_cross_attention — attention of each sequence's query tokens to all of
+ * another sequence of cached states (an encoder's: speech frames, image
+ * patches), of its own length and written to the pool by pa_reshape_and_cache.
+ * Query i of sequence s sees tokens 0 .. kv_lens[s] - 1, whatever i is; one
+ * query per sequence is the decode step, several may be a prompt's tokens or a
+ * request's candidates (beams). kv_lens[s] = 0 gives zero rows.
+ *
+ *   out, query, kv_cache, block_tables, max_blocks_per_seq, cu_seqlens_q,
+ *   num_seqs, total_q, max_seqlen_q, scale, num_q_heads, num_kv_heads,
+ *   head_size, num_blocks, block_size, dtype: as for pa_prefill. Rows of query
+ *   and out behind cu_seqlens_q[num_seqs] are not read for a result and not
+ *   written. Several sequences may use the same blocks.
+ *   kv_lens        device, [num_seqs] int32, in [0, max_blocks_per_seq *
+ *                  block_size], longer or shorter than the queries
+ *   workspace      device, NULL or >= pa_cross_attention_workspace_size(...)
+ *                  bytes, 256-byte aligned, under pa_prefill's rules. NULL:
+ *                  the K/V ranges stay whole (same result up to fp32 rounding).
+ *   flags          0 or PA_DECODE_SHARED_BLOCKS (tables share blocks)
+ * Bad offsets, lengths and block ids are handled as pa_prefill handles them
+ * (PA_DEVERR_SEQ_LEN, rows not written; PA_DEVERR_BLOCK_ID, read as zeros).
+ * fp32 scores, softmax and accumulation, P rounded once to dtype, one rounding
+ * at the end. Deterministic for a given device, shape and workspace choice.
+ * Allocates nothing. Returns PA_OK or a PA_ERR_* code.
+ */
+int pa_cross_attention(void *out, const void *query, const void *kv_cache,
+                       const int32_t *block_tables, int max_blocks_per_seq,
+                       const int32_t *cu_seqlens_q, const int32_t *kv_lens, int num_seqs,
+                       int total_q, int max_seqlen_q, float scale,
+                       int num_q_heads, int num_kv_heads, int head_size,
+                       int num_blocks, int block_size, int dtype,
+                       void *workspace, size_t workspace_bytes, unsigned flags,
+                       pa_stream_t stream);
+
+/* pa_cross_attention over an FP8 pool, with pa_prefill_fp8's conventions. */
+int pa_cross_attention_fp8(void *out, const void *query, const void *kv_cache,
+                           const int32_t *block_tables, int max_blocks_per_seq,
+                           const int32_t *cu_seqlens_q, const int32_t *kv_lens, int num_seqs,
+                           int total_q, int max_seqlen_q, float scale,
+                           int num_q_heads, int num_kv_heads, int head_size,
+                           int num_blocks, int block_size, int dtype,
+                           float k_scale, float v_scale,
+                           void *workspace, size_t workspace_bytes, unsigned flags,
+                           pa_stream_t stream);
+
+/*
+ * pa_cross_attention_workspace_size — bytes of workspace with which the cross
+ * attention calls split this shape's K/V ranges on the current device; 0 when
+ * they would not. cache_dtype: dtype, or PA_FP8_E4M3 for
+ * pa_cross_attention_fp8. Writes *bytes.
+ */
+int pa_cross_attention_workspace_size(int num_seqs, int max_seqlen_q, int num_q_heads,
+                                      int num_kv_heads, int head_size, int block_size,
+                                      int dtype, int cache_dtype, size_t *bytes);
+
+/*
  * pa_get_device_error — read and clear the current device's error word
  * (PA_DEVERR_* bits, 0 if none). Synchronises the device first, so every
  * earlier launch has finished. Returns PA_OK or PA_ERR_CUDA.

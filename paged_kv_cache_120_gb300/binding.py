@@ -37,7 +37,7 @@ PA_DEVERR_TIMEOUT = 16
 
 # (name, restype, argtypes) of every exported function, in header order.
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
-_u = ctypes.c_uint
+_u, _i64 = ctypes.c_uint, ctypes.c_int64
 _i32p = ctypes.POINTER(ctypes.c_int32)
 _ip = ctypes.POINTER(ctypes.c_int)
 SIGNATURES = [
@@ -56,6 +56,17 @@ SIGNATURES = [
     ("pa_prefill_workspace_size", _i, [_i, _i, _i, _i, _i, ctypes.POINTER(_sz)]),
     ("pa_prefill_fp8", _i, [_vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _f, _i, _i, _i, _i, _i, _i, _f, _f,
                             _vp, _sz, _vp]),
+    ("pa_build_step", _i, [_vp, _i, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _i, _i, _vp]),
+    ("pa_rope_plan", _i, [_vp, _vp, _i, _vp]),
+    ("pa_rope_and_cache", _i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i64, _vp, _i, _i, _i, _i64, _i64, _i64, _i64,
+                               _i, _i, _i, _i, _i, _i, _vp]),
+    ("pa_rope_and_cache_fp8", _i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i64, _vp, _i, _i, _i, _i64, _i64, _i64,
+                                   _i64, _i, _i, _i, _i, _i, _i, _f, _f, _vp]),
+    ("pa_cross_attention", _i, [_vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _f, _i, _i, _i, _i, _i, _i,
+                                _vp, _sz, _u, _vp]),
+    ("pa_cross_attention_fp8", _i, [_vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _f, _i, _i, _i, _i, _i, _i, _f, _f,
+                                    _vp, _sz, _u, _vp]),
+    ("pa_cross_attention_workspace_size", _i, [_i, _i, _i, _i, _i, _i, _i, _i, ctypes.POINTER(_sz)]),
     ("pa_copy_blocks", _i, [ctypes.POINTER(_vp), _i, _vp, _i, _i, _i, _i, _i, _i, _vp]),
     ("pa_get_device_error", _i, [_ip]),
     ("pa_alloc_create", _vp, [_i, _i, _i32p]),
@@ -341,6 +352,174 @@ def pa_prefill_fp8(out, query, kv_cache, block_tables, cu_seqlens_q, seq_lens, s
         _dev(cu_seqlens_q, "cu_seqlens_q"), _dev(seq_lens, "seq_lens"), int(seq_lens.shape[0]),
         total_q, int(max_seqlen_q), float(scale), hq, hkv, d, nb, bs, _dtype_code(query),
         float(k_scale), float(v_scale), ws, ws_bytes, _stream(stream)))
+
+
+def _bad(message):
+    raise PAError(PA_ERR_INVALID_ARG, message)
+
+
+def _on(device, **tensors):
+    """The tensors' device is the current one: libpa launches on the current device."""
+    import torch
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        _bad(f"tensors on {device}, but the current device is cuda:{torch.cuda.current_device()}")
+    for name, t in tensors.items():
+        if t.device != device:
+            _bad(f"{name} is on {t.device}, not {device}")
+
+
+def _i32(t, name, n):
+    """Address of a contiguous int32 CUDA tensor of n entries."""
+    import torch
+    if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous():
+        _bad(f"{name} must be a contiguous int32 tensor of {n} entries, not {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def pa_build_step(block_tables, seq_lens, query_lens, free_list, num_free, seq_lens_out, num_free_out,
+                  cu_seqlens_q, positions, slot_mapping, num_admitted, block_size, stream=None) -> None:
+    """int32 CUDA tensors: block_tables [S, maxblk] (extended in place), seq_lens / query_lens / seq_lens_out
+    [S], free_list [num_blocks] (a stack, in place), num_free / num_free_out / num_admitted [1], cu_seqlens_q
+    [S + 1], slot_mapping [capacity] and positions [capacity] or None. seq_lens_out and num_free_out may be
+    seq_lens and num_free. query_lens: new tokens; 0 idle; negative: finished, its blocks are returned."""
+    s, width = block_tables.shape
+    cap = slot_mapping.numel()
+    _on(block_tables.device, seq_lens=seq_lens, query_lens=query_lens, free_list=free_list, num_free=num_free,
+        seq_lens_out=seq_lens_out, num_free_out=num_free_out, cu_seqlens_q=cu_seqlens_q, slot_mapping=slot_mapping,
+        num_admitted=num_admitted, **({} if positions is None else {"positions": positions}))
+    _check(lib().pa_build_step(
+        _i32(block_tables, "block_tables", s * width), width, _i32(seq_lens, "seq_lens", s),
+        _i32(query_lens, "query_lens", s), s, _i32(free_list, "free_list", free_list.numel()),
+        _i32(num_free, "num_free", 1), _i32(seq_lens_out, "seq_lens_out", s), _i32(num_free_out, "num_free_out", 1),
+        _i32(cu_seqlens_q, "cu_seqlens_q", s + 1), None if positions is None else _i32(positions, "positions", cap),
+        _i32(slot_mapping, "slot_mapping", cap), cap, _i32(num_admitted, "num_admitted", 1), free_list.numel(),
+        int(block_size), _stream(stream)))
+
+
+def pa_rope_plan(inv_freq, pair_axes=None) -> np.ndarray:
+    """The plan words (int64 array, [num_pairs]) of the pairs' radians per position, and their axes (None: axis 0)."""
+    f = np.ascontiguousarray(inv_freq, dtype=np.float64).reshape(-1)
+    plan = np.empty(f.size, dtype=np.int64)
+    axes = None
+    if pair_axes is not None:
+        axes = np.ascontiguousarray(pair_axes, dtype=np.int32).reshape(-1)
+        if axes.size != f.size:
+            _bad(f"pair_axes has {axes.size} entries for {f.size} pairs")
+    _check(lib().pa_rope_plan(f.ctypes.data, None if axes is None else axes.ctypes.data, f.size, plan.ctypes.data))
+    return plan
+
+
+def rope_plan(inv_freq, pair_axes=None, device="cuda"):
+    """pa_rope_plan's words as an int64 tensor on the device, made once per model."""
+    import torch
+    return torch.from_numpy(pa_rope_plan(inv_freq, pair_axes)).to(device)
+
+
+def _rows(t, name, tokens, heads, d, dtype):
+    """(address, token stride) of [T, heads, D] rows whose heads lie side by side; T may be strided."""
+    if t.dtype != dtype or tuple(t.shape) != (tokens, heads, d) or t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+        _bad(f"{name} must be {dtype} of shape ({tokens}, {heads}, {d}) with dense heads, "
+             f"not {t.dtype} {tuple(t.shape)} strides {t.stride()}")
+    return t.data_ptr(), t.stride(0) if tokens > 1 else heads * d
+
+
+def _rope_args(query_out, query, key, value, kv_cache, slot_mapping, positions, plan, adjacent):
+    import torch
+    tokens, hq, d = query.shape
+    _, nb, bs, hkv, dc = kv_cache.shape
+    dt = query.dtype
+    _on(query.device, query_out=query_out, key=key, value=value, kv_cache=kv_cache, slot_mapping=slot_mapping,
+        positions=positions, plan=plan)
+    if dc != d:
+        _bad(f"kv_cache holds heads of {dc}, the queries {d}")
+    if positions.dtype != torch.int32 or positions.dim() not in (1, 2) or positions.shape[-1] != tokens or \
+            positions.stride(-1) != 1:
+        _bad(f"positions must be int32 [T] or [axes, T], not {positions.dtype} {tuple(positions.shape)}")
+    if plan.dtype != torch.int64 or not plan.is_contiguous():
+        _bad("plan must be a contiguous int64 tensor (see rope_plan)")
+    axes = positions.shape[0] if positions.dim() == 2 else 1
+    qo, qos = _rows(query_out, "query_out", tokens, hq, d, dt)
+    q, qs = _rows(query, "query", tokens, hq, d, dt)
+    k, ks = _rows(key, "key", tokens, hkv, d, dt)
+    v, vs = _rows(value, "value", tokens, hkv, d, dt)
+    return (qo, q, k, v, _dev(kv_cache, "kv_cache"), _i32(slot_mapping, "slot_mapping", tokens), positions.data_ptr(), axes,
+            positions.stride(0) if positions.dim() == 2 else tokens, plan.data_ptr(), 2 * plan.numel(), 1 if adjacent else 0,
+            tokens, qos, qs, ks, vs, hq, hkv, d, nb, bs)
+
+
+def pa_rope_and_cache(query_out, query, key, value, kv_cache, slot_mapping, positions, plan, adjacent=False,
+                      stream=None) -> None:
+    """query_out/query [T, Hq, D], key/value [T, Hkv, D] (any token stride), kv_cache (2, NB, B, Hkv, D), slot_mapping
+    [T] int32, positions [T] or [axes, T] int32, plan of the rot_dim / 2 pairs (see rope_plan)."""
+    if kv_cache.dtype != query.dtype:
+        _bad(f"kv_cache is {kv_cache.dtype}, the queries {query.dtype}")
+    _check(lib().pa_rope_and_cache(
+        *_rope_args(query_out, query, key, value, kv_cache, slot_mapping, positions, plan, adjacent),
+        _dtype_code(query), _stream(stream)))
+
+
+def pa_rope_and_cache_fp8(query_out, query, key, value, kv_cache, slot_mapping, positions, plan, k_scale, v_scale,
+                          adjacent=False, stream=None) -> None:
+    """pa_rope_and_cache into a pool of E4M3 codes (uint8 or float8_e4m3fn)."""
+    _fp8_pool(kv_cache, "kv_cache")
+    _check(lib().pa_rope_and_cache_fp8(
+        *_rope_args(query_out, query, key, value, kv_cache, slot_mapping, positions, plan, adjacent),
+        _dtype_code(query), float(k_scale), float(v_scale), _stream(stream)))
+
+
+def pa_cross_attention_workspace_size(num_seqs, max_seqlen_q, num_q_heads, num_kv_heads, head_size, block_size, dtype,
+                                      cache_dtype) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().pa_cross_attention_workspace_size(int(num_seqs), int(max_seqlen_q), num_q_heads, num_kv_heads, head_size,
+                                                   block_size, dtype, cache_dtype, ctypes.byref(out)))
+    return out.value
+
+
+def cross_attention_workspace(query, kv_cache, num_seqs, max_seqlen_q):
+    """A uint8 workspace tensor with which the cross attention calls split the K/V ranges of this shape, or None
+    when they would not."""
+    import torch
+    _, hq, d = query.shape
+    _, _, bs, hkv, _ = kv_cache.shape
+    n = pa_cross_attention_workspace_size(num_seqs, max_seqlen_q, hq, hkv, d, bs, _dtype_code(query), _pool_code(kv_cache))
+    return torch.empty(n, dtype=torch.uint8, device=query.device) if n else None
+
+
+def _cross_args(out, query, kv_cache, block_tables, cu_seqlens_q, kv_lens, scale, max_seqlen_q, workspace):
+    total_q, hq, d = query.shape
+    _, nb, bs, hkv, dc = kv_cache.shape
+    s = kv_lens.numel()
+    _on(query.device, out=out, kv_cache=kv_cache, block_tables=block_tables, cu_seqlens_q=cu_seqlens_q, kv_lens=kv_lens,
+        **({} if workspace is None else {"workspace": workspace}))
+    if dc != d or out.shape != query.shape or out.dtype != query.dtype:
+        _bad(f"out {tuple(out.shape)} {out.dtype}, kv_cache heads of {dc}: want the query's {tuple(query.shape)} {query.dtype}")
+    if block_tables.dim() != 2 or block_tables.shape[0] != s:
+        _bad(f"block_tables {tuple(block_tables.shape)} for {s} sequences")
+    ws, ws_bytes = _workspace_args(workspace)
+    args = (_dev(out, "out"), _dev(query, "query"), _dev(kv_cache, "kv_cache"),
+            _i32(block_tables, "block_tables", block_tables.numel()), block_tables.shape[1],
+            _i32(cu_seqlens_q, "cu_seqlens_q", s + 1), _i32(kv_lens, "kv_lens", s), s, total_q, int(max_seqlen_q),
+            float(scale), hq, hkv, d, nb, bs, _dtype_code(query))
+    return args, (ws, ws_bytes)
+
+
+def pa_cross_attention(out, query, kv_cache, block_tables, cu_seqlens_q, kv_lens, scale, max_seqlen_q, workspace=None,
+                       flags=0, stream=None) -> None:
+    """out/query [total_q, Hq, D]; kv_cache (2, NB, B, Hkv, D) of the encoder's states; block_tables [S, maxblk] int32;
+    cu_seqlens_q [S + 1] int32; kv_lens [S] int32 (cached states); max_seqlen_q: host int; workspace: None (no K/V split)
+    or a uint8 CUDA tensor (see cross_attention_workspace); flags: 0 or PA_DECODE_SHARED_BLOCKS."""
+    if kv_cache.dtype != query.dtype:
+        _bad(f"kv_cache is {kv_cache.dtype}, the queries {query.dtype}")
+    args, ws = _cross_args(out, query, kv_cache, block_tables, cu_seqlens_q, kv_lens, scale, max_seqlen_q, workspace)
+    _check(lib().pa_cross_attention(*args, *ws, int(flags), _stream(stream)))
+
+
+def pa_cross_attention_fp8(out, query, kv_cache, block_tables, cu_seqlens_q, kv_lens, scale, max_seqlen_q, k_scale, v_scale,
+                           workspace=None, flags=0, stream=None) -> None:
+    """pa_cross_attention over a pool of E4M3 codes (uint8 or float8_e4m3fn)."""
+    _fp8_pool(kv_cache, "kv_cache")
+    args, ws = _cross_args(out, query, kv_cache, block_tables, cu_seqlens_q, kv_lens, scale, max_seqlen_q, workspace)
+    _check(lib().pa_cross_attention_fp8(*args, float(k_scale), float(v_scale), *ws, int(flags), _stream(stream)))
 
 
 def pa_copy_blocks(kv_caches, src_dst_pairs, stream=None) -> None:

@@ -29,6 +29,8 @@ UNITS = [
     ("pa_kernels.cu", "nvcc"),
     ("pa_prefill.cu", "nvcc"),
     ("pa_static_scratch.cu", "nvcc"),
+    ("pa_step.cu", "nvcc"),
+    ("pa_rope.cu", "nvcc"),
     ("block_allocator.cpp", "g++"),
     ("prefix_cache.cpp", "g++"),
     ("pa_errors.cpp", "g++"),

@@ -12,4 +12,8 @@ int set_error(int code, const char *fmt, ...);
 // on the current device. Returns a cudaError_t value (0 on success).
 int prefill_take_device_error(int *bits);
 
+// The same for pa_build_step and for the rotary write.
+int step_take_device_error(int *bits);
+int rope_take_device_error(int *bits);
+
 }  // namespace pa

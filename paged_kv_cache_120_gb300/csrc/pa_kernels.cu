@@ -1764,6 +1764,14 @@ extern "C" int pa_get_device_error(int *bits)
     e = static_cast<cudaError_t>(prefill_take_device_error(&w));
     if (e != cudaSuccess)
         return cuda_fail(e, "pa_get_device_error: prefill word");
+    v |= w;
+    e = static_cast<cudaError_t>(step_take_device_error(&w));
+    if (e != cudaSuccess)
+        return cuda_fail(e, "pa_get_device_error: step word");
+    v |= w;
+    e = static_cast<cudaError_t>(rope_take_device_error(&w));
+    if (e != cudaSuccess)
+        return cuda_fail(e, "pa_get_device_error: rotary word");
     *bits = v | w;
     return PA_OK;
 }

@@ -408,6 +408,7 @@ struct PrefillParams {
                         //  first query head}
     float scale_log2;   // scale * log2(e) (* k_scale with an FP8 cache)
     float v_scale;      // 1, or the FP8 cache's V scale
+    int cross;          // 1: every query sees all L cached tokens (cross attention); 0: causally
 };
 
 // One work unit: the two adjacent query tiles A = 2 qp and B = 2 qp + 1 of
@@ -436,7 +437,8 @@ struct Item {
 // A sequence's offsets and length are consistent.
 __device__ __forceinline__ bool seq_ok(const PrefillParams &p, int q0, int q_len, int L)
 {
-    return !(q_len < 0 || q_len > p.max_q || q0 < 0 || q0 + q_len > p.total_q || L < q_len || L > p.max_len);
+    return !(q_len < 0 || q_len > p.max_q || q0 < 0 || q0 > p.total_q - q_len || L < (p.cross ? 0 : q_len) ||
+             L > p.max_len);
 }
 
 // K/V tiles the unit of query pair qr of a sequence reads (those its tile
@@ -447,7 +449,7 @@ __device__ __forceinline__ int pair_tiles(const PrefillParams &p, int q_len, int
     const int ta = 2 * (p.q_pairs - 1 - qr) * p.rows_per_head;
     if (ta >= q_len)
         return 0;
-    return (L - q_len + min(q_len, ta + 2 * p.rows_per_head) + kN - 1) / kN;
+    return ((p.cross ? L : L - q_len + min(q_len, ta + 2 * p.rows_per_head)) + kN - 1) / kN;
 }
 
 // SK: the stream-K numbering (sequence-major).
@@ -478,7 +480,7 @@ __device__ __forceinline__ bool unit_of(const PrefillParams &p, int u, Unit &w, 
     }
     const int T = p.rows_per_head;
     const int ta = 2 * (p.q_pairs - 1 - qr) * T;
-    if (ta >= q_len)
+    if (ta >= q_len || L == 0)  // L == 0: cross attention to nothing, zero rows (written by zero_rows)
         return false;
     w.s = s;
     w.h = h;
@@ -489,9 +491,26 @@ __device__ __forceinline__ bool unit_of(const PrefillParams &p, int u, Unit &w, 
     for (int x = 0; x < 2; ++x) {
         w.t0[x] = ta + x * T;
         const int t_end = min(q_len, w.t0[x] + T);
-        w.n[x] = w.t0[x] < q_len ? (L - q_len + t_end + kN - 1) / kN : 0;  // tiles its last query sees
+        w.n[x] = w.t0[x] < q_len ? ((p.cross ? L : L - q_len + t_end) + kN - 1) / kN : 0;  // tiles its last query sees
     }
     return true;
+}
+
+// Cross attention to a sequence without cached tokens gives zero rows: they
+// have no work unit, so the CTAs' softmax threads (tid < 256) write them,
+// sequence by sequence, before they wait for their first unit.
+template <int D>
+__device__ __forceinline__ void zero_rows(const PrefillParams &p, int tid)
+{
+    for (int s = blockIdx.x; s < p.num_seqs; s += gridDim.x) {
+        const int q0 = p.cu_q[s], q_len = p.cu_q[s + 1] - q0, L = p.seq_lens[s];
+        if (L != 0 || !seq_ok(p, q0, q_len, L))
+            continue;
+        const long long row = (long long)p.num_q_heads * (D / 8);
+        uint4 *out = static_cast<uint4 *>(p.out) + q0 * row;
+        for (long long i = tid; i < q_len * row; i += 256)
+            out[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
 }
 
 struct PrefillBars {
@@ -1066,6 +1085,8 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
         const int r = quarter * 32 + lane;  // this thread's TMEM lane (row)
         const int g = r / T, t = r - g * T;
         const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+        if (p.cross)
+            zero_rows<D>(p, tid);
         float sc = p.scale_log2;  // this row's score factor (base 2)
         const bool sc_pos = sc >= 0.f;
         int gx = 0, vbase = 0;  // tiles of this query tile, and V tiles of the CTA, so far
@@ -1085,7 +1106,8 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
             const int jp = (w.L % kN) ? w.L / kN : -1;
             const bool zeroes = !FP8 && jp >= j0 && jp < nx && (x == 0 || jp >= (SPLIT ? min(w.n[0], j1) : w.n[0]));
             const bool valid = g < HPC && w.t0[x] + t < w.q_len;
-            const int pos = valid ? w.L - w.q_len + w.t0[x] + t : -1;  // last token this row sees
+            // Last token this row sees (cross: rows without a query run on, unread).
+            const int pos = p.cross ? w.L - 1 : valid ? w.L - w.q_len + w.t0[x] + t : -1;
             if constexpr (kQToF16) {
                 // Move Q row r of this tile to fp16 in place, scaled by 2^-e
                 // so that the row's largest magnitude lies in [2^14, 2^15):
@@ -1705,7 +1727,7 @@ int prefill_impl(const char *who, void *out, const void *query, const void *kv_c
                  int max_blocks_per_seq, const int32_t *cu_seqlens_q, const int32_t *seq_lens, int num_seqs,
                  int total_q, int max_seqlen_q, float scale, int num_q_heads, int num_kv_heads, int head_size,
                  int num_blocks, int block_size, int dtype, bool fp8, float k_scale, float v_scale,
-                 void *workspace, size_t workspace_bytes, pa_stream_t stream)
+                 void *workspace, size_t workspace_bytes, bool cross, pa_stream_t stream)
 {
     if (dtype != PA_F16 && dtype != PA_BF16)
         return set_error(PA_ERR_UNSUPPORTED, "%s: dtype %d (want PA_F16 or PA_BF16)", who, dtype);
@@ -1766,6 +1788,7 @@ int prefill_impl(const char *who, void *out, const void *query, const void *kv_c
     prm.max_len = max_blocks_per_seq * block_size;
     prm.scale_log2 = scale * 1.4426950408889634f * (fp8 ? k_scale : 1.f);
     prm.v_scale = fp8 ? v_scale : 1.f;
+    prm.cross = cross ? 1 : 0;
     prm.num_kv_heads = num_kv_heads;
     prm.num_units = (int)lp.units;
     prm.part_o = split ? static_cast<float *>(workspace) : nullptr;
@@ -1852,6 +1875,20 @@ int prefill_impl(const char *who, void *out, const void *query, const void *kv_c
     return PA_OK;
 }
 
+// Cross attention's sizes and arguments are checked and launched as prefill's.
+int cross_impl(const char *who, void *out, const void *query, const void *kv_cache, const int32_t *block_tables,
+               int max_blocks_per_seq, const int32_t *cu_seqlens_q, const int32_t *kv_lens, int num_seqs, int total_q,
+               int max_seqlen_q, float scale, int num_q_heads, int num_kv_heads, int head_size, int num_blocks,
+               int block_size, int dtype, bool fp8, float k_scale, float v_scale, void *workspace,
+               size_t workspace_bytes, unsigned flags, pa_stream_t stream)
+{
+    if (flags & ~PA_DECODE_SHARED_BLOCKS)
+        return set_error(PA_ERR_INVALID_ARG, "%s: unknown flags 0x%x", who, flags);
+    return prefill_impl(who, out, query, kv_cache, block_tables, max_blocks_per_seq, cu_seqlens_q, kv_lens, num_seqs,
+                        total_q, max_seqlen_q, scale, num_q_heads, num_kv_heads, head_size, num_blocks, block_size, dtype,
+                        fp8, k_scale, v_scale, workspace, workspace_bytes, true, stream);
+}
+
 }  // namespace
 
 extern "C" int pa_prefill(void *out, const void *query, const void *kv_cache, const int32_t *block_tables,
@@ -1862,7 +1899,7 @@ extern "C" int pa_prefill(void *out, const void *query, const void *kv_cache, co
 {
     return prefill_impl("pa_prefill", out, query, kv_cache, block_tables, max_blocks_per_seq, cu_seqlens_q,
                         seq_lens, num_seqs, total_q, max_seqlen_q, scale, num_q_heads, num_kv_heads, head_size,
-                        num_blocks, block_size, dtype, false, 1.f, 1.f, workspace, workspace_bytes, stream);
+                        num_blocks, block_size, dtype, false, 1.f, 1.f, workspace, workspace_bytes, false, stream);
 }
 
 extern "C" int pa_prefill_fp8(void *out, const void *query, const void *kv_cache, const int32_t *block_tables,
@@ -1876,7 +1913,7 @@ extern "C" int pa_prefill_fp8(void *out, const void *query, const void *kv_cache
         return set_error(PA_ERR_INVALID_ARG, "pa_prefill_fp8: k_scale and v_scale must be finite and > 0");
     return prefill_impl("pa_prefill_fp8", out, query, kv_cache, block_tables, max_blocks_per_seq, cu_seqlens_q,
                         seq_lens, num_seqs, total_q, max_seqlen_q, scale, num_q_heads, num_kv_heads, head_size,
-                        num_blocks, block_size, dtype, true, k_scale, v_scale, workspace, workspace_bytes, stream);
+                        num_blocks, block_size, dtype, true, k_scale, v_scale, workspace, workspace_bytes, false, stream);
 }
 
 extern "C" int pa_prefill_workspace_size(int num_seqs, int max_seqlen_q, int num_q_heads, int num_kv_heads,
@@ -1899,4 +1936,45 @@ extern "C" int pa_prefill_workspace_size(int num_seqs, int max_seqlen_q, int num
         return rc;
     *bytes = plan_launch(num_seqs, max_seqlen_q, num_q_heads, num_kv_heads, head_size, sms).split_bytes;
     return PA_OK;
+}
+
+extern "C" int pa_cross_attention(void *out, const void *query, const void *kv_cache, const int32_t *block_tables,
+                                  int max_blocks_per_seq, const int32_t *cu_seqlens_q, const int32_t *kv_lens,
+                                  int num_seqs, int total_q, int max_seqlen_q, float scale, int num_q_heads,
+                                  int num_kv_heads, int head_size, int num_blocks, int block_size, int dtype,
+                                  void *workspace, size_t workspace_bytes, unsigned flags, pa_stream_t stream)
+{
+    return cross_impl("pa_cross_attention", out, query, kv_cache, block_tables, max_blocks_per_seq, cu_seqlens_q, kv_lens,
+                      num_seqs, total_q, max_seqlen_q, scale, num_q_heads, num_kv_heads, head_size, num_blocks, block_size,
+                      dtype, false, 1.f, 1.f, workspace, workspace_bytes, flags, stream);
+}
+
+extern "C" int pa_cross_attention_fp8(void *out, const void *query, const void *kv_cache, const int32_t *block_tables,
+                                      int max_blocks_per_seq, const int32_t *cu_seqlens_q, const int32_t *kv_lens,
+                                      int num_seqs, int total_q, int max_seqlen_q, float scale, int num_q_heads,
+                                      int num_kv_heads, int head_size, int num_blocks, int block_size, int dtype,
+                                      float k_scale, float v_scale, void *workspace, size_t workspace_bytes,
+                                      unsigned flags, pa_stream_t stream)
+{
+    if (!(std::isfinite(k_scale) && k_scale > 0.f && std::isfinite(v_scale) && v_scale > 0.f))
+        return set_error(PA_ERR_INVALID_ARG, "pa_cross_attention_fp8: k_scale and v_scale must be finite and > 0");
+    return cross_impl("pa_cross_attention_fp8", out, query, kv_cache, block_tables, max_blocks_per_seq, cu_seqlens_q,
+                      kv_lens, num_seqs, total_q, max_seqlen_q, scale, num_q_heads, num_kv_heads, head_size, num_blocks,
+                      block_size, dtype, true, k_scale, v_scale, workspace, workspace_bytes, flags, stream);
+}
+
+extern "C" int pa_cross_attention_workspace_size(int num_seqs, int max_seqlen_q, int num_q_heads, int num_kv_heads,
+                                                 int head_size, int block_size, int dtype, int cache_dtype, size_t *bytes)
+{
+    const char *who = "pa_cross_attention_workspace_size";
+    if (!bytes)
+        return set_error(PA_ERR_INVALID_ARG, "%s: null bytes", who);
+    *bytes = 0;
+    if (dtype != PA_F16 && dtype != PA_BF16)
+        return set_error(PA_ERR_UNSUPPORTED, "%s: dtype %d (want PA_F16 or PA_BF16)", who, dtype);
+    if (cache_dtype != dtype && cache_dtype != PA_FP8_E4M3)
+        return set_error(PA_ERR_UNSUPPORTED, "%s: cache_dtype %d (want dtype or PA_FP8_E4M3)", who, cache_dtype);
+    if (block_size < kBoxTokens || block_size % kBoxTokens != 0)
+        return set_error(PA_ERR_INVALID_ARG, "%s: block_size %d must be a positive multiple of 16", who, block_size);
+    return pa_prefill_workspace_size(num_seqs, max_seqlen_q, num_q_heads, num_kv_heads, head_size, bytes);
 }
