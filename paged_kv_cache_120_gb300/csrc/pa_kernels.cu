@@ -238,6 +238,14 @@ struct DecodeParams {
     int kv_stream;        // 1: stream K/V with the L2 evict-first hint (no block shared)
     int lens_early;       // 1: seq_lens may be read before the preceding kernel has finished
     int total_warps;      // grid * warps per CTA
+    // Ragged queries (cross attention of a few rows): sequence s holds the
+    // queries cu_q[s] .. cu_q[s + 1] - 1, and a tile's columns are its (query,
+    // head) pairs, tile_heads heads of every query side by side; tile_q is
+    // then tile_heads * max_q.
+    const int32_t *cu_q;
+    int tile_heads;
+    int max_q;
+    int total_q;
 };
 
 template <int D, int NT>
@@ -246,7 +254,7 @@ constexpr int record_floats()
     return NT * 8 * (D + 2);  // m[GP], l[GP], O[GP][D]; only live query columns are written
 }
 
-template <int D, int WARPS, bool FP8>
+template <int D, int WARPS, bool FP8, bool RAGGED>
 inline size_t decode_smem_bytes(int num_seqs)
 {
     constexpr int kStages = decode_stages<FP8>();
@@ -255,6 +263,8 @@ inline size_t decode_smem_bytes(int num_seqs)
     b += (size_t)WARPS * kStages * sizeof(uint64_t);
     b += (size_t)(num_seqs + 1) * sizeof(long long);
     b += (size_t)num_seqs * sizeof(int);
+    if (RAGGED)
+        b += (size_t)num_seqs * sizeof(int2) + sizeof(int);
     return b;
 }
 
@@ -310,9 +320,9 @@ __device__ __forceinline__ int owner_of(long long u, long long N, long long K)
 }
 
 // Main decode kernel. Template: head size D, N-tiles of 8 query heads NT,
-// element type of Q and the output, FP8 cache or not. One CTA =
-// decode_warps<NT>() independent warp pipelines.
-template <int D, int NT, bool BF16, bool FP8>
+// element type of Q and the output, FP8 cache or not, one query per sequence
+// or a ragged few. One CTA = decode_warps<NT>() independent warp pipelines.
+template <int D, int NT, bool BF16, bool FP8, bool RAGGED>
 __global__ void __launch_bounds__(decode_warps<NT, FP8>() * 32)
     paged_decode_kernel(const __grid_constant__ CUtensorMap kv_map, const DecodeParams p)
 {
@@ -343,6 +353,8 @@ __global__ void __launch_bounds__(decode_warps<NT, FP8>() * 32)
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + kWarps * kStages * STAGE);
     long long *prefix = reinterpret_cast<long long *>(bars + kWarps * kStages);
     int *lens = reinterpret_cast<int *>(prefix + p.num_seqs + 1);
+    // Ragged: {first query, queries} of each sequence (none if inconsistent).
+    int2 *rows = reinterpret_cast<int2 *>(prefix + p.num_seqs + 1 + (p.num_seqs + 1) / 2);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int S = p.num_seqs;
@@ -362,6 +374,16 @@ __global__ void __launch_bounds__(decode_warps<NT, FP8>() * 32)
         long long local = 0;
         for (int s = s0; s < s1; ++s) {
             int L = p.seq_lens[s];
+            if constexpr (RAGGED) {
+                const int q0 = p.cu_q[s];
+                const long long n = (long long)p.cu_q[s + 1] - q0;
+                const bool ok = n >= 0 && n <= p.max_q && q0 >= 0 && q0 <= p.total_q - n && L >= 0 && L <= max_len;
+                if (!ok)
+                    raise_error(PA_DEVERR_SEQ_LEN);
+                rows[s] = ok ? make_int2(q0, (int)n) : make_int2(0, 0);
+                if (!ok || n == 0)
+                    L = 0;  // no rows to compute
+            }
             if (L < 0 || L > max_len) {
                 raise_error(PA_DEVERR_SEQ_LEN);
                 L = L < 0 ? 0 : max_len;
@@ -411,9 +433,13 @@ __global__ void __launch_bounds__(decode_warps<NT, FP8>() * 32)
             p.prefix_ws[s] = prefix[s];
     // Empty sequences get zero output rows (no warp streams them).
     for (int s = blockIdx.x; s < S; s += gridDim.x)
-        if (lens[s] == 0)
-            for (int i = tid; i < p.num_q_heads * D; i += blockDim.x)
-                static_cast<uint16_t *>(p.out)[(long long)s * p.num_q_heads * D + i] = 0;
+        if (lens[s] == 0) {
+            const long long row = (long long)p.num_q_heads * D;
+            uint16_t *out = static_cast<uint16_t *>(p.out) + (RAGGED ? rows[s].x : s) * row;
+            const long long n = RAGGED ? rows[s].y * row : row;
+            for (long long i = tid; i < n; i += blockDim.x)
+                out[i] = 0;
+        }
 
     // 2. This warp's contiguous share of the unit sequence.
     const int gw = blockIdx.x * kWarps + warp;
@@ -521,15 +547,28 @@ __global__ void __launch_bounds__(decode_warps<NT, FP8>() * 32)
         hq0 = h * p.group + qt * 16;
     };
 
+    // Column col of a segment: its row, in rows of D elements behind the
+    // segment's first (query 0, head hq0); false if it is none of s's.
+    auto column = [&](int s, int col, long long &row) {
+        if constexpr (RAGGED) {
+            const int q = col / p.tile_heads;
+            row = (long long)q * p.num_q_heads + (col - q * p.tile_heads);
+            return q < rows[s].y;
+        } else {
+            row = col;
+            return col < p.tile_q;
+        }
+    };
+
     auto begin_segment = [&](int seg) {
         int s, segl, hq0;
         seg_coords(seg, s, segl, hq0);
-        const uint16_t *qbase = p.query + ((long long)s * p.num_q_heads + hq0) * D;
+        const uint16_t *qbase = p.query + ((long long)(RAGGED ? rows[s].x : s) * p.num_q_heads + hq0) * D;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int col = nt * 8 + g;
-            const bool live = col < p.tile_q;
-            const uint32_t *qrow = reinterpret_cast<const uint32_t *>(qbase + (long long)col * D);
+            long long qr;
+            const bool live = column(s, nt * 8 + g, qr);
+            const uint32_t *qrow = reinterpret_cast<const uint32_t *>(qbase + qr * D);
             if constexpr (FP8) {
                 // Permuted k-step kk = 4j + w: dims 16c + 4w + {0..3} of chunk
                 // c = CPT tig + j, the same dims the K fragments hold.
@@ -613,14 +652,15 @@ __global__ void __launch_bounds__(decode_warps<NT, FP8>() * 32)
         const long long seg_end = seg_start + ntiles;
         if (seg_start >= r0 && seg_end <= r1) {
             // Whole segment in this warp's share: normalise and store.
-            uint16_t *out = static_cast<uint16_t *>(p.out) + ((long long)s * p.num_q_heads + hq0) * D;
+            uint16_t *out =
+                static_cast<uint16_t *>(p.out) + ((long long)(RAGGED ? rows[s].x : s) * p.num_q_heads + hq0) * D;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int col = nt * 8 + 2 * tig + e;
-                    if (col < p.tile_q) {
-                        uint16_t *row = out + (long long)col * D;
+                    long long qr;
+                    if (column(s, nt * 8 + 2 * tig + e, qr)) {
+                        uint16_t *row = out + qr * D;
                         if constexpr (FP8) {
                             // Rows g / g+8 of m-tile mt are dims VB g + 2mt / + 1.
                             const float inv = p.v_scale / lsum[nt][e];
@@ -1009,7 +1049,7 @@ constexpr size_t reduce_smem_bytes()
 // task with many pieces by the whole CTA, pieces split across the warps and
 // the warps' states combined in shared memory. Every merge runs in a fixed
 // order, so results do not depend on timing.
-template <int D, int NT, bool BF16>
+template <int D, int NT, bool BF16, bool RAGGED>
 __global__ void __launch_bounds__(kReduceWarps * 32) paged_decode_reduce_kernel(const DecodeParams p)
 {
     constexpr int GP = NT * 8, KD = D / 32, PART = 2 * GP + GP * D;
@@ -1022,19 +1062,35 @@ __global__ void __launch_bounds__(kReduceWarps * 32) paged_decode_reduce_kernel(
     const int tq = p.tile_q;
     const int segs_per_seq = p.num_kv_heads * p.qtiles;
     uint16_t *out_base = static_cast<uint16_t *>(p.out);
+    // Column c's output row of a segment, or null if it is none of the
+    // sequence's (a task exists only for a consistent sequence with queries).
+    struct OutRows {
+        uint16_t *first;
+        int n;  // ragged: queries
+    };
     auto out_rows = [&](int seg) {
         const int s = seg / segs_per_seq, segl = seg - (seg / segs_per_seq) * segs_per_seq;
         const int h = segl / p.qtiles, qt = segl - (segl / p.qtiles) * p.qtiles;
-        return out_base + ((long long)s * p.num_q_heads + h * p.group + qt * 16) * D;
+        const int q0 = RAGGED ? p.cu_q[s] : s;
+        return OutRows{out_base + ((long long)q0 * p.num_q_heads + h * p.group + qt * 16) * D,
+                       RAGGED ? p.cu_q[s + 1] - q0 : 1};
     };
-    auto store = [&](uint16_t *out, const MergeState<D, NT> &st) {
+    auto out_row = [&](const OutRows &o, int c) -> uint16_t * {
+        if constexpr (RAGGED) {
+            const int q = c / p.tile_heads;
+            return q < o.n ? o.first + ((long long)q * p.num_q_heads + (c - q * p.tile_heads)) * D : nullptr;
+        } else {
+            return c < tq ? o.first + (long long)c * D : nullptr;
+        }
+    };
+    auto store = [&](const OutRows &o, const MergeState<D, NT> &st) {
 #pragma unroll
         for (int c = 0; c < GP; ++c)
-            if (c < tq) {
+            if (uint16_t *out = out_row(o, c)) {
                 const float inv = 1.f / st.l[c];
 #pragma unroll
                 for (int k = 0; k < KD; ++k)
-                    out[(long long)c * D + lane + 32 * k] = to_elem<BF16>(st.acc[c][k] * inv);
+                    out[lane + 32 * k] = to_elem<BF16>(st.acc[c][k] * inv);
             }
     };
 
@@ -1071,9 +1127,12 @@ __global__ void __launch_bounds__(kReduceWarps * 32) paged_decode_reduce_kernel(
         }
         __syncthreads();
         // Combine the warps' states (fixed order), elements across the CTA.
-        uint16_t *out = out_rows(t.x);
+        const OutRows o = out_rows(t.x);
         for (int e = threadIdx.x; e < tq * D; e += kReduceWarps * 32) {
             const int c = e / D, d = e - (e / D) * D;
+            uint16_t *out = out_row(o, c);
+            if (!out)
+                continue;
             float Mx = -INFINITY;
             for (int v = 0; v < kReduceWarps; ++v)
                 Mx = fmaxf(Mx, s_part[v * PART + c]);
@@ -1084,7 +1143,7 @@ __global__ void __launch_bounds__(kReduceWarps * 32) paged_decode_reduce_kernel(
                 lt += f * pv[GP + c];
                 ot += f * pv[2 * GP + c * D + d];
             }
-            out[(long long)c * D + d] = to_elem<BF16>(ot / lt);
+            out[d] = to_elem<BF16>(ot / lt);
         }
         __syncthreads();
     }
@@ -1346,6 +1405,7 @@ cudaError_t launch_pdl(const void *fn, dim3 grid, dim3 block, void **args, size_
 struct DecodePlan {
     int nt = 1;       // 8-query N-tiles
     int tile_q = 1;
+    int tile_heads = 1;
     int qtiles = 1;
     int grid = 0;     // CTAs
     int warps = 0;    // warps per CTA
@@ -1360,23 +1420,33 @@ struct DecodePlan {
     size_t total() const { return prefix_bytes + task_bytes + warp_record_bytes; }
 };
 
-template <int D, int NT, bool BF16, bool FP8>
+template <int D, int NT, bool BF16, bool FP8, bool RAGGED>
 void pick_kernels(DecodePlan &pl, int num_seqs)
 {
-    pl.main_fn = reinterpret_cast<const void *>(&paged_decode_kernel<D, NT, BF16, FP8>);
+    pl.main_fn = reinterpret_cast<const void *>(&paged_decode_kernel<D, NT, BF16, FP8, RAGGED>);
     pl.warps = decode_warps<NT, FP8>();
-    pl.reduce_fn = reinterpret_cast<const void *>(&paged_decode_reduce_kernel<D, NT, BF16>);
+    pl.reduce_fn = reinterpret_cast<const void *>(&paged_decode_reduce_kernel<D, NT, BF16, RAGGED>);
     pl.reduce_smem = reduce_smem_bytes<D, NT>();
-    pl.smem = decode_smem_bytes<D, decode_warps<NT, FP8>(), FP8>(num_seqs);
+    pl.smem = decode_smem_bytes<D, decode_warps<NT, FP8>(), FP8, RAGGED>(num_seqs);
 }
 
-template <int D, int NT>
+template <int D, int NT, bool RAGGED>
 void pick_kernels(DecodePlan &pl, int num_seqs, bool bf, bool fp8)
 {
     if (fp8)
-        bf ? pick_kernels<D, NT, true, true>(pl, num_seqs) : pick_kernels<D, NT, false, true>(pl, num_seqs);
+        bf ? pick_kernels<D, NT, true, true, RAGGED>(pl, num_seqs) : pick_kernels<D, NT, false, true, RAGGED>(pl, num_seqs);
     else
-        bf ? pick_kernels<D, NT, true, false>(pl, num_seqs) : pick_kernels<D, NT, false, false>(pl, num_seqs);
+        bf ? pick_kernels<D, NT, true, false, RAGGED>(pl, num_seqs)
+           : pick_kernels<D, NT, false, false, RAGGED>(pl, num_seqs);
+}
+
+template <bool RAGGED>
+void pick_kernels(DecodePlan &pl, int head_size, int num_seqs, bool bf, bool fp8)
+{
+    if (head_size == 64)
+        pl.nt == 1 ? pick_kernels<64, 1, RAGGED>(pl, num_seqs, bf, fp8) : pick_kernels<64, 2, RAGGED>(pl, num_seqs, bf, fp8);
+    else
+        pl.nt == 1 ? pick_kernels<128, 1, RAGGED>(pl, num_seqs, bf, fp8) : pick_kernels<128, 2, RAGGED>(pl, num_seqs, bf, fp8);
 }
 
 int validate_decode_shape(int num_seqs, int num_q_heads, int num_kv_heads, int head_size,
@@ -1445,18 +1515,18 @@ cudaError_t kernel_setup(const void *fn, int dev, size_t smem, int threads, int 
     return cudaSuccess;
 }
 
+// max_q: 0 for one query per sequence (pa_decode), else the most queries of a
+// ragged sequence.
 int make_plan(DecodePlan &pl, int num_seqs, int num_q_heads, int num_kv_heads, int head_size,
-              int dtype, bool fp8)
+              int dtype, bool fp8, int max_q = 0)
 {
     const int group = num_q_heads / num_kv_heads;
-    pl.tile_q = group <= 16 ? group : 16;
+    pl.tile_heads = group <= 16 ? group : 16;
+    pl.tile_q = pl.tile_heads * (max_q > 0 ? max_q : 1);
     pl.qtiles = group <= 16 ? 1 : group / 16;
     pl.nt = pl.tile_q <= 8 ? 1 : 2;
     const bool bf = dtype == PA_BF16;
-    if (head_size == 64)
-        pl.nt == 1 ? pick_kernels<64, 1>(pl, num_seqs, bf, fp8) : pick_kernels<64, 2>(pl, num_seqs, bf, fp8);
-    else
-        pl.nt == 1 ? pick_kernels<128, 1>(pl, num_seqs, bf, fp8) : pick_kernels<128, 2>(pl, num_seqs, bf, fp8);
+    max_q > 0 ? pick_kernels<true>(pl, head_size, num_seqs, bf, fp8) : pick_kernels<false>(pl, head_size, num_seqs, bf, fp8);
     int dev = 0, sms = 0, occ = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
@@ -1504,34 +1574,16 @@ int workspace_size_impl(const char *fn, int num_seqs, int num_q_heads, int num_k
     return PA_OK;
 }
 
-int decode_impl(const char *fn, void *out, const void *query, const void *kv_cache,
-                const int32_t *block_tables, int max_blocks_per_seq, const int32_t *seq_lens,
-                int num_seqs, float scale, int num_q_heads, int num_kv_heads, int head_size,
-                int num_blocks, int block_size, int dtype, bool fp8, float k_scale, float v_scale,
-                void *workspace, size_t workspace_bytes, unsigned flags, pa_stream_t stream)
+// Plan and launch a checked call: the stream kernel and the merge. cu_q null:
+// one query per sequence; else ragged, at most max_q of total_q in all.
+int launch_decode(const char *fn, void *out, const void *query, const void *kv_cache, const int32_t *block_tables,
+                  int max_blocks_per_seq, const int32_t *seq_lens, int num_seqs, float scale, int num_q_heads,
+                  int num_kv_heads, int head_size, int num_blocks, int block_size, int dtype, bool fp8, float k_scale,
+                  float v_scale, void *workspace, size_t workspace_bytes, unsigned flags, const int32_t *cu_q, int max_q,
+                  int total_q, pa_stream_t stream)
 {
-    int rc = validate_decode_shape(num_seqs, num_q_heads, num_kv_heads, head_size, block_size, dtype);
-    if (rc != PA_OK)
-        return rc;
-    if (fp8 && !(std::isfinite(k_scale) && k_scale > 0.f && std::isfinite(v_scale) && v_scale > 0.f))
-        return set_error(PA_ERR_INVALID_ARG, "%s: k_scale and v_scale must be finite and > 0", fn);
-    if (num_seqs == 0)
-        return PA_OK;
-    if (!out || !query || !kv_cache || !block_tables || !seq_lens || !workspace)
-        return set_error(PA_ERR_INVALID_ARG, "%s: null pointer argument", fn);
-    if (num_blocks <= 0 || max_blocks_per_seq <= 0)
-        return set_error(PA_ERR_INVALID_ARG, "%s: num_blocks and max_blocks_per_seq must be > 0", fn);
-    if ((long long)max_blocks_per_seq * block_size > (1LL << 30))
-        return set_error(PA_ERR_INVALID_ARG, "%s: max_blocks_per_seq * block_size too large", fn);
-    if (!std::isfinite(scale))
-        return set_error(PA_ERR_INVALID_ARG, "%s: scale is not finite", fn);
-    if (flags & ~(PA_DECODE_SHARED_BLOCKS | PA_DECODE_LENS_READY))
-        return set_error(PA_ERR_INVALID_ARG, "%s: unknown flags 0x%x", fn, flags);
-    if (!aligned(kv_cache, 16) || !aligned(query, 16) || !aligned(out, 16) ||
-        !aligned(workspace, 256) || !aligned(block_tables, 4) || !aligned(seq_lens, 4))
-        return set_error(PA_ERR_INVALID_ARG, "%s: misaligned pointer (pool/query/out 16 B, workspace 256 B)", fn);
     DecodePlan pl;
-    rc = make_plan(pl, num_seqs, num_q_heads, num_kv_heads, head_size, dtype, fp8);
+    int rc = make_plan(pl, num_seqs, num_q_heads, num_kv_heads, head_size, dtype, fp8, cu_q ? max_q : 0);
     if (rc != PA_OK)
         return rc;
     if (workspace_bytes < pl.total())
@@ -1568,6 +1620,10 @@ int decode_impl(const char *fn, void *out, const void *query, const void *kv_cac
     prm.kv_stream = (flags & PA_DECODE_SHARED_BLOCKS) ? 0 : 1;
     prm.lens_early = (flags & PA_DECODE_LENS_READY) ? 1 : 0;
     prm.total_warps = pl.total_warps;
+    prm.cu_q = cu_q;
+    prm.tile_heads = pl.tile_heads;
+    prm.max_q = max_q;
+    prm.total_q = total_q;
 
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     void *args[] = {&map, &prm};
@@ -1580,6 +1636,37 @@ int decode_impl(const char *fn, void *out, const void *query, const void *kv_cac
     if (e != cudaSuccess)
         return set_error(PA_ERR_CUDA, "%s: reduce kernel launch: %s", fn, cudaGetErrorString(e));
     return PA_OK;
+}
+
+int decode_impl(const char *fn, void *out, const void *query, const void *kv_cache,
+                const int32_t *block_tables, int max_blocks_per_seq, const int32_t *seq_lens,
+                int num_seqs, float scale, int num_q_heads, int num_kv_heads, int head_size,
+                int num_blocks, int block_size, int dtype, bool fp8, float k_scale, float v_scale,
+                void *workspace, size_t workspace_bytes, unsigned flags, pa_stream_t stream)
+{
+    int rc = validate_decode_shape(num_seqs, num_q_heads, num_kv_heads, head_size, block_size, dtype);
+    if (rc != PA_OK)
+        return rc;
+    if (fp8 && !(std::isfinite(k_scale) && k_scale > 0.f && std::isfinite(v_scale) && v_scale > 0.f))
+        return set_error(PA_ERR_INVALID_ARG, "%s: k_scale and v_scale must be finite and > 0", fn);
+    if (num_seqs == 0)
+        return PA_OK;
+    if (!out || !query || !kv_cache || !block_tables || !seq_lens || !workspace)
+        return set_error(PA_ERR_INVALID_ARG, "%s: null pointer argument", fn);
+    if (num_blocks <= 0 || max_blocks_per_seq <= 0)
+        return set_error(PA_ERR_INVALID_ARG, "%s: num_blocks and max_blocks_per_seq must be > 0", fn);
+    if ((long long)max_blocks_per_seq * block_size > (1LL << 30))
+        return set_error(PA_ERR_INVALID_ARG, "%s: max_blocks_per_seq * block_size too large", fn);
+    if (!std::isfinite(scale))
+        return set_error(PA_ERR_INVALID_ARG, "%s: scale is not finite", fn);
+    if (flags & ~(PA_DECODE_SHARED_BLOCKS | PA_DECODE_LENS_READY))
+        return set_error(PA_ERR_INVALID_ARG, "%s: unknown flags 0x%x", fn, flags);
+    if (!aligned(kv_cache, 16) || !aligned(query, 16) || !aligned(out, 16) ||
+        !aligned(workspace, 256) || !aligned(block_tables, 4) || !aligned(seq_lens, 4))
+        return set_error(PA_ERR_INVALID_ARG, "%s: misaligned pointer (pool/query/out 16 B, workspace 256 B)", fn);
+    return launch_decode(fn, out, query, kv_cache, block_tables, max_blocks_per_seq, seq_lens, num_seqs, scale, num_q_heads,
+                         num_kv_heads, head_size, num_blocks, block_size, dtype, fp8, k_scale, v_scale, workspace,
+                         workspace_bytes, flags, nullptr, 0, 0, stream);
 }
 
 // Checks shared by both write paths; *row_vecs = 8-element groups per row.
@@ -1607,6 +1694,38 @@ int validate_reshape(const char *fn, const void *key, const void *value, const v
 }
 
 }  // namespace
+
+namespace pa {
+
+bool cross_rows_fit(int num_seqs, int max_seqlen_q, int num_q_heads, int num_kv_heads, int block_size)
+{
+    const int group = num_q_heads / num_kv_heads;
+    return num_seqs <= kMaxSeqs && block_size <= 2048 * kTile && num_kv_heads <= 65535 &&
+           (group <= 16 ? (long long)max_seqlen_q * group <= 16 : max_seqlen_q == 1);
+}
+
+int cross_rows_workspace(int num_seqs, int max_seqlen_q, int num_q_heads, int num_kv_heads, int head_size, int dtype, bool fp8,
+                         size_t *bytes)
+{
+    DecodePlan pl;
+    int rc = make_plan(pl, num_seqs, num_q_heads, num_kv_heads, head_size, dtype, fp8, max_seqlen_q);
+    if (rc == PA_OK)
+        *bytes = pl.total();
+    return rc;
+}
+
+int cross_rows(const char *who, void *out, const void *query, const void *kv_cache, const int32_t *block_tables,
+               int max_blocks_per_seq, const int32_t *cu_seqlens_q, const int32_t *kv_lens, int num_seqs, int total_q,
+               int max_seqlen_q, float scale, int num_q_heads, int num_kv_heads, int head_size, int num_blocks,
+               int block_size, int dtype, bool fp8, float k_scale, float v_scale, void *workspace, size_t workspace_bytes,
+               unsigned flags, pa_stream_t stream)
+{
+    return launch_decode(who, out, query, kv_cache, block_tables, max_blocks_per_seq, kv_lens, num_seqs, scale, num_q_heads,
+                         num_kv_heads, head_size, num_blocks, block_size, dtype, fp8, k_scale, v_scale, workspace,
+                         workspace_bytes, flags, cu_seqlens_q, max_seqlen_q, total_q, stream);
+}
+
+}  // namespace pa
 
 extern "C" int pa_decode_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads,
                                         int head_size, int block_size, int dtype, size_t *bytes)

@@ -1723,18 +1723,18 @@ int check_heads(const char *who, int num_q_heads, int num_kv_heads, int head_siz
     return PA_OK;
 }
 
-int prefill_impl(const char *who, void *out, const void *query, const void *kv_cache, const int32_t *block_tables,
-                 int max_blocks_per_seq, const int32_t *cu_seqlens_q, const int32_t *seq_lens, int num_seqs,
-                 int total_q, int max_seqlen_q, float scale, int num_q_heads, int num_kv_heads, int head_size,
-                 int num_blocks, int block_size, int dtype, bool fp8, float k_scale, float v_scale,
-                 void *workspace, size_t workspace_bytes, bool cross, pa_stream_t stream)
+// Checks shared by the causal and the cross calls; *empty: nothing to do.
+int check_call(const char *who, const void *out, const void *query, const void *kv_cache, const int32_t *block_tables,
+               int max_blocks_per_seq, const int32_t *cu_seqlens_q, const int32_t *seq_lens, int num_seqs, int total_q,
+               int max_seqlen_q, float scale, int num_q_heads, int num_kv_heads, int head_size, int num_blocks,
+               int block_size, int dtype, bool *empty)
 {
+    *empty = false;
     if (dtype != PA_F16 && dtype != PA_BF16)
         return set_error(PA_ERR_UNSUPPORTED, "%s: dtype %d (want PA_F16 or PA_BF16)", who, dtype);
     int rc = check_heads(who, num_q_heads, num_kv_heads, head_size);
     if (rc != PA_OK)
         return rc;
-    const int group = num_q_heads / num_kv_heads;
     if (block_size < kBoxTokens || block_size % kBoxTokens != 0)
         return set_error(PA_ERR_INVALID_ARG, "%s: block_size %d must be a positive multiple of 16", who,
                          block_size);
@@ -1744,7 +1744,8 @@ int prefill_impl(const char *who, void *out, const void *query, const void *kv_c
         return set_error(PA_ERR_INVALID_ARG, "%s: max_blocks_per_seq * block_size too large", who);
     if (!std::isfinite(scale))
         return set_error(PA_ERR_INVALID_ARG, "%s: scale is not finite", who);
-    if (num_seqs == 0 || total_q == 0 || max_seqlen_q == 0)
+    *empty = num_seqs == 0 || total_q == 0 || max_seqlen_q == 0;
+    if (*empty)
         return PA_OK;
     if (!out || !query || !kv_cache || !block_tables || !cu_seqlens_q || !seq_lens)
         return set_error(PA_ERR_INVALID_ARG, "%s: null pointer argument", who);
@@ -1752,6 +1753,21 @@ int prefill_impl(const char *who, void *out, const void *query, const void *kv_c
         (reinterpret_cast<uintptr_t>(block_tables) & 3) || (reinterpret_cast<uintptr_t>(cu_seqlens_q) & 3) ||
         (reinterpret_cast<uintptr_t>(seq_lens) & 3))
         return set_error(PA_ERR_INVALID_ARG, "%s: misaligned pointer (query/out/pool 16 B)", who);
+    return PA_OK;
+}
+
+int prefill_impl(const char *who, void *out, const void *query, const void *kv_cache, const int32_t *block_tables,
+                 int max_blocks_per_seq, const int32_t *cu_seqlens_q, const int32_t *seq_lens, int num_seqs,
+                 int total_q, int max_seqlen_q, float scale, int num_q_heads, int num_kv_heads, int head_size,
+                 int num_blocks, int block_size, int dtype, bool fp8, float k_scale, float v_scale,
+                 void *workspace, size_t workspace_bytes, bool cross, pa_stream_t stream)
+{
+    bool empty = false;
+    int rc = check_call(who, out, query, kv_cache, block_tables, max_blocks_per_seq, cu_seqlens_q, seq_lens, num_seqs, total_q,
+                        max_seqlen_q, scale, num_q_heads, num_kv_heads, head_size, num_blocks, block_size, dtype, &empty);
+    if (rc != PA_OK || empty)
+        return rc;
+    const int group = num_q_heads / num_kv_heads;
     if (!encoder())
         return set_error(PA_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
 
@@ -1875,7 +1891,11 @@ int prefill_impl(const char *who, void *out, const void *query, const void *kv_c
     return PA_OK;
 }
 
-// Cross attention's sizes and arguments are checked and launched as prefill's.
+// Cross attention: with a workspace, a few rows per kv head (the decode step
+// of one query or a few candidates per sequence) are bound by reading K and V
+// and take the decode kernels' ragged form, whose warps stream them; more rows
+// take the prefill kernel without its causal limit. Arguments are checked
+// alike either way.
 int cross_impl(const char *who, void *out, const void *query, const void *kv_cache, const int32_t *block_tables,
                int max_blocks_per_seq, const int32_t *cu_seqlens_q, const int32_t *kv_lens, int num_seqs, int total_q,
                int max_seqlen_q, float scale, int num_q_heads, int num_kv_heads, int head_size, int num_blocks,
@@ -1884,6 +1904,19 @@ int cross_impl(const char *who, void *out, const void *query, const void *kv_cac
 {
     if (flags & ~PA_DECODE_SHARED_BLOCKS)
         return set_error(PA_ERR_INVALID_ARG, "%s: unknown flags 0x%x", who, flags);
+    bool empty = false;
+    const int rc = check_call(who, out, query, kv_cache, block_tables, max_blocks_per_seq, cu_seqlens_q, kv_lens, num_seqs,
+                              total_q, max_seqlen_q, scale, num_q_heads, num_kv_heads, head_size, num_blocks, block_size,
+                              dtype, &empty);
+    if (rc != PA_OK || empty)
+        return rc;
+    if (workspace && cross_rows_fit(num_seqs, max_seqlen_q, num_q_heads, num_kv_heads, block_size)) {
+        if (reinterpret_cast<uintptr_t>(workspace) & 255)
+            return set_error(PA_ERR_WORKSPACE, "%s: workspace at %p (256-byte aligned)", who, workspace);
+        return cross_rows(who, out, query, kv_cache, block_tables, max_blocks_per_seq, cu_seqlens_q, kv_lens, num_seqs,
+                          total_q, max_seqlen_q, scale, num_q_heads, num_kv_heads, head_size, num_blocks, block_size, dtype,
+                          fp8, k_scale, v_scale, workspace, workspace_bytes, flags, stream);
+    }
     return prefill_impl(who, out, query, kv_cache, block_tables, max_blocks_per_seq, cu_seqlens_q, kv_lens, num_seqs,
                         total_q, max_seqlen_q, scale, num_q_heads, num_kv_heads, head_size, num_blocks, block_size, dtype,
                         fp8, k_scale, v_scale, workspace, workspace_bytes, true, stream);
@@ -1976,5 +2009,11 @@ extern "C" int pa_cross_attention_workspace_size(int num_seqs, int max_seqlen_q,
         return set_error(PA_ERR_UNSUPPORTED, "%s: cache_dtype %d (want dtype or PA_FP8_E4M3)", who, cache_dtype);
     if (block_size < kBoxTokens || block_size % kBoxTokens != 0)
         return set_error(PA_ERR_INVALID_ARG, "%s: block_size %d must be a positive multiple of 16", who, block_size);
+    const int rc = check_heads(who, num_q_heads, num_kv_heads, head_size);
+    if (rc != PA_OK)
+        return rc;
+    if (num_seqs > 0 && max_seqlen_q > 0 && cross_rows_fit(num_seqs, max_seqlen_q, num_q_heads, num_kv_heads, block_size))
+        return cross_rows_workspace(num_seqs, max_seqlen_q, num_q_heads, num_kv_heads, head_size, dtype,
+                                    cache_dtype == PA_FP8_E4M3, bytes);
     return pa_prefill_workspace_size(num_seqs, max_seqlen_q, num_q_heads, num_kv_heads, head_size, bytes);
 }
