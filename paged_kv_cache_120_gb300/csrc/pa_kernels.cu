@@ -162,6 +162,9 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 #ifndef PA_DECODE_STAGES
 #define PA_DECODE_STAGES 1
 #endif
+#ifndef PA_ROWS_WARPS_64
+#define PA_ROWS_WARPS_64 16
+#endif
 #ifndef PA_DECODE_WARPS_WIDE
 #define PA_DECODE_WARPS_WIDE 8
 #endif
@@ -170,13 +173,17 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 #endif
 
 // Warps per CTA, each an independent pipeline: 12 for 8-column query tiles;
-// 16-column tiles need ~195 registers per thread, so 8 warps fit an SM.
+// 16-column tiles need ~195 registers per thread, so 8 warps fit an SM. The
+// ragged form at head size 64 (at most 128 registers) takes 16 (measured at
+// 64 x 1500 states of 20 heads: 12 / 16 / 20 warps 92.7 / 87.2 / 88.2 us).
 #ifndef PA_DECODE_WARPS_FP8
 #define PA_DECODE_WARPS_FP8 12
 #endif
-template <int NT, bool FP8 = false>
+template <int D, int NT, bool FP8, bool RAGGED>
 constexpr int decode_warps()
 {
+    if (RAGGED && D == 64)
+        return PA_ROWS_WARPS_64;
     return NT == 1 ? (FP8 ? PA_DECODE_WARPS_FP8 : PA_DECODE_WARPS) : PA_DECODE_WARPS_WIDE;
 }
 // TMA ring depth per warp. An FP8 tile is half the bytes of a 16-bit one, so
@@ -323,11 +330,11 @@ __device__ __forceinline__ int owner_of(long long u, long long N, long long K)
 // element type of Q and the output, FP8 cache or not, one query per sequence
 // or a ragged few. One CTA = decode_warps<NT>() independent warp pipelines.
 template <int D, int NT, bool BF16, bool FP8, bool RAGGED>
-__global__ void __launch_bounds__(decode_warps<NT, FP8>() * 32)
+__global__ void __launch_bounds__(decode_warps<D, NT, FP8, RAGGED>() * 32)
     paged_decode_kernel(const __grid_constant__ CUtensorMap kv_map, const DecodeParams p)
 {
     using Geo = TileGeo<D, FP8>;
-    constexpr int kWarps = decode_warps<NT, FP8>();
+    constexpr int kWarps = decode_warps<D, NT, FP8, RAGGED>();
     constexpr int kStages = decode_stages<FP8>();
     constexpr int KS = D / 16;  // k-steps of QK^T and m-tiles of V^T P^T
     constexpr int GP = NT * 8;
@@ -1364,11 +1371,13 @@ int encode_kv_map(CUtensorMap *map, const void *kv, int num_blocks, int block_si
     cuuint32_t estr[5] = {1, 1, 1, 1, 1};
     const CUtensorMapSwizzle swz =
         (fp8 && head_size == 64) ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
-    // A 16-bit row of one head is 256 bytes (fetched as two 128-byte boxes):
-    // promote to 256-byte L2 lines. An FP8 row is at most 128 bytes, and a
-    // 256-byte promotion would also pull the next head's row from DRAM.
+    // A 16-bit row of one 128-wide head is 256 bytes (fetched as two 128-byte
+    // boxes): promote to 256-byte L2 lines. An FP8 row or one of a 64-wide
+    // head is at most 128 bytes, and a 256-byte promotion would also pull the
+    // next head's row from DRAM (measured at 20 heads of 64: 731 MB read for
+    // 492 MB of K and V).
     const CUtensorMapL2promotion promo =
-        fp8 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
+        head_size * e <= 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
     CUtensorMap m;
     CUresult r = enc(&m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 5,
                      const_cast<void *>(kv), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -1424,10 +1433,10 @@ template <int D, int NT, bool BF16, bool FP8, bool RAGGED>
 void pick_kernels(DecodePlan &pl, int num_seqs)
 {
     pl.main_fn = reinterpret_cast<const void *>(&paged_decode_kernel<D, NT, BF16, FP8, RAGGED>);
-    pl.warps = decode_warps<NT, FP8>();
+    pl.warps = decode_warps<D, NT, FP8, RAGGED>();
     pl.reduce_fn = reinterpret_cast<const void *>(&paged_decode_reduce_kernel<D, NT, BF16, RAGGED>);
     pl.reduce_smem = reduce_smem_bytes<D, NT>();
-    pl.smem = decode_smem_bytes<D, decode_warps<NT, FP8>(), FP8, RAGGED>(num_seqs);
+    pl.smem = decode_smem_bytes<D, decode_warps<D, NT, FP8, RAGGED>(), FP8, RAGGED>(num_seqs);
 }
 
 template <int D, int NT, bool RAGGED>
