@@ -130,8 +130,8 @@ def _check(rc: int) -> int:
 
 def _stream(stream):
     import torch
-    if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    if stream is None:  # the current stream of the current device, without building its Python object
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return ctypes.c_void_p(stream)
     return ctypes.c_void_p(stream.cuda_stream)
@@ -358,21 +358,37 @@ def _bad(message):
     raise PAError(PA_ERR_INVALID_ARG, message)
 
 
-def _on(device, **tensors):
-    """The tensors' device is the current one: libpa launches on the current device."""
+def _device(t, name):
+    """Index of a CUDA tensor's device, which is the current one: libpa launches there."""
     import torch
-    if device.type != "cuda" or device.index != torch.cuda.current_device():
-        _bad(f"tensors on {device}, but the current device is cuda:{torch.cuda.current_device()}")
-    for name, t in tensors.items():
-        if t.device != device:
-            _bad(f"{name} is on {t.device}, not {device}")
+    index = t.get_device()
+    if index < 0 or index != torch._C._cuda_getDevice():
+        _bad(f"{name} is on {t.device}, not on the current CUDA device")
+    return index
 
 
-def _i32(t, name, n):
-    """Address of a contiguous int32 CUDA tensor of n entries."""
-    import torch
-    if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous():
-        _bad(f"{name} must be a contiguous int32 tensor of {n} entries, not {t.dtype} {tuple(t.shape)}")
+def _ints(t, name, n, index, dtype):
+    """Address of a contiguous tensor of n entries of the type on device `index`."""
+    if t.dtype is not dtype or t.numel() != n or t.get_device() != index or not t.is_contiguous():
+        _bad(f"{name} must be a contiguous {dtype} tensor of {n} entries on cuda:{index}, "
+             f"not {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _rows(t, name, shape, index, dtype):
+    """(address, token stride) of [T, heads, D] rows whose heads lie side by side; T may be strided."""
+    tokens, heads, d = shape
+    st = t.stride()
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or st[2] != 1 or (heads > 1 and st[1] != d):
+        _bad(f"{name} must be {dtype} of shape {tuple(shape)} with dense heads on cuda:{index}, "
+             f"not {t.dtype} {tuple(t.shape)} strides {st} on {t.device}")
+    return t.data_ptr(), st[0] if tokens > 1 else heads * d
+
+
+def _pool(t, name, index):
+    """Address of a contiguous pool on device `index`."""
+    if t.get_device() != index or not t.is_contiguous():
+        _bad(f"{name} must be contiguous on cuda:{index}, not on {t.device}")
     return t.data_ptr()
 
 
@@ -382,17 +398,18 @@ def pa_build_step(block_tables, seq_lens, query_lens, free_list, num_free, seq_l
     [S], free_list [num_blocks] (a stack, in place), num_free / num_free_out / num_admitted [1], cu_seqlens_q
     [S + 1], slot_mapping [capacity] and positions [capacity] or None. seq_lens_out and num_free_out may be
     seq_lens and num_free. query_lens: new tokens; 0 idle; negative: finished, its blocks are returned."""
+    import torch
+    i32 = torch.int32
     s, width = block_tables.shape
-    cap = slot_mapping.numel()
-    _on(block_tables.device, seq_lens=seq_lens, query_lens=query_lens, free_list=free_list, num_free=num_free,
-        seq_lens_out=seq_lens_out, num_free_out=num_free_out, cu_seqlens_q=cu_seqlens_q, slot_mapping=slot_mapping,
-        num_admitted=num_admitted, **({} if positions is None else {"positions": positions}))
+    cap, blocks = slot_mapping.numel(), free_list.numel()
+    dev = _device(block_tables, "block_tables")
     _check(lib().pa_build_step(
-        _i32(block_tables, "block_tables", s * width), width, _i32(seq_lens, "seq_lens", s),
-        _i32(query_lens, "query_lens", s), s, _i32(free_list, "free_list", free_list.numel()),
-        _i32(num_free, "num_free", 1), _i32(seq_lens_out, "seq_lens_out", s), _i32(num_free_out, "num_free_out", 1),
-        _i32(cu_seqlens_q, "cu_seqlens_q", s + 1), None if positions is None else _i32(positions, "positions", cap),
-        _i32(slot_mapping, "slot_mapping", cap), cap, _i32(num_admitted, "num_admitted", 1), free_list.numel(),
+        _ints(block_tables, "block_tables", s * width, dev, i32), width, _ints(seq_lens, "seq_lens", s, dev, i32),
+        _ints(query_lens, "query_lens", s, dev, i32), s, _ints(free_list, "free_list", blocks, dev, i32),
+        _ints(num_free, "num_free", 1, dev, i32), _ints(seq_lens_out, "seq_lens_out", s, dev, i32),
+        _ints(num_free_out, "num_free_out", 1, dev, i32), _ints(cu_seqlens_q, "cu_seqlens_q", s + 1, dev, i32),
+        None if positions is None else _ints(positions, "positions", cap, dev, i32),
+        _ints(slot_mapping, "slot_mapping", cap, dev, i32), cap, _ints(num_admitted, "num_admitted", 1, dev, i32), blocks,
         int(block_size), _stream(stream)))
 
 
@@ -415,35 +432,28 @@ def rope_plan(inv_freq, pair_axes=None, device="cuda"):
     return torch.from_numpy(pa_rope_plan(inv_freq, pair_axes)).to(device)
 
 
-def _rows(t, name, tokens, heads, d, dtype):
-    """(address, token stride) of [T, heads, D] rows whose heads lie side by side; T may be strided."""
-    if t.dtype != dtype or tuple(t.shape) != (tokens, heads, d) or t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
-        _bad(f"{name} must be {dtype} of shape ({tokens}, {heads}, {d}) with dense heads, "
-             f"not {t.dtype} {tuple(t.shape)} strides {t.stride()}")
-    return t.data_ptr(), t.stride(0) if tokens > 1 else heads * d
-
-
 def _rope_args(query_out, query, key, value, kv_cache, slot_mapping, positions, plan, adjacent):
     import torch
-    tokens, hq, d = query.shape
+    shape, dt = query.shape, query.dtype
+    tokens, hq, d = shape
     _, nb, bs, hkv, dc = kv_cache.shape
-    dt = query.dtype
-    _on(query.device, query_out=query_out, key=key, value=value, kv_cache=kv_cache, slot_mapping=slot_mapping,
-        positions=positions, plan=plan)
+    dev = _device(query, "query")
     if dc != d:
         _bad(f"kv_cache holds heads of {dc}, the queries {d}")
-    if positions.dtype != torch.int32 or positions.dim() not in (1, 2) or positions.shape[-1] != tokens or \
-            positions.stride(-1) != 1:
-        _bad(f"positions must be int32 [T] or [axes, T], not {positions.dtype} {tuple(positions.shape)}")
-    if plan.dtype != torch.int64 or not plan.is_contiguous():
-        _bad("plan must be a contiguous int64 tensor (see rope_plan)")
-    axes = positions.shape[0] if positions.dim() == 2 else 1
-    qo, qos = _rows(query_out, "query_out", tokens, hq, d, dt)
-    q, qs = _rows(query, "query", tokens, hq, d, dt)
-    k, ks = _rows(key, "key", tokens, hkv, d, dt)
-    v, vs = _rows(value, "value", tokens, hkv, d, dt)
-    return (qo, q, k, v, _dev(kv_cache, "kv_cache"), _i32(slot_mapping, "slot_mapping", tokens), positions.data_ptr(), axes,
-            positions.stride(0) if positions.dim() == 2 else tokens, plan.data_ptr(), 2 * plan.numel(), 1 if adjacent else 0,
+    axes, stride = 1, tokens
+    ps = positions.shape
+    if len(ps) == 2:
+        axes, stride = ps[0], positions.stride(0)
+    if positions.dtype is not torch.int32 or ps[-1] != tokens or len(ps) > 2 or positions.get_device() != dev or \
+            (tokens > 1 and positions.stride(-1) != 1):
+        _bad(f"positions must be int32 [T] or [axes, T] on cuda:{dev}, not {positions.dtype} {tuple(ps)} on {positions.device}")
+    pairs = plan.numel()
+    qo, qos = _rows(query_out, "query_out", shape, dev, dt)
+    q, qs = _rows(query, "query", shape, dev, dt)
+    k, ks = _rows(key, "key", (tokens, hkv, d), dev, dt)
+    v, vs = _rows(value, "value", (tokens, hkv, d), dev, dt)
+    return (qo, q, k, v, _pool(kv_cache, "kv_cache", dev), _ints(slot_mapping, "slot_mapping", tokens, dev, torch.int32),
+            positions.data_ptr(), axes, stride, _ints(plan, "plan", pairs, dev, torch.int64), 2 * pairs, 1 if adjacent else 0,
             tokens, qos, qs, ks, vs, hq, hkv, d, nb, bs)
 
 
@@ -486,21 +496,21 @@ def cross_attention_workspace(query, kv_cache, num_seqs, max_seqlen_q):
 
 
 def _cross_args(out, query, kv_cache, block_tables, cu_seqlens_q, kv_lens, scale, max_seqlen_q, workspace):
+    import torch
+    i32 = torch.int32
     total_q, hq, d = query.shape
     _, nb, bs, hkv, dc = kv_cache.shape
-    s = kv_lens.numel()
-    _on(query.device, out=out, kv_cache=kv_cache, block_tables=block_tables, cu_seqlens_q=cu_seqlens_q, kv_lens=kv_lens,
-        **({} if workspace is None else {"workspace": workspace}))
-    if dc != d or out.shape != query.shape or out.dtype != query.dtype:
+    s, width = block_tables.shape
+    dev = _device(query, "query")
+    if dc != d or out.shape != query.shape or out.dtype is not query.dtype:
         _bad(f"out {tuple(out.shape)} {out.dtype}, kv_cache heads of {dc}: want the query's {tuple(query.shape)} {query.dtype}")
-    if block_tables.dim() != 2 or block_tables.shape[0] != s:
-        _bad(f"block_tables {tuple(block_tables.shape)} for {s} sequences")
-    ws, ws_bytes = _workspace_args(workspace)
-    args = (_dev(out, "out"), _dev(query, "query"), _dev(kv_cache, "kv_cache"),
-            _i32(block_tables, "block_tables", block_tables.numel()), block_tables.shape[1],
-            _i32(cu_seqlens_q, "cu_seqlens_q", s + 1), _i32(kv_lens, "kv_lens", s), s, total_q, int(max_seqlen_q),
-            float(scale), hq, hkv, d, nb, bs, _dtype_code(query))
-    return args, (ws, ws_bytes)
+    args = (_pool(out, "out", dev), _pool(query, "query", dev), _pool(kv_cache, "kv_cache", dev),
+            _ints(block_tables, "block_tables", s * width, dev, i32), width, _ints(cu_seqlens_q, "cu_seqlens_q", s + 1, dev, i32),
+            _ints(kv_lens, "kv_lens", s, dev, i32), s, total_q, int(max_seqlen_q), float(scale), hq, hkv, d, nb, bs,
+            _dtype_code(query))
+    if workspace is None:
+        return args, (None, 0)
+    return args, (_pool(workspace, "workspace", dev), workspace.numel() * workspace.element_size())
 
 
 def pa_cross_attention(out, query, kv_cache, block_tables, cu_seqlens_q, kv_lens, scale, max_seqlen_q, workspace=None,

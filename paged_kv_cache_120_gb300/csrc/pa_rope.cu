@@ -18,11 +18,17 @@
 // the angle in [-1, 1) half turns.
 //
 // HBM-bound: per token the q row is read and written, the k and v rows read
-// and written once; the sines are computed once per token, not per head.
+// and written once; the sines are computed once per unit, not per head.
+// Measured (GB300, of the 6.80 TB/s copy rate): 8192 tokens of 40/40 heads of
+// 128, 503 MB in 80 us (6.3 TB/s, 92 %); 16383 tokens of 32/8 heads, 396 MB in
+// 61 us (6.5 TB/s, 95 %); 5001 tokens of 32/8 heads into an FP8 cache, 113 MB
+// in 22 us (5.1 TB/s, 75 %: a fifth of it is the launch and the first loads).
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 #include <type_traits>
 
 #include "../../include/pa.h"
@@ -35,9 +41,17 @@ __device__ int g_rope_error;  // PA_DEVERR_* bits of the rotary kernels
 
 namespace {
 
-constexpr int kRopeThreads = 256;
-constexpr int kRopeMaxPairs = 256;  // rot <= 512
-constexpr int kRopeMaxAxes = 4;     // the axis is kept in a plan word's low 2 bits
+constexpr int kRopeWarps = 8;                         // that turn and store
+constexpr int kRopeThreads = 32 * (kRopeWarps + 2);   // and one that copies, one for the sines
+constexpr int kRopeMaxStages = 8;
+// A unit's rows at most (but a group of heads at least), and a CTA's ring, two
+// CTAs an SM: about 80 KB of rows in flight an SM. Both less and more is
+// slower: the units in flight are the stretch of memory that is read and
+// written at a time (measured at 16383 tokens of 32 + 2 x 8 heads, rings of
+// 24 / 36 / 40 / 57 / 96 KB: 108 / 71 / 61 / 69 / 73 us).
+constexpr int kRopeUnitBytes = 12288, kRopeSmemBytes = 40960;
+constexpr int kRopeMaxDims = 512;  // that turn
+constexpr int kRopeMaxAxes = 4;    // the axis is kept in a plan word's low 2 bits
 
 __device__ __forceinline__ void rope_raise(int bit) { atomicOr(&g_rope_error, bit); }
 
@@ -51,11 +65,44 @@ struct RopeParams {
     long long pos_stride;                                  // entries per axis
     long long num_slots;
     int num_tokens, num_q_heads, num_kv_heads, head_vecs, rot_vecs, num_axes;
-    float k_scale, v_scale;
+    long long units;  // num_tokens * units_per_token
+    int units_per_token, heads_per_unit;
+    int stages, stage_bytes, sines_at;  // a stage: the unit's rows, then cosines and sines of rot / 2 pairs
+    float k_scale, v_scale, k_inv, v_inv;  // inv: 1 / scale, 0 where quotients are to be divided
 };
 
+// Two fp32 lanes in a register pair: one packed instruction for both.
+__device__ __forceinline__ uint64_t pair(float lo, float hi)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+
+__device__ __forceinline__ float2 lanes(uint64_t x)
+{
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(x));
+    return f;
+}
+
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+// Eight elements as four fp32 pairs, and back.
 struct F8 {
-    float f[8];
+    uint64_t p[4];
 };
 
 template <bool BF16>
@@ -65,9 +112,9 @@ __device__ __forceinline__ F8 unpack8(const uint4 x)
     F8 r;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float2 f = unpack2<BF16>(w[i]);
-        r.f[2 * i] = f.x;
-        r.f[2 * i + 1] = f.y;
+        const float2 f = BF16 ? make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u))
+                              : unpack2<false>(w[i]);
+        r.p[i] = pair(f.x, f.y);
     }
     return r;
 }
@@ -75,128 +122,327 @@ __device__ __forceinline__ F8 unpack8(const uint4 x)
 template <bool BF16>
 __device__ __forceinline__ uint4 pack8(const F8 &x)
 {
-    return make_uint4(pack2<BF16>(x.f[0], x.f[1]), pack2<BF16>(x.f[2], x.f[3]), pack2<BF16>(x.f[4], x.f[5]),
-                      pack2<BF16>(x.f[6], x.f[7]));
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = lanes(x.p[i]);
+        w[i] = pack2<BF16>(f.x, f.y);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Eight values to E4M3 codes of value / scale (IEEE fp32 division, nearest
-// even, saturating), as pa_reshape_and_cache_fp8 rounds.
-__device__ __forceinline__ uint2 codes8(const F8 &x, float scale)
+__device__ __forceinline__ uint4 negated(const uint4 x)  // eight 16-bit elements
+{
+    return make_uint4(x.x ^ 0x80008000u, x.y ^ 0x80008000u, x.z ^ 0x80008000u, x.w ^ 0x80008000u);
+}
+
+// E4M3 codes (nearest even, saturating) of the IEEE fp32 quotients of eight
+// values by the scale, as pa_reshape_and_cache_fp8 rounds; nx holds the values
+// NEGATED. With inv = 1 / scale correctly rounded, Markstein's theorem
+// ("Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990) gives the correctly rounded quotient as
+// q - (q scale - x) inv, q = x inv, as long as the residual is exact. It is
+// for scale within 2^+-64 and |x / scale| >= 2^-12; smaller quotients have
+// code 0 of their sign whatever their last bits are (the residual of a zero is
+// taken with the sign that leaves -0 alone). q is held to 2^24 so that an
+// infinite x stays one instead of becoming NaN; all such quotients saturate.
+// Other scales (inv 0) are divided, which takes about three times the
+// instructions.
+__device__ __forceinline__ uint2 codes8(const F8 &nx, float scale, float inv)
 {
     uint32_t c[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4; ++i) {
+        float2 r;
+        if (inv != 0.f) {
+            const uint64_t ninv = pair(-inv, -inv);
+            const float2 q0 = lanes(mul2(nx.p[i], ninv));
+            const uint64_t q = pair(fmaxf(fminf(q0.x, 0x1p24f), -0x1p24f), fmaxf(fminf(q0.y, 0x1p24f), -0x1p24f));
+            r = lanes(fma2(fma2(q, pair(scale, scale), nx.p[i]), ninv, q));
+        } else {
+            const float2 n = lanes(nx.p[i]);
+            r = make_float2(__fdiv_rn(-n.x, scale), __fdiv_rn(-n.y, scale));
+        }
         asm("{\n\t.reg .b16 r;\n\tcvt.rn.satfinite.e4m3x2.f32 r, %1, %2;\n\tcvt.u32.u16 %0, r;\n\t}"
             : "=r"(c[i])
-            : "f"(__fdiv_rn(x.f[2 * i + 1], scale)), "f"(__fdiv_rn(x.f[2 * i], scale)));
+            : "f"(r.y), "f"(r.x));
+    }
     return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
-// Sine and cosine of pair `word`'s angle at the token's positions.
-__device__ __forceinline__ float2 turn_of(uint64_t word, const int32_t *positions, long long stride, int num_axes, int t)
+__device__ __forceinline__ uint4 lds128(uint32_t addr)
 {
-    const int axis = min((int)(word & 3u), num_axes - 1);
-    const long long pos = positions[axis * stride + t];
-    const uint64_t frac = (uint64_t)pos * (word & ~3ull);
-    float s, c;
-    sincospif((float)(int32_t)(frac >> 32) * 0x1p-31f, &s, &c);
-    return make_float2(c, s);
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
 }
 
-// One CTA per token.
-template <bool BF16, bool FP8, bool ADJ>
-__global__ void __launch_bounds__(kRopeThreads) rope_and_cache_kernel(const RopeParams p)
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
 {
-    __shared__ __align__(16) float s_cos[kRopeMaxPairs], s_sin[kRopeMaxPairs];
-    const int t = blockIdx.x;
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+                 "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+struct RopeBars {
+    uint64_t full[kRopeMaxStages], empty[kRopeMaxStages];
+    long long slot[kRopeMaxStages];
+    int token[kRopeMaxStages], first[kRopeMaxStages], count[kRopeMaxStages];  // heads first .. first + count - 1
+};
+
+// Persistent CTAs over units: a unit is a token, or heads_per_unit of its
+// heads (q, then k, then v heads, counted through). One warp brings the units'
+// rows into a ring of shared-memory stages by bulk copies, so that the bytes
+// in flight do not depend on registers; another computes each unit's sines
+// into its stage meanwhile; the others turn the heads and store.
+//
+// A lane of those holds one place of a head: 16 bytes of it (adjacent pairs),
+// or two times 16 bytes that lie rot / 2 apart, or of the dimensions that
+// pass; `per` lanes a head and 32 / per heads side by side make a group, and
+// the warps take the groups of all units in turn.
+template <bool BF16, bool FP8, bool ADJ>
+__global__ void __launch_bounds__(kRopeThreads, 2) rope_and_cache_kernel(const RopeParams p)
+{
+    constexpr int kPairs = ADJ ? 4 : 8;  // of a lane
+    constexpr int kVecs = ADJ ? 1 : 2;   // 16-byte vectors of a lane
+    extern __shared__ __align__(128) uint8_t rope_smem[];
+    __shared__ RopeBars bars;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t base = smem_addr(rope_smem);
+    if (threadIdx.x == 0) {
+        for (int st = 0; st < p.stages; ++st) {
+            mbar_init(smem_addr(&bars.full[st]), 2);  // the copies' bytes, the sines
+            mbar_init(smem_addr(&bars.empty[st]), kRopeWarps);
+        }
+        fence_barrier_init();
+    }
+    __syncthreads();
     // Launched with a programmatic dependency: nothing is read before the
     // preceding kernel (which may write the slots) is done, and only then may
     // the next one start, so that what it may read early is older still.
     grid_dependency_wait();
     grid_launch_dependents();
-    for (int i = threadIdx.x; i < p.rot_vecs * 4; i += kRopeThreads) {
-        const float2 cs = turn_of(p.plan[i], p.positions, p.pos_stride, p.num_axes, t);
-        s_cos[i] = cs.x;
-        s_sin[i] = cs.y;
+
+    const int hv = p.head_vecs, rv = p.rot_vecs, hq = p.num_q_heads, hk = hq + p.num_kv_heads, heads = hk + p.num_kv_heads;
+    const int pairs = rv * 4;
+    auto token_of = [&](long long u) { return (int)(p.units_per_token == 1 ? u : u / p.units_per_token); };
+    if (warp == kRopeWarps) {
+        // ---------------------------------------------------------- copies
+        long long slots = -1;  // of this CTA's units ahead, one a lane
+        int st = 0, ahead = 0;
+        uint32_t used = 0;  // rounds of the ring behind this stage
+        for (long long u = blockIdx.x; u < p.units; u += gridDim.x) {
+            if (ahead == 0) {
+                const long long mine = u + (long long)lane * gridDim.x;
+                if (mine < p.units)
+                    slots = p.slots[token_of(mine)];
+            }
+            const int t = token_of(u), h0 = (int)(u - (long long)t * p.units_per_token) * p.heads_per_unit;
+            const long long slot = __shfl_sync(kFull, slots, ahead);
+            const bool write = slot >= 0 && slot < p.num_slots;
+            const int h1 = min(h0 + p.heads_per_unit, write ? heads : hq), n = max(h1 - h0, 0);
+            const uint32_t full = smem_addr(&bars.full[st]), data = base + st * p.stage_bytes;
+            if (used > 0 && !__all_sync(kFull, mbar_wait(smem_addr(&bars.empty[st]), (used - 1) & 1))) {
+                if (lane == 0)
+                    rope_raise(PA_DEVERR_TIMEOUT);
+                return;  // the other warps wait (bounded) for what is in flight
+            }
+            if (lane == 0) {
+                if (slot >= p.num_slots && h0 == 0)
+                    rope_raise(PA_DEVERR_SLOT);
+                bars.slot[st] = slot;
+                bars.token[st] = t;
+                bars.first[st] = h0;
+                bars.count[st] = n;
+                fence_proxy_async();  // the stage's last reads, before it is written again
+                mbar_expect_tx(full, (uint32_t)(n * hv) * 16u);
+                auto load = [&](const void *row, long long stride, int a, int b, int from) {  // heads [a, b) of the unit's
+                    if (a < b)
+                        bulk_load(data + (uint32_t)((a - h0) * hv) * 16u,
+                                  static_cast<const uint4 *>(row) + t * stride + (long long)(a - from) * hv,
+                                  (uint32_t)((b - a) * hv) * 16u, full);
+                };
+                load(p.q, p.q_stride, h0, min(h1, hq), 0);
+                load(p.k, p.k_stride, max(h0, hq), min(h1, hk), hq);
+                load(p.v, p.v_stride, max(h0, hk), h1, hk);
+            }
+            __syncwarp();
+            ahead = (ahead + 1) & 31;
+            if (++st == p.stages) {
+                st = 0;
+                ++used;
+            }
+        }
+        return;
     }
-    const long long slot = p.slots[t];
-    const bool write = slot >= 0 && slot < p.num_slots;
-    if (slot >= p.num_slots && threadIdx.x == 0)
-        rope_raise(PA_DEVERR_SLOT);
-    __syncthreads();
-    const int hv = p.head_vecs, rv = p.rot_vecs, half = rv / 2;
-    const long long kv_row = (long long)p.num_kv_heads * hv;
-    const uint4 *q = static_cast<const uint4 *>(p.q) + t * p.q_stride, *k = static_cast<const uint4 *>(p.k) + t * p.k_stride,
-                *v = static_cast<const uint4 *>(p.v) + t * p.v_stride;
-    uint4 *q_out = static_cast<uint4 *>(p.q_out) + t * p.q_out_stride;
+    if (warp > kRopeWarps) {
+        // ----------------------------------------------------------- sines
+        uint64_t words[kRopeMaxDims / 64];  // a lane's plan words
+#pragma unroll
+        for (int k = 0; k < kRopeMaxDims / 64; ++k)
+            words[k] = lane + 32 * k < pairs ? p.plan[lane + 32 * k] : 0;
+        int pos[kRopeMaxAxes] = {0, 0, 0, 0};  // of this CTA's units ahead, one a lane
+        int st = 0, ahead = 0;
+        uint32_t used = 0;
+        for (long long u = blockIdx.x; u < p.units; u += gridDim.x) {
+            if (ahead == 0) {
+                const long long mine = u + (long long)lane * gridDim.x;
+                if (mine < p.units) {
+                    const int t = token_of(mine);
+#pragma unroll
+                    for (int a = 0; a < kRopeMaxAxes; ++a)
+                        if (a < p.num_axes)
+                            pos[a] = p.positions[a * p.pos_stride + t];
+                }
+            }
+            int at[kRopeMaxAxes];
+#pragma unroll
+            for (int a = 0; a < kRopeMaxAxes; ++a)
+                at[a] = __shfl_sync(kFull, pos[a], ahead);
+            if (used > 0 && !__all_sync(kFull, mbar_wait(smem_addr(&bars.empty[st]), (used - 1) & 1))) {
+                if (lane == 0)
+                    rope_raise(PA_DEVERR_TIMEOUT);
+                return;
+            }
+            float *cs = reinterpret_cast<float *>(rope_smem + st * p.stage_bytes + p.sines_at), *sn = cs + pairs;
+#pragma unroll
+            for (int k = 0; k < kRopeMaxDims / 64; ++k) {
+                const int e = lane + 32 * k;
+                if (e < pairs) {
+                    const int axis = min((int)(words[k] & 3u), p.num_axes - 1);
+                    const long long x = axis == 0 ? at[0] : axis == 1 ? at[1] : axis == 2 ? at[2] : at[3];
+                    const uint64_t turn = (uint64_t)x * (words[k] & ~3ull);
+                    sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, sn + e, cs + e);
+                }
+            }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(smem_addr(&bars.full[st]));
+            ahead = (ahead + 1) & 31;
+            if (++st == p.stages) {
+                st = 0;
+                ++used;
+            }
+        }
+        return;
+    }
+
+    // ---------------------------------------------------- turn and store
     using Out = typename std::conditional<FP8, uint2, uint4>::type;
-    Out *k_out = static_cast<Out *>(p.kv) + slot * kv_row, *v_out = k_out + p.num_slots * kv_row;
-    auto put_k = [&](long long i, const F8 &x) {
-        if constexpr (FP8)
-            k_out[i] = codes8(x, p.k_scale);
-        else
-            k_out[i] = pack8<BF16>(x);
-    };
-    // Units of a head: rotated vectors (in pairs, unless the pairs are
-    // adjacent), then those that pass.
-    const int per_head = ADJ ? hv : half + (hv - rv);
-    const int heads = p.num_q_heads + (write ? p.num_kv_heads : 0);
-    for (int i = threadIdx.x; i < heads * per_head; i += kRopeThreads) {
-        const int h = i / per_head, u = i - h * per_head;
-        const bool is_q = h < p.num_q_heads;
-        const long long at = (long long)(is_q ? h : h - p.num_q_heads) * hv;
-        const uint4 *src = is_q ? q : k;
-        if constexpr (ADJ) {
-            F8 x = unpack8<BF16>(src[at + u]);
-            if (u < rv) {
-                F8 y;
+    const long long kv_row = (long long)p.num_kv_heads * hv;
+    // Places of a head: those that turn, then those that pass.
+    const int turning = rv / kVecs, rest = hv - rv, passing = (rest + kVecs - 1) / kVecs, places = turning + passing;
+    const int segs = (places + 31) / 32, per = min(places, 32), side = 32 / per;
+    const int h_in = lane / per, in = lane - h_in * per;
+    int next = warp;  // this warp's next group, counted from the unit's first
+    int st = 0;
+    uint32_t phase = 0;
+    for (long long un = blockIdx.x; un < p.units; un += gridDim.x) {
+        if (!__all_sync(kFull, mbar_wait(smem_addr(&bars.full[st]), phase))) {
+            if (lane == 0)
+                rope_raise(PA_DEVERR_TIMEOUT);
+            return;
+        }
+        const long long slot = bars.slot[st];
+        const int t = bars.token[st], first = bars.first[st], n = bars.count[st];
+        const uint32_t data = base + st * p.stage_bytes, sines = data + p.sines_at;
+        uint4 *q_out = static_cast<uint4 *>(p.q_out) + t * p.q_out_stride;
+        Out *k_out = static_cast<Out *>(p.kv) + slot * kv_row, *v_out = k_out + p.num_slots * kv_row;
+        const int across = (n + side - 1) / side, groups = across * segs;
+        for (; next < groups; next += kRopeWarps) {
+            const int seg = segs == 1 ? 0 : next / across;
+            const int h = (next - seg * across) * side + h_in;  // of the unit
+            const int u = seg * 32 + in;
+            if (h_in >= side || h >= n || u >= places)
+                continue;
+            const bool turns = u < turning;
+            const int v0 = turns ? u : rv + (u - turning), v1 = turns ? turning + u : v0 + passing;
+            const bool two = !ADJ && v1 < hv;  // the second may be missing among those that pass
+            const int head = first + h;
+            const bool turn = turns && head < hk, code = FP8 && head >= hq;
+            uint4 a[kVecs];
+            a[0] = lds128(data + (uint32_t)(h * hv + v0) * 16u);
+            if constexpr (!ADJ)
+                a[1] = two ? lds128(data + (uint32_t)(h * hv + v1) * 16u) : make_uint4(0u, 0u, 0u, 0u);
+            if (code) {  // codes8 takes negated values
+#pragma unroll
+                for (int c = 0; c < kVecs; ++c)
+                    a[c] = negated(a[c]);
+            }
+            F8 y[kVecs];
+#pragma unroll
+            for (int c = 0; c < kVecs; ++c)
+                y[c] = unpack8<BF16>(a[c]);
+            if (turn) {
+                float cs[kPairs], sn[kPairs];
+#pragma unroll
+                for (int e = 0; e < kPairs; e += 4) {
+                    const uint4 c4 = lds128(sines + (uint32_t)(u * kPairs + e) * 4u);
+                    const uint4 s4 = lds128(sines + (uint32_t)(pairs + u * kPairs + e) * 4u);
+                    const uint32_t cw[4] = {c4.x, c4.y, c4.z, c4.w}, sw[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+                    for (int f = 0; f < 4; ++f) {
+                        cs[e + f] = __uint_as_float(cw[f]);
+                        sn[e + f] = __uint_as_float(sw[f]);
+                    }
+                }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float c = s_cos[4 * u + e], s = s_sin[4 * u + e];
-                    y.f[2 * e] = x.f[2 * e] * c - x.f[2 * e + 1] * s;
-                    y.f[2 * e + 1] = x.f[2 * e] * s + x.f[2 * e + 1] * c;
+                    if constexpr (ADJ) {
+                        // (x0, x1) (c, c) + (x1, x0) (-s, s)
+                        const float2 x = lanes(y[0].p[e]);
+                        y[0].p[e] = fma2(y[0].p[e], pair(cs[e], cs[e]), mul2(pair(x.y, x.x), pair(-sn[e], sn[e])));
+                    } else {
+                        const uint64_t x = y[0].p[e], z = y[1].p[e], c = pair(cs[2 * e], cs[2 * e + 1]);
+                        y[0].p[e] = fma2(x, c, mul2(z, pair(-sn[2 * e], -sn[2 * e + 1])));
+                        y[1].p[e] = fma2(z, c, mul2(x, pair(sn[2 * e], sn[2 * e + 1])));
+                    }
                 }
-                x = y;
             }
-            if (is_q)
-                q_out[at + u] = pack8<BF16>(x);
-            else
-                put_k(at + u, x);
-        } else if (u < half) {
-            const F8 a = unpack8<BF16>(src[at + u]), b = unpack8<BF16>(src[at + half + u]);
-            F8 y, z;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float c = s_cos[8 * u + e], s = s_sin[8 * u + e];
-                y.f[e] = a.f[e] * c - b.f[e] * s;
-                z.f[e] = a.f[e] * s + b.f[e] * c;
-            }
-            if (is_q) {
-                q_out[at + u] = pack8<BF16>(y);
-                q_out[at + half + u] = pack8<BF16>(z);
+            const long long row = (long long)(head < hq ? head : head < hk ? head - hq : head - hk) * hv;
+            if (code) {
+                uint2 *to = reinterpret_cast<uint2 *>((head < hk ? k_out : v_out) + row);
+                const float scale = head < hk ? p.k_scale : p.v_scale, inv = head < hk ? p.k_inv : p.v_inv;
+                to[v0] = codes8(y[0], scale, inv);
+                if constexpr (!ADJ)
+                    if (two)
+                        to[v1] = codes8(y[1], scale, inv);
             } else {
-                put_k(at + u, y);
-                put_k(at + half + u, z);
+                uint4 *to = head < hq ? q_out + row : reinterpret_cast<uint4 *>((head < hk ? k_out : v_out) + row);
+                to[v0] = turn ? pack8<BF16>(y[0]) : a[0];
+                if constexpr (!ADJ)
+                    if (two)
+                        to[v1] = turn ? pack8<BF16>(y[1]) : a[1];
             }
-        } else {
-            const int w = rv + (u - half);
-            const uint4 x = src[at + w];
-            if (is_q)
-                q_out[at + w] = x;
-            else
-                put_k(at + w, unpack8<BF16>(x));
+        }
+        next -= groups;  // >= 0: this warp's turn in the next unit
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(smem_addr(&bars.empty[st]));
+        if (++st == p.stages) {
+            st = 0;
+            phase ^= 1;
         }
     }
-    if (write)
-        for (int i = threadIdx.x; i < kv_row; i += kRopeThreads) {
-            if constexpr (FP8)
-                v_out[i] = codes8(unpack8<BF16>(v[i]), p.v_scale);
-            else
-                v_out[i] = v[i];
-        }
 }
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// The current device and its SM count (cached per device).
+int rope_device(const char *who, int *dev, int *sms)
+{
+    static std::mutex mu;
+    static int count[64] = {};
+    cudaError_t e = cudaGetDevice(dev);
+    std::lock_guard<std::mutex> lock(mu);
+    *sms = e == cudaSuccess && *dev < 64 ? count[*dev] : 0;
+    if (e == cudaSuccess && *sms <= 0) {
+        e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev);
+        if (e == cudaSuccess && *dev < 64)
+            count[*dev] = *sms;
+    }
+    return e == cudaSuccess && *sms > 0 ? PA_OK : set_error(PA_ERR_CUDA, "%s: device: %s", who, cudaGetErrorString(e));
+}
 
 int rope_impl(const char *who, void *query_out, const void *query, const void *key, const void *value, void *kv_cache,
               const int32_t *slot_mapping, const int32_t *positions, int num_axes, long long position_stride,
@@ -212,9 +458,9 @@ int rope_impl(const char *who, void *query_out, const void *query, const void *k
         return set_error(PA_ERR_INVALID_ARG, "%s: bad sizes", who);
     if (head_size <= 0 || head_size % 8 != 0 || head_size > 1024)
         return set_error(PA_ERR_UNSUPPORTED, "%s: head_size %d (want a multiple of 8, at most 1024)", who, head_size);
-    if (rot_dim <= 0 || rot_dim % 16 != 0 || rot_dim > head_size || rot_dim > 2 * kRopeMaxPairs)
+    if (rot_dim <= 0 || rot_dim % 16 != 0 || rot_dim > head_size || rot_dim > kRopeMaxDims)
         return set_error(PA_ERR_UNSUPPORTED, "%s: rot_dim %d (want a multiple of 16, at most head_size and %d)", who, rot_dim,
-                         2 * kRopeMaxPairs);
+                         kRopeMaxDims);
     if (num_axes < 1 || num_axes > kRopeMaxAxes || (num_axes > 1 && position_stride < num_tokens))
         return set_error(PA_ERR_INVALID_ARG, "%s: num_axes %d (1 to %d), position_stride %lld (at least num_tokens)", who,
                          num_axes, kRopeMaxAxes, position_stride);
@@ -257,6 +503,9 @@ int rope_impl(const char *who, void *query_out, const void *query, const void *k
     prm.num_axes = num_axes;
     prm.k_scale = k_scale;
     prm.v_scale = v_scale;
+    auto inverse = [](float scale) { return scale >= 0x1p-64f && scale <= 0x1p64f ? 1.f / scale : 0.f; };
+    prm.k_inv = inverse(k_scale);
+    prm.v_inv = inverse(v_scale);
     static const void *const kernels[8] = {
         reinterpret_cast<const void *>(&rope_and_cache_kernel<false, false, false>),
         reinterpret_cast<const void *>(&rope_and_cache_kernel<true, false, false>),
@@ -266,9 +515,47 @@ int rope_impl(const char *who, void *query_out, const void *query, const void *k
         reinterpret_cast<const void *>(&rope_and_cache_kernel<true, false, true>),
         reinterpret_cast<const void *>(&rope_and_cache_kernel<false, true, true>),
         reinterpret_cast<const void *>(&rope_and_cache_kernel<true, true, true>)};
+    int dev = 0, sms = 0;
+    int rc = rope_device(who, &dev, &sms);
+    if (rc != PA_OK)
+        return rc;
+    // Units: a token, in equal parts if its rows are longer than a unit's, or
+    // if there are too few tokens for the CTAs; not below a group for each warp.
+    const int heads = num_q_heads + 2 * num_kv_heads, head_bytes = head_size * 2;
+    const int vecs = adjacent ? 1 : 2, places = rot_dim / 8 / vecs + ((head_size - rot_dim) / 8 + vecs - 1) / vecs;
+    const int side = places < 32 ? 32 / places : 1;
+    int parts = std::max(1, (heads * head_bytes + kRopeUnitBytes - 1) / kRopeUnitBytes);
+    const long long wanted = (2LL * sms + num_tokens - 1) / num_tokens;
+    const int most = std::max(parts, heads / (side * kRopeWarps));
+    parts = (int)std::min<long long>(std::max<long long>(parts, wanted), most);
+    parts = std::min(parts, heads);
+    prm.heads_per_unit = ((heads + parts - 1) / parts + side - 1) / side * side;
+    prm.units_per_token = (heads + prm.heads_per_unit - 1) / prm.heads_per_unit;
+    prm.units = (long long)num_tokens * prm.units_per_token;
+    prm.sines_at = prm.heads_per_unit * head_bytes;
+    prm.stage_bytes = (prm.sines_at + rot_dim * 4 + 127) & ~127;
+    prm.stages = std::max(1, std::min(kRopeMaxStages, kRopeSmemBytes / prm.stage_bytes));
+    const int smem = prm.stages * prm.stage_bytes;
+    const void *fn = kernels[(adjacent ? 4 : 0) + (fp8 ? 2 : 0) + (dtype == PA_BF16 ? 1 : 0)];
+    // Allow the largest ring once per kernel and device, so that a call being
+    // captured into a CUDA graph makes no attribute call.
+    {
+        static std::mutex mu;
+        static bool raised[8][64] = {};
+        const int variant = (adjacent ? 4 : 0) + (fp8 ? 2 : 0) + (dtype == PA_BF16 ? 1 : 0);
+        std::lock_guard<std::mutex> lock(mu);
+        if (dev >= 64 || !raised[variant][dev]) {
+            cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kRopeSmemBytes);
+            if (e != cudaSuccess)
+                return set_error(PA_ERR_CUDA, "%s: cudaFuncSetAttribute: %s", who, cudaGetErrorString(e));
+            if (dev < 64)
+                raised[variant][dev] = true;
+        }
+    }
     void *args[] = {&prm};
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(num_tokens);
+    cfg.gridDim = dim3((unsigned)std::min<long long>(prm.units, 2LL * sms));
+    cfg.dynamicSmemBytes = (size_t)smem;
     cfg.blockDim = dim3(kRopeThreads);
     cfg.stream = reinterpret_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[1];
@@ -276,7 +563,7 @@ int rope_impl(const char *who, void *query_out, const void *query, const void *k
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelExC(&cfg, kernels[(adjacent ? 4 : 0) + (fp8 ? 2 : 0) + (dtype == PA_BF16 ? 1 : 0)], args);
+    cudaError_t e = cudaLaunchKernelExC(&cfg, fn, args);
     if (e != cudaSuccess)
         return set_error(PA_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
     return PA_OK;

@@ -268,6 +268,31 @@ def test_a_pool_past_2_to_the_32_bytes(dev):
     assert binding.pa_get_device_error() == 0
 
 
+@pytest.mark.parametrize("dtype", [workloads.F16, workloads.BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("scale", [0.0125, 0.01, 1.0, 1 / 3, 448.0, 6.1e-5, 1e-19, 3.3e19, 1e-25, 7e30])
+def test_codes_of_every_value_are_the_write_paths(dev, dtype, scale):
+    """All 65536 bit patterns as V and (unturned, at position 0) as K: the codes of pa_reshape_and_cache_fp8, which
+    divides; the last two scales are outside the range of the reciprocal."""
+    import torch
+    T, hkv, D = 64, 8, 128
+    x = torch.arange(65536, device=dev).to(torch.int32).to(torch.int16).view(workloads.torch_dtype(dtype)).view(T, hkv, D)
+    pools = [torch.zeros((2, 4, 16, hkv, D), dtype=torch.uint8, device=dev) for _ in range(2)]
+    slots = torch.arange(T, dtype=torch.int32, device=dev)
+    binding.pa_reshape_and_cache_fp8(x, x, pools[0], slots, scale, scale)
+    binding.pa_rope_and_cache_fp8(torch.empty_like(x), x, x, x, pools[1], slots, torch.zeros_like(slots),
+                                  binding.rope_plan(np.ones(8), None, dev), scale, scale)
+    torch.cuda.synchronize()
+    assert torch.equal(pools[0][1], pools[1][1])
+    # A turned pair mixes NaN and Inf (x 1 - Inf 0): compare K where the pair is finite, and the dimensions that pass.
+    pair = torch.isfinite(x[..., :8]) & torch.isfinite(x[..., 8:16])
+    got, want = (p[0].view(T, hkv, D) for p in pools)
+    assert torch.equal(got[..., 16:], want[..., 16:])
+    for a in (slice(0, 8), slice(8, 16)):
+        # -0 - Inf-free products can turn -0 into +0: the codes of both are equal values.
+        same = (got[..., a] == want[..., a]) | (((got[..., a] | want[..., a]) & 0x7F) == 0)
+        assert bool(same[pair].all())
+
+
 def test_no_tokens(dev):
     import torch
     c = RopeCase(dev, workloads.F16, 4, 2, 2, 64, seed=15)
