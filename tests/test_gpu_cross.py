@@ -168,6 +168,19 @@ def test_a_larger_bound_than_the_longest_chunk(dev):
         c.check(c.run(ws, max_q=most))
 
 
+@pytest.mark.parametrize("fp8", [False, True], ids=["16bit", "fp8"])
+@pytest.mark.parametrize("dtype", [workloads.F16, workloads.BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("heads,most", [((4, 4, 64), 128), ((8, 2, 128), 32), ((32, 1, 128), 8), ((12, 2, 128), 16), ((20, 20, 64), 127)],
+                         ids=lambda x: "%dx%dx%d" % x if isinstance(x, tuple) else str(x))
+def test_chunks_of_one_query_tile(dev, heads, most, dtype, fp8):
+    """Chunks that fit one 128-row tile (up to exactly): its two halves of the tensor memory then take every other K/V
+    tile. One tile, odd and even counts of them, ends inside a tile, none; one sequence and many."""
+    kv = [1, 127, 128, 129, 256, 257, 384, 1000, 0, 1151, 5, 640]
+    qlen = [most, 1, most, most - 1, 2, most, 0, most, most, 3, most, most // 2]
+    CrossCase(dev, dtype, *heads, qlen, kv, fp8=fp8, seed=most + dtype).both()
+    CrossCase(dev, dtype, *heads, [most], [3333], fp8=fp8, seed=most + 1).both()
+
+
 @pytest.mark.parametrize("qlen", [[1], [7], [600]])
 def test_one_long_sequence(dev, qlen):
     CrossCase(dev, workloads.F16, 8, 2, 128, qlen, [30011], seed=5).both()
