@@ -179,18 +179,33 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 #ifndef PA_DECODE_WARPS_FP8
 #define PA_DECODE_WARPS_FP8 12
 #endif
+// Whether a tile's fragments are read as the MMAs need them, V's after the
+// softmax, instead of all up front: ragged 16-column tiles of an FP8 cache at
+// head size 128, where that lets 12 warps fit an SM's registers (a stage is
+// then held longer, and the ring is one deeper). Measured at 48 x 1-4 queries
+// over up to 6404 states of 32/8 heads: 94 us up front, 87 us late; with a
+// 16-bit cache at 48 x 4 over 6404 it is 199 against 215 us the other way.
+template <int D, int NT, bool FP8, bool RAGGED>
+constexpr bool decode_late()
+{
+    return RAGGED && FP8 && NT == 2 && D == 128;
+}
 template <int D, int NT, bool FP8, bool RAGGED>
 constexpr int decode_warps()
 {
     if (RAGGED && D == 64)
         return PA_ROWS_WARPS_64;
+    if (decode_late<D, NT, FP8, RAGGED>())
+        return 12;
     return NT == 1 ? (FP8 ? PA_DECODE_WARPS_FP8 : PA_DECODE_WARPS) : PA_DECODE_WARPS_WIDE;
 }
 // TMA ring depth per warp. An FP8 tile is half the bytes of a 16-bit one, so
 // the FP8 pipelines keep two in flight to hold the same bytes in flight.
-template <bool FP8>
+template <int D, int NT, bool FP8, bool RAGGED>
 constexpr int decode_stages()
 {
+    if (decode_late<D, NT, FP8, RAGGED>())
+        return 3;
     return FP8 ? PA_DECODE_STAGES_FP8 : PA_DECODE_STAGES;
 }
 constexpr int kTile = 16;       // tokens per tile (the MMA's M)
@@ -261,10 +276,10 @@ constexpr int record_floats()
     return NT * 8 * (D + 2);  // m[GP], l[GP], O[GP][D]; only live query columns are written
 }
 
-template <int D, int WARPS, bool FP8, bool RAGGED>
+template <int D, int NT, bool FP8, bool RAGGED>
 inline size_t decode_smem_bytes(int num_seqs)
 {
-    constexpr int kStages = decode_stages<FP8>();
+    constexpr int kStages = decode_stages<D, NT, FP8, RAGGED>(), WARPS = decode_warps<D, NT, FP8, RAGGED>();
     size_t b = 1024;  // alignment slack for the 1024-byte swizzle atoms
     b += (size_t)WARPS * kStages * TileGeo<D, FP8>::kStageBytes;
     b += (size_t)WARPS * kStages * sizeof(uint64_t);
@@ -335,7 +350,7 @@ __global__ void __launch_bounds__(decode_warps<D, NT, FP8, RAGGED>() * 32)
 {
     using Geo = TileGeo<D, FP8>;
     constexpr int kWarps = decode_warps<D, NT, FP8, RAGGED>();
-    constexpr int kStages = decode_stages<FP8>();
+    constexpr int kStages = decode_stages<D, NT, FP8, RAGGED>();
     constexpr int KS = D / 16;  // k-steps of QK^T and m-tiles of V^T P^T
     constexpr int GP = NT * 8;
     constexpr int STAGE = Geo::kStageBytes;
@@ -350,6 +365,7 @@ __global__ void __launch_bounds__(decode_warps<D, NT, FP8, RAGGED>() * 32)
     // that fp16 keeps weights down to 2^-32 of the largest.
     constexpr bool MBF16 = BF16 && !FP8;
     constexpr float kPShift = FP8 ? 8.f : 0.f;
+    constexpr bool kLate = decode_late<D, NT, FP8, RAGGED>();
 
     extern __shared__ uint8_t smem_raw[];
     __shared__ long long warp_sums[kWarps];
@@ -782,8 +798,38 @@ __global__ void __launch_bounds__(decode_warps<D, NT, FP8, RAGGED>() * 32)
         // first, and the k-steps alternate between two accumulators, so the
         // MMA chain is half as long as the head dimension. V^T fragments do
         // not depend on P: they are loaded up front as well.
-        uint32_t kf[KS][4];
-        uint32_t vf[KS][4];
+        float sc[NT][4], sc2[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                sc[nt][c] = sc2[nt][c] = 0.f;
+        uint32_t kf[kLate ? 4 : KS][4];
+        uint32_t vf[kLate ? 1 : KS][4];
+        if constexpr (kLate) {
+            // Four k-steps at a time: their fragments, then their MMAs.
+#pragma unroll
+            for (int k0 = 0; k0 < KS; k0 += 4) {
+                const int c = CPT * tig + k0 / 4;
+                const uint4 r0 = lds128(sbuf + fp8_off<D>(g, c));
+                const uint4 r1 = lds128(sbuf + fp8_off<D>(g + 8, c));
+                const uint32_t w0[4] = {r0.x, r0.y, r0.z, r0.w};
+                const uint32_t w1[4] = {r1.x, r1.y, r1.z, r1.w};
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    kf[w][0] = e4m3x2_lo_to_f16x2(w0[w]);
+                    kf[w][1] = e4m3x2_lo_to_f16x2(w1[w]);
+                    kf[w][2] = e4m3x2_hi_to_f16x2(w0[w]);
+                    kf[w][3] = e4m3x2_hi_to_f16x2(w1[w]);
+                }
+#pragma unroll
+                for (int w = 0; w < 4; ++w)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma16816<MBF16>(w & 1 ? sc2[nt] : sc[nt], kf[w][0], kf[w][1], kf[w][2], kf[w][3], qf[nt][k0 + w][0],
+                                        qf[nt][k0 + w][1]);
+            }
+        } else {
         if constexpr (FP8) {
             // K rows g and g+8, chunks c = CPT tig + j, widened in registers.
             // Word w of chunk j holds the dims of permuted k-step 4j + w.
@@ -852,12 +898,6 @@ __global__ void __launch_bounds__(decode_warps<D, NT, FP8, RAGGED>() * 32)
             }
         }
 
-        float sc[NT][4], sc2[NT][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-                sc[nt][c] = sc2[nt][c] = 0.f;
 #pragma unroll
         for (int kk = 0; kk < KS; kk += 2)
 #pragma unroll
@@ -870,6 +910,7 @@ __global__ void __launch_bounds__(decode_warps<D, NT, FP8, RAGGED>() * 32)
         // Every fragment of this tile is now in registers: hand the stage back
         // to the TMA right away, so the ring stays full while the math runs.
         refill();
+        }
 
         // Online softmax (base 2) per query column. P is rounded to the
         // element type; with an FP8 cache it is rounded to fp16 (V is widened
@@ -924,12 +965,39 @@ __global__ void __launch_bounds__(decode_warps<D, NT, FP8, RAGGED>() * 32)
         }
 
         // O^T[D][8*NT] += V^T P^T
+        if constexpr (kLate) {
+            // This thread's V bytes and their m-tiles, as above.
+            const uint32_t vbase = sbuf + Geo::kVOffset;
+            uint32_t vw[4][4];
 #pragma unroll
-        for (int mt = 0; mt < KS; ++mt)
+            for (int t = 0; t < 4; ++t) {
+                const uint4 x = lds128(vbase + fp8_off<D>(2 * tig + (t & 1) + (t >> 1) * 8, g));
+                vw[t][0] = x.x;
+                vw[t][1] = x.y;
+                vw[t][2] = x.z;
+                vw[t][3] = x.w;
+            }
+            refill();
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-                mma16816<MBF16>(acc[mt][nt], vf[mt][0], vf[mt][1], vf[mt][2], vf[mt][3], pb[nt][0],
-                                pb[nt][1]);
+            for (int mt = 0; mt < KS; ++mt) {
+                const int wi = mt >> 1;
+                const uint32_t sel = (mt & 1) ? 0x7362u : 0x5140u;
+                const uint32_t x01 = prmt(vw[0][wi], vw[1][wi], sel), x23 = prmt(vw[2][wi], vw[3][wi], sel);
+                vf[0][0] = e4m3x2_lo_to_f16x2(x01);
+                vf[0][1] = e4m3x2_hi_to_f16x2(x01);
+                vf[0][2] = e4m3x2_lo_to_f16x2(x23);
+                vf[0][3] = e4m3x2_hi_to_f16x2(x23);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    mma16816<MBF16>(acc[mt][nt], vf[0][0], vf[0][1], vf[0][2], vf[0][3], pb[nt][0], pb[nt][1]);
+            }
+        } else {
+#pragma unroll
+            for (int mt = 0; mt < KS; ++mt)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    mma16816<MBF16>(acc[mt][nt], vf[mt][0], vf[mt][1], vf[mt][2], vf[mt][3], pb[nt][0], pb[nt][1]);
+        }
 
         if (++st == kStages) {
             st = 0;
@@ -971,13 +1039,14 @@ struct MergeState {
 // Fold the pieces o = o_first, o_first + ostep, ... <= o_hi into the state.
 // Piece o's record is slot first_slot when o == o_lo, else 2o. PPR pieces
 // are loaded per round (m, l and the O rows together) and folded with the
-// online-softmax rule; a piece with m = -inf (an empty share) weighs 0.
-template <int D, int NT>
+// online-softmax rule; a piece with m = -inf (an empty share) weighs 0. The
+// state holds CN * 8 of a record's NT * 8 columns, from column c0 on.
+template <int D, int NT, int CN>
 __device__ void fold_pieces(const float *recs, int o_first, int ostep, int o_hi, int o_lo,
-                            int first_slot, int tq, MergeState<D, NT> &st)
+                            int first_slot, int tq, int c0, MergeState<D, CN> &st)
 {
-    constexpr int GP = NT * 8, KD = D / 32, REC = record_floats<D, NT>();
-    constexpr int PPR = NT == 1 ? 2 : 1;
+    constexpr int RP = NT * 8, GP = CN * 8, KD = D / 32, REC = record_floats<D, NT>();
+    constexpr int PPR = CN == 1 ? 2 : 1;
     const int lane = threadIdx.x & 31;
     for (int o0 = o_first; o0 <= o_hi; o0 += PPR * ostep) {
         float mp[PPR][GP], lp[PPR][GP], x[PPR][GP][KD];
@@ -988,12 +1057,12 @@ __device__ void fold_pieces(const float *recs, int o_first, int ostep, int o_hi,
             const float *r = recs + (long long)(o == o_lo ? first_slot : 2 * o) * REC;
 #pragma unroll
             for (int c = 0; c < GP; ++c) {
-                const bool live = ok && c < tq;
-                mp[j][c] = live ? __ldcg(r + c) : -INFINITY;
-                lp[j][c] = live ? __ldcg(r + GP + c) : 0.f;
+                const bool live = ok && c0 + c < tq;
+                mp[j][c] = live ? __ldcg(r + c0 + c) : -INFINITY;
+                lp[j][c] = live ? __ldcg(r + RP + c0 + c) : 0.f;
 #pragma unroll
                 for (int k = 0; k < KD; ++k)
-                    x[j][c][k] = live ? __ldcg(r + 2 * GP + c * D + lane + 32 * k) : 0.f;
+                    x[j][c][k] = live ? __ldcg(r + 2 * RP + (c0 + c) * D + lane + 32 * k) : 0.f;
             }
         }
         // A marked empty share (m = -inf) has no O rows: never read them.
@@ -1041,10 +1110,19 @@ __device__ void fold_pieces(const float *recs, int o_first, int ostep, int o_hi,
 constexpr int kSmallTask = 6;    // pieces a single warp merges on its own
 constexpr int kReduceWarps = 4;  // warps per reduce CTA
 
-template <int D, int NT>
+// Ragged 16-column tiles are merged in two halves of 8 columns, each by a warp
+// of its own (16 columns of state take 210 registers and one piece at a time).
+template <int NT, bool RAGGED>
+constexpr int merge_groups()
+{
+    return RAGGED ? NT : 1;
+}
+
+template <int D, int NT, bool RAGGED>
 constexpr size_t reduce_smem_bytes()
 {
-    return (size_t)kReduceWarps * (2 * NT * 8 + D * NT * 8) * sizeof(float);  // per warp: M, l, O
+    constexpr int CN = NT / merge_groups<NT, RAGGED>();
+    return (size_t)kReduceWarps * (2 * CN * 8 + D * CN * 8) * sizeof(float);  // per warp: M, l, O
 }
 
 // Finish the segments cut by warp-share boundaries. Warp j of reduce CTA r
@@ -1059,13 +1137,14 @@ constexpr size_t reduce_smem_bytes()
 template <int D, int NT, bool BF16, bool RAGGED>
 __global__ void __launch_bounds__(kReduceWarps * 32) paged_decode_reduce_kernel(const DecodeParams p)
 {
-    constexpr int GP = NT * 8, KD = D / 32, PART = 2 * GP + GP * D;
+    constexpr int NG = merge_groups<NT, RAGGED>(), CN = NT / NG, GP = CN * 8, KD = D / 32, PART = 2 * GP + GP * D;
     extern __shared__ float s_part[];  // [kReduceWarps][M GP | l GP | O GP x D]
     __shared__ int4 s_task[kReduceWarps];
 
     grid_dependency_wait();  // the main grid's records and tasks are complete
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int w = blockIdx.x * kReduceWarps + warp;
+    const int w = (blockIdx.x * kReduceWarps + warp) / NG;
+    const int c0 = NG == 1 ? 0 : ((blockIdx.x * kReduceWarps + warp) % NG) * GP;  // this warp's columns
     const int tq = p.tile_q;
     const int segs_per_seq = p.num_kv_heads * p.qtiles;
     uint16_t *out_base = static_cast<uint16_t *>(p.out);
@@ -1090,10 +1169,10 @@ __global__ void __launch_bounds__(kReduceWarps * 32) paged_decode_reduce_kernel(
             return c < tq ? o.first + (long long)c * D : nullptr;
         }
     };
-    auto store = [&](const OutRows &o, const MergeState<D, NT> &st) {
+    auto store = [&](const OutRows &o, const MergeState<D, CN> &st) {
 #pragma unroll
         for (int c = 0; c < GP; ++c)
-            if (uint16_t *out = out_row(o, c)) {
+            if (uint16_t *out = out_row(o, c0 + c)) {
                 const float inv = 1.f / st.l[c];
 #pragma unroll
                 for (int k = 0; k < KD; ++k)
@@ -1106,9 +1185,9 @@ __global__ void __launch_bounds__(kReduceWarps * 32) paged_decode_reduce_kernel(
     if (lane == 0)
         s_task[warp] = (task.x >= 0 && !small) ? task : make_int4(-1, 0, 0, 0);
     if (small) {
-        MergeState<D, NT> st;
+        MergeState<D, CN> st;
         st.clear();
-        fold_pieces<D, NT>(p.warp_records, task.y, 1, w, task.y, task.z, tq, st);
+        fold_pieces<D, NT, CN>(p.warp_records, task.y, 1, w, task.y, task.z, tq, c0, st);
         store(out_rows(task.x), st);
     }
     __syncthreads();
@@ -1117,10 +1196,11 @@ __global__ void __launch_bounds__(kReduceWarps * 32) paged_decode_reduce_kernel(
         const int4 t = s_task[j];
         if (t.x < 0)
             continue;
-        const int last = blockIdx.x * kReduceWarps + j;
-        MergeState<D, NT> st;
+        const int last = (blockIdx.x * kReduceWarps + j) / NG;
+        const int cj = NG == 1 ? 0 : ((blockIdx.x * kReduceWarps + j) % NG) * GP;
+        MergeState<D, CN> st;
         st.clear();
-        fold_pieces<D, NT>(p.warp_records, t.y + warp, kReduceWarps, last, t.y, t.z, tq, st);
+        fold_pieces<D, NT, CN>(p.warp_records, t.y + warp, kReduceWarps, last, t.y, t.z, tq, cj, st);
         float *mine = s_part + warp * PART;
 #pragma unroll
         for (int c = 0; c < GP; ++c) {
@@ -1135,9 +1215,9 @@ __global__ void __launch_bounds__(kReduceWarps * 32) paged_decode_reduce_kernel(
         __syncthreads();
         // Combine the warps' states (fixed order), elements across the CTA.
         const OutRows o = out_rows(t.x);
-        for (int e = threadIdx.x; e < tq * D; e += kReduceWarps * 32) {
+        for (int e = threadIdx.x; e < min(tq - cj, GP) * D; e += kReduceWarps * 32) {
             const int c = e / D, d = e - (e / D) * D;
-            uint16_t *out = out_row(o, c);
+            uint16_t *out = out_row(o, cj + c);
             if (!out)
                 continue;
             float Mx = -INFINITY;
@@ -1426,6 +1506,7 @@ struct DecodePlan {
     const void *main_fn = nullptr;
     const void *reduce_fn = nullptr;
     size_t reduce_smem = 0;
+    int merge_groups = 1;  // merge warps per main-grid warp
     size_t total() const { return prefix_bytes + task_bytes + warp_record_bytes; }
 };
 
@@ -1435,8 +1516,9 @@ void pick_kernels(DecodePlan &pl, int num_seqs)
     pl.main_fn = reinterpret_cast<const void *>(&paged_decode_kernel<D, NT, BF16, FP8, RAGGED>);
     pl.warps = decode_warps<D, NT, FP8, RAGGED>();
     pl.reduce_fn = reinterpret_cast<const void *>(&paged_decode_reduce_kernel<D, NT, BF16, RAGGED>);
-    pl.reduce_smem = reduce_smem_bytes<D, NT>();
-    pl.smem = decode_smem_bytes<D, decode_warps<D, NT, FP8, RAGGED>(), FP8, RAGGED>(num_seqs);
+    pl.reduce_smem = reduce_smem_bytes<D, NT, RAGGED>();
+    pl.merge_groups = merge_groups<NT, RAGGED>();
+    pl.smem = decode_smem_bytes<D, NT, FP8, RAGGED>(num_seqs);
 }
 
 template <int D, int NT, bool RAGGED>
@@ -1640,7 +1722,7 @@ int launch_decode(const char *fn, void *out, const void *query, const void *kv_c
     if (e != cudaSuccess)
         return set_error(PA_ERR_CUDA, "%s: main kernel launch: %s", fn, cudaGetErrorString(e));
     void *red_args[] = {&prm};
-    e = launch_pdl(pl.reduce_fn, dim3((pl.total_warps + kReduceWarps - 1) / kReduceWarps),
+    e = launch_pdl(pl.reduce_fn, dim3((pl.total_warps * pl.merge_groups + kReduceWarps - 1) / kReduceWarps),
                    dim3(kReduceWarps * 32), red_args, pl.reduce_smem, s);
     if (e != cudaSuccess)
         return set_error(PA_ERR_CUDA, "%s: reduce kernel launch: %s", fn, cudaGetErrorString(e));
