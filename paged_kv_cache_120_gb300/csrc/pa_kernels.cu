@@ -209,6 +209,7 @@ constexpr int decode_stages()
     return FP8 ? PA_DECODE_STAGES_FP8 : PA_DECODE_STAGES;
 }
 constexpr int kTile = 16;       // tokens per tile (the MMA's M)
+constexpr int kMinShare = 8;    // ragged: tiles of a share at least
 constexpr int kMaxSeqs = 4096;  // sequences per pa_decode call (prefix lives in smem)
 
 // One pipeline stage: a 16-token tile of one kv head, K rows then V rows.
@@ -465,11 +466,16 @@ __global__ void __launch_bounds__(decode_warps<D, NT, FP8, RAGGED>() * 32)
         }
 
     // 2. This warp's contiguous share of the unit sequence.
-    const int gw = blockIdx.x * kWarps + warp;
-    const long long r0 = share_lo(N, gw, p.total_warps);
-    const long long r1 = share_lo(N, gw + 1, p.total_warps);
+    // Ragged: with few tiles fewer warps get a share, of kMinShare tiles at
+    // least (fewer pieces to merge), and those spread over the SMs.
+    const int owners = RAGGED ? (int)max(1LL, min((long long)p.total_warps, N / kMinShare)) : p.total_warps;
+    const int gw = owners < p.total_warps ? warp * gridDim.x + blockIdx.x : blockIdx.x * kWarps + warp;
+    const long long r0 = share_lo(N, gw, owners);
+    const long long r1 = share_lo(N, gw + 1, owners);
     if (lane == 0)
         p.tasks[gw] = make_int4(-1, 0, 0, 0);
+    if (RAGGED && gw >= owners)
+        return;
     if (r0 >= r1) {
         // An empty share is a zero-weight piece of whatever segment spans it:
         // mark its first record (m = -inf, l = 0) so merges can skip it.
@@ -709,8 +715,8 @@ __global__ void __launch_bounds__(decode_warps<D, NT, FP8, RAGGED>() * 32)
             if (lane == 0 && seg_start < r0 && seg_end <= r1) {
                 // This warp holds the segment's last piece: post the merge task
                 // with the segment's first owner and that owner's record slot.
-                const int o_lo = owner_of(seg_start, N, p.total_warps);
-                const int first = seg_start == share_lo(N, o_lo, p.total_warps) ? 2 * o_lo : 2 * o_lo + 1;
+                const int o_lo = owner_of(seg_start, N, owners);
+                const int first = seg_start == share_lo(N, o_lo, owners) ? 2 * o_lo : 2 * o_lo + 1;
                 p.tasks[gw] = make_int4(seg, o_lo, first, 0);
             }
 #pragma unroll
@@ -1108,7 +1114,11 @@ __device__ void fold_pieces(const float *recs, int o_first, int ostep, int o_hi,
 }
 
 constexpr int kSmallTask = 6;    // pieces a single warp merges on its own
-constexpr int kReduceWarps = 4;  // warps per reduce CTA
+// Warps per merge CTA. A segment cut into many pieces is merged by one CTA:
+// ragged batches of so few segments that each has kManyPieces or more take the
+// larger one (measured at 1 / 4 / 48 sequences of 6404 states and 8 kv heads:
+// 36 / 40 / 81 us with 4 warps, 29 / 35 / 88 with 8).
+constexpr int kMergeWarps = 4, kMergeWarpsMany = 8, kManyPieces = 8;
 
 // Ragged 16-column tiles are merged in two halves of 8 columns, each by a warp
 // of its own (16 columns of state take 210 registers and one piece at a time).
@@ -1118,33 +1128,33 @@ constexpr int merge_groups()
     return RAGGED ? NT : 1;
 }
 
-template <int D, int NT, bool RAGGED>
+template <int D, int NT, bool RAGGED, int W>
 constexpr size_t reduce_smem_bytes()
 {
     constexpr int CN = NT / merge_groups<NT, RAGGED>();
-    return (size_t)kReduceWarps * (2 * CN * 8 + D * CN * 8) * sizeof(float);  // per warp: M, l, O
+    return (size_t)W * (2 * CN * 8 + D * CN * 8) * sizeof(float);  // per warp: M, l, O
 }
 
 // Finish the segments cut by warp-share boundaries. Warp j of reduce CTA r
 // serves main-grid warp
-// r * kReduceWarps + j: if that warp holds the last piece of a split segment,
+// r * W + j: if that warp holds the last piece of a split segment,
 // the segment's pieces (one record per main-grid warp, ascending) are merged
 // with the online-softmax rule m = max m_p, l = sum l_p 2^(m_p - m),
 // O = sum O_p 2^(m_p - m). A task with few pieces is merged by its warp; a
 // task with many pieces by the whole CTA, pieces split across the warps and
 // the warps' states combined in shared memory. Every merge runs in a fixed
 // order, so results do not depend on timing.
-template <int D, int NT, bool BF16, bool RAGGED>
-__global__ void __launch_bounds__(kReduceWarps * 32) paged_decode_reduce_kernel(const DecodeParams p)
+template <int D, int NT, bool BF16, bool RAGGED, int W>
+__global__ void __launch_bounds__(W * 32) paged_decode_reduce_kernel(const DecodeParams p)
 {
     constexpr int NG = merge_groups<NT, RAGGED>(), CN = NT / NG, GP = CN * 8, KD = D / 32, PART = 2 * GP + GP * D;
-    extern __shared__ float s_part[];  // [kReduceWarps][M GP | l GP | O GP x D]
-    __shared__ int4 s_task[kReduceWarps];
+    extern __shared__ float s_part[];  // [W][M GP | l GP | O GP x D]
+    __shared__ int4 s_task[W];
 
     grid_dependency_wait();  // the main grid's records and tasks are complete
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int w = (blockIdx.x * kReduceWarps + warp) / NG;
-    const int c0 = NG == 1 ? 0 : ((blockIdx.x * kReduceWarps + warp) % NG) * GP;  // this warp's columns
+    const int w = (blockIdx.x * W + warp) / NG;
+    const int c0 = NG == 1 ? 0 : ((blockIdx.x * W + warp) % NG) * GP;  // this warp's columns
     const int tq = p.tile_q;
     const int segs_per_seq = p.num_kv_heads * p.qtiles;
     uint16_t *out_base = static_cast<uint16_t *>(p.out);
@@ -1192,15 +1202,15 @@ __global__ void __launch_bounds__(kReduceWarps * 32) paged_decode_reduce_kernel(
     }
     __syncthreads();
     // Tasks with many pieces: the whole CTA, pieces split across warps.
-    for (int j = 0; j < kReduceWarps; ++j) {
+    for (int j = 0; j < W; ++j) {
         const int4 t = s_task[j];
         if (t.x < 0)
             continue;
-        const int last = (blockIdx.x * kReduceWarps + j) / NG;
-        const int cj = NG == 1 ? 0 : ((blockIdx.x * kReduceWarps + j) % NG) * GP;
+        const int last = (blockIdx.x * W + j) / NG;
+        const int cj = NG == 1 ? 0 : ((blockIdx.x * W + j) % NG) * GP;
         MergeState<D, CN> st;
         st.clear();
-        fold_pieces<D, NT, CN>(p.warp_records, t.y + warp, kReduceWarps, last, t.y, t.z, tq, cj, st);
+        fold_pieces<D, NT, CN>(p.warp_records, t.y + warp, W, last, t.y, t.z, tq, cj, st);
         float *mine = s_part + warp * PART;
 #pragma unroll
         for (int c = 0; c < GP; ++c) {
@@ -1215,16 +1225,16 @@ __global__ void __launch_bounds__(kReduceWarps * 32) paged_decode_reduce_kernel(
         __syncthreads();
         // Combine the warps' states (fixed order), elements across the CTA.
         const OutRows o = out_rows(t.x);
-        for (int e = threadIdx.x; e < min(tq - cj, GP) * D; e += kReduceWarps * 32) {
+        for (int e = threadIdx.x; e < min(tq - cj, GP) * D; e += W * 32) {
             const int c = e / D, d = e - (e / D) * D;
             uint16_t *out = out_row(o, cj + c);
             if (!out)
                 continue;
             float Mx = -INFINITY;
-            for (int v = 0; v < kReduceWarps; ++v)
+            for (int v = 0; v < W; ++v)
                 Mx = fmaxf(Mx, s_part[v * PART + c]);
             float lt = 0.f, ot = 0.f;
-            for (int v = 0; v < kReduceWarps; ++v) {
+            for (int v = 0; v < W; ++v) {
                 const float *pv = s_part + v * PART;
                 const float f = pv[c] == -INFINITY ? 0.f : ex2(pv[c] - Mx);  // warp had no pieces
                 lt += f * pv[GP + c];
@@ -1507,6 +1517,9 @@ struct DecodePlan {
     const void *reduce_fn = nullptr;
     size_t reduce_smem = 0;
     int merge_groups = 1;  // merge warps per main-grid warp
+    int reduce_warps = 0;  // per merge CTA
+    const void *many_fn = nullptr;  // ragged: the merge for segments of many pieces
+    size_t many_smem = 0;
     size_t total() const { return prefix_bytes + task_bytes + warp_record_bytes; }
 };
 
@@ -1515,9 +1528,14 @@ void pick_kernels(DecodePlan &pl, int num_seqs)
 {
     pl.main_fn = reinterpret_cast<const void *>(&paged_decode_kernel<D, NT, BF16, FP8, RAGGED>);
     pl.warps = decode_warps<D, NT, FP8, RAGGED>();
-    pl.reduce_fn = reinterpret_cast<const void *>(&paged_decode_reduce_kernel<D, NT, BF16, RAGGED>);
-    pl.reduce_smem = reduce_smem_bytes<D, NT, RAGGED>();
+    pl.reduce_fn = reinterpret_cast<const void *>(&paged_decode_reduce_kernel<D, NT, BF16, RAGGED, kMergeWarps>);
+    pl.reduce_smem = reduce_smem_bytes<D, NT, RAGGED, kMergeWarps>();
+    pl.reduce_warps = kMergeWarps;
     pl.merge_groups = merge_groups<NT, RAGGED>();
+    if constexpr (RAGGED) {
+        pl.many_fn = reinterpret_cast<const void *>(&paged_decode_reduce_kernel<D, NT, BF16, RAGGED, kMergeWarpsMany>);
+        pl.many_smem = reduce_smem_bytes<D, NT, RAGGED, kMergeWarpsMany>();
+    }
     pl.smem = decode_smem_bytes<D, NT, FP8, RAGGED>(num_seqs);
 }
 
@@ -1575,7 +1593,7 @@ cudaError_t kernel_setup(const void *fn, int dev, size_t smem, int threads, int 
         size_t allowed, occ_smem;
         int occ;
     };
-    constexpr int kEntries = 64;
+    constexpr int kEntries = 128;
     static Entry table[kEntries];
     static int used = 0;
     static std::mutex mu;
@@ -1628,13 +1646,21 @@ int make_plan(DecodePlan &pl, int num_seqs, int num_q_heads, int num_kv_heads, i
     e = kernel_setup(pl.main_fn, dev, pl.smem, pl.warps * 32, &occ);
     if (e != cudaSuccess)
         return cuda_fail(e, "pa_decode: kernel attributes / occupancy");
-    e = kernel_setup(pl.reduce_fn, dev, pl.reduce_smem, kReduceWarps * 32, nullptr);
+    e = kernel_setup(pl.reduce_fn, dev, pl.reduce_smem, pl.reduce_warps * 32, nullptr);
     if (e != cudaSuccess)
         return cuda_fail(e, "pa_decode: reduce kernel attributes");
     if (occ < 1)
         return set_error(PA_ERR_UNSUPPORTED, "pa_decode: kernel does not fit on an SM (smem %zu)", pl.smem);
     pl.grid = sms * occ;
     pl.total_warps = pl.grid * pl.warps;
+    if (pl.many_fn && (long long)num_seqs * num_kv_heads * pl.qtiles * kManyPieces <= pl.total_warps) {
+        pl.reduce_fn = pl.many_fn;
+        pl.reduce_smem = pl.many_smem;
+        pl.reduce_warps = kMergeWarpsMany;
+        e = kernel_setup(pl.reduce_fn, dev, pl.reduce_smem, pl.reduce_warps * 32, nullptr);
+        if (e != cudaSuccess)
+            return cuda_fail(e, "pa_decode: merge kernel attributes");
+    }
     const size_t rec = (size_t)pl.nt * 8 * (head_size + 2) * sizeof(float);
     pl.prefix_bytes = ((size_t)(num_seqs + 1) * sizeof(long long) + 255) / 256 * 256;
     pl.task_bytes = ((size_t)pl.total_warps * sizeof(int4) + 255) / 256 * 256;
@@ -1722,8 +1748,8 @@ int launch_decode(const char *fn, void *out, const void *query, const void *kv_c
     if (e != cudaSuccess)
         return set_error(PA_ERR_CUDA, "%s: main kernel launch: %s", fn, cudaGetErrorString(e));
     void *red_args[] = {&prm};
-    e = launch_pdl(pl.reduce_fn, dim3((pl.total_warps * pl.merge_groups + kReduceWarps - 1) / kReduceWarps),
-                   dim3(kReduceWarps * 32), red_args, pl.reduce_smem, s);
+    e = launch_pdl(pl.reduce_fn, dim3((pl.total_warps * pl.merge_groups + pl.reduce_warps - 1) / pl.reduce_warps),
+                   dim3(pl.reduce_warps * 32), red_args, pl.reduce_smem, s);
     if (e != cudaSuccess)
         return set_error(PA_ERR_CUDA, "%s: reduce kernel launch: %s", fn, cudaGetErrorString(e));
     return PA_OK;
