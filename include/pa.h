@@ -420,7 +420,9 @@ int pa_copy_blocks(void *const *kv_caches, int num_layers,
  * returns blocks. A block id outside the pool that is taken or found in a
  * table sets PA_DEVERR_BLOCK_ID; its tokens' slots are -1. A free count
  * outside [0, num_blocks], or blocks returned beyond num_blocks in all, set
- * PA_DEVERR_BLOCK_ID too, and the count is held to that range. One launch;
+ * PA_DEVERR_BLOCK_ID too, and the count is held to that range. It writes
+ * lengths: a pa_decode enqueued right behind it must not claim
+ * PA_DECODE_LENS_READY (behind a kernel in between it may). One launch;
  * reads only what earlier work on the stream has written. Deterministic.
  * Returns PA_OK or a PA_ERR_* code.
  */
@@ -510,8 +512,13 @@ int pa_rope_and_cache_fp8(void *query_out, const void *query, const void *key, c
  *   kv_lens        device, [num_seqs] int32, in [0, max_blocks_per_seq *
  *                  block_size], longer or shorter than the queries
  *   workspace      device, NULL or >= pa_cross_attention_workspace_size(...)
- *                  bytes, 256-byte aligned, under pa_prefill's rules. NULL:
- *                  the K/V ranges stay whole (same result up to fp32 rounding).
+ *                  bytes for this shape, 256-byte aligned: split K/V ranges'
+ *                  partial results, or with many work units their counter. Its
+ *                  contents need no initialisation and are not preserved; calls
+ *                  that share it must not overlap on the GPU. NULL: K/V ranges
+ *                  stay whole and work is dealt out in a fixed order (same
+ *                  result up to fp32 rounding, slower). Too small or misaligned:
+ *                  PA_ERR_WORKSPACE.
  *   flags          0 or PA_DECODE_SHARED_BLOCKS (tables share blocks)
  * Bad offsets, lengths and block ids are handled as pa_prefill handles them
  * (PA_DEVERR_SEQ_LEN, rows not written; PA_DEVERR_BLOCK_ID, read as zeros).
@@ -540,9 +547,9 @@ int pa_cross_attention_fp8(void *out, const void *query, const void *kv_cache,
                            pa_stream_t stream);
 
 /*
- * pa_cross_attention_workspace_size — bytes of workspace with which the cross
- * attention calls split this shape's K/V ranges on the current device; 0 when
- * they would not. cache_dtype: dtype, or PA_FP8_E4M3 for
+ * pa_cross_attention_workspace_size — bytes of workspace the cross attention
+ * calls want for this shape on the current device (0 only for an empty one).
+ * A larger one serves too. cache_dtype: dtype, or PA_FP8_E4M3 for
  * pa_cross_attention_fp8. Writes *bytes.
  */
 int pa_cross_attention_workspace_size(int num_seqs, int max_seqlen_q, int num_q_heads,

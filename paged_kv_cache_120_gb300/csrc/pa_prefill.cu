@@ -409,6 +409,7 @@ struct PrefillParams {
     float scale_log2;   // scale * log2(e) (* k_scale with an FP8 cache)
     float v_scale;      // 1, or the FP8 cache's V scale
     int cross;          // 1: every query sees all L cached tokens (cross attention); 0: causally
+    int *counter;       // cross, whole units: the next unit, in the caller's workspace (null: dealt out in turn)
 };
 
 // One work unit: the two adjacent query tiles A = 2 qp and B = 2 qp + 1 of
@@ -723,7 +724,8 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
             }
         }
         if (lane == 0) {
-            int* next = &g_prefill_sched[p.sched_slot][0];
+            int *next = p.cross ? p.counter : &g_prefill_sched[p.sched_slot][0];
+            int dealt = blockIdx.x;
             // Stream-K walk: unit (ws, hh, qr) holds tiles [Tu, Tu + nu).
             int hh = 0, qr = 0, wq_len = 0, wL = 0, nu = 0;
             bool wok = false;
@@ -789,7 +791,8 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                 } else {
                     int u;
                     do {
-                        u = atomicAdd(next, 1);
+                        u = p.cross && !p.counter ? dealt : atomicAdd(next, 1);
+                        dealt += gridDim.x;
                     } while (u < p.num_units && !unit_of<false>(p, u, w, true));
                     if (u < p.num_units) {
                         it.u = u;
@@ -1485,7 +1488,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
     // Every role has left its loop, so this CTA takes no more units; the
     // last CTA to get here resets the launch's counters for the next use
     // (a stream-K launch uses none).
-    if (!SPLIT && tid == 0) {
+    if (!SPLIT && tid == 0 && !p.cross) {
         __threadfence();
         if (atomicAdd(&g_prefill_sched[p.sched_slot][1], 1) == (int)gridDim.x - 1) {
             g_prefill_sched[p.sched_slot][0] = 0;
@@ -1734,6 +1737,7 @@ namespace {
 // one CTA per SM, however many pieces that cuts a unit into (the merge
 // spreads a unit's pieces over several threads per row).
 constexpr int kSplitUnitsPerSm = 4;
+constexpr size_t kCounterBytes = 256;  // cross attention's workspace for its unit counter
 
 struct LaunchPlan {
     int heads_per_cta, head_tiles, rows_per_head, q_pairs;
@@ -1901,15 +1905,21 @@ int prefill_impl(const char *who, void *out, const void *query, const void *kv_c
     prm.scale_log2 = scale * 1.4426950408889634f * (fp8 ? k_scale : 1.f);
     prm.v_scale = fp8 ? v_scale : 1.f;
     prm.cross = cross ? 1 : 0;
+    prm.counter = cross && !split ? static_cast<int *>(workspace) : nullptr;
     prm.num_kv_heads = num_kv_heads;
     prm.num_units = (int)lp.units;
+    if (cross && !split && workspace &&
+        (workspace_bytes < kCounterBytes || (reinterpret_cast<uintptr_t>(workspace) & 255)))
+        return set_error(PA_ERR_WORKSPACE, "%s: workspace of %zu bytes at %p (need %zu, 256-byte aligned)", who,
+                         workspace_bytes, workspace, kCounterBytes);
     prm.part_o = split ? static_cast<float *>(workspace) : nullptr;
     prm.part_ml = split ? reinterpret_cast<float2 *>(static_cast<float *>(workspace) +
                                                      (size_t)lp.split_grid * 2 * 2 * kM * head_size)
                         : nullptr;
     prm.jobs = split ? reinterpret_cast<int4 *>(prm.part_ml + (size_t)lp.split_grid * 2 * 2 * kM) : nullptr;
+    // Prefill's counters live in the library, a slot per launch in turn.
     static std::atomic<unsigned> launches{0};
-    prm.sched_slot = (int)(launches.fetch_add(1u) % (unsigned)kSchedSlots);
+    prm.sched_slot = cross ? 0 : (int)(launches.fetch_add(1u) % (unsigned)kSchedSlots);
 
     CUtensorMap kv_map, q_map;
     rc = fp8 ? encode_kv_map_fp8(&kv_map, kv_cache, num_blocks, block_size, num_kv_heads, head_size)
@@ -1957,6 +1967,11 @@ int prefill_impl(const char *who, void *out, const void *query, const void *kv_c
     // Persistent grid: one CTA per SM (the CTA holds 225 KB of shared
     // memory), never more CTAs than units; G CTAs under stream-K.
     const dim3 grid(split ? (unsigned)lp.split_grid : (unsigned)std::min<long long>(lp.units, sms));
+    if (prm.counter) {
+        e = cudaMemsetAsync(prm.counter, 0, sizeof(int), reinterpret_cast<cudaStream_t>(stream));
+        if (e != cudaSuccess)
+            return set_error(PA_ERR_CUDA, "%s: unit counter: %s", who, cudaGetErrorString(e));
+    }
     void *args[] = {&kv_map, &q_map, &prm};
     e = cudaLaunchKernel(fn, grid, dim3(threads_for(fp8)), args, kSmemBytes, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess)
@@ -2114,5 +2129,8 @@ extern "C" int pa_cross_attention_workspace_size(int num_seqs, int max_seqlen_q,
     if (num_seqs > 0 && max_seqlen_q > 0 && cross_rows_fit(num_seqs, max_seqlen_q, num_q_heads, num_kv_heads, block_size))
         return cross_rows_workspace(num_seqs, max_seqlen_q, num_q_heads, num_kv_heads, head_size, dtype,
                                     cache_dtype == PA_FP8_E4M3, bytes);
-    return pa_prefill_workspace_size(num_seqs, max_seqlen_q, num_q_heads, num_kv_heads, head_size, bytes);
+    const int rc2 = pa_prefill_workspace_size(num_seqs, max_seqlen_q, num_q_heads, num_kv_heads, head_size, bytes);
+    if (rc2 == PA_OK && num_seqs > 0 && max_seqlen_q > 0)
+        *bytes = std::max(*bytes, kCounterBytes);
+    return rc2;
 }

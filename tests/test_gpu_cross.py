@@ -346,3 +346,48 @@ def test_a_pool_past_2_to_the_32_bytes(dev):
     c.pool = pool
     c.bt_d.copy_(torch.from_numpy(np.where(c.bt >= 0, move.cpu().numpy()[c.bt], -1)))
     c.both()
+
+
+def test_two_graphs_at_once_share_nothing(dev):
+    """Two captured calls of many work units each, replayed on two streams at once, over and over: each takes its units
+    from its own workspace."""
+    import torch
+    rng = np.random.default_rng(19)
+    cases = [CrossCase(dev, workloads.F16, 8, 8, 64, rng.integers(100, 400, 60), rng.integers(1, 600, 60), seed=20 + k)
+             for k in range(2)]
+    outs = [torch.full_like(c.q, float("nan")) for c in cases]
+    ws = [c.workspace() for c in cases]
+    graphs, streams = [torch.cuda.CUDAGraph() for _ in cases], [torch.cuda.Stream() for _ in cases]
+    for c, w, o in zip(cases, ws, outs):
+        c.run(w, out=o)
+    torch.cuda.synchronize()
+    for c, w, o, g in zip(cases, ws, outs, graphs):
+        with torch.cuda.graph(g, capture_error_mode="relaxed"):
+            for _ in range(40):
+                c.run(w, out=o)
+    for o in outs:
+        o.fill_(float("nan"))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for c, o in zip(cases, outs):
+        c.check(o)
+
+
+def test_workspace_rules(dev):
+    """The size asked for serves; less, or a misaligned one, is refused, whichever form the shape takes."""
+    import torch
+    for qlen, kv in (([1, 1], [100, 200]), ([40, 30], [100, 200]), ([400] * 130, [64] * 130)):
+        c = CrossCase(dev, workloads.F16, 8, 2 if len(qlen) == 2 else 8, 64, qlen, kv, seed=25)
+        n = binding.pa_cross_attention_workspace_size(len(qlen), c.max_q, c.hq, c.hkv, 64, 16, binding.PA_F16, binding.PA_F16)
+        big = torch.empty(n + 512, dtype=torch.uint8, device=dev)
+        c.check(c.run(big[:n]))
+        c.check(c.run(big))
+        for bad in (big[:n - 128], big[16:16 + n]):
+            with pytest.raises(binding.PAError) as e:
+                c.run(bad)
+            assert e.value.code == binding.PA_ERR_WORKSPACE
+    assert binding.pa_get_device_error() == 0
