@@ -43,7 +43,7 @@ namespace {
 
 constexpr int kRopeWarps = 8;                         // that turn and store
 constexpr int kRopeThreads = 32 * (kRopeWarps + 2);   // and one that copies, one for the sines
-constexpr int kRopeMaxStages = 8;
+constexpr int kRopeMaxStages = 8, kRopeMaxTokens = 8;  // of the ring, of a unit
 // A unit's rows at most (but a group of heads at least), and a CTA's ring, two
 // CTAs an SM: about 80 KB of rows in flight an SM. Both less and more is
 // slower: the units in flight are the stretch of memory that is read and
@@ -65,9 +65,9 @@ struct RopeParams {
     long long pos_stride;                                  // entries per axis
     long long num_slots;
     int num_tokens, num_q_heads, num_kv_heads, head_vecs, rot_vecs, num_axes;
-    long long units;  // num_tokens * units_per_token
-    int units_per_token, heads_per_unit;
-    int stages, stage_bytes, sines_at;  // a stage: the unit's rows, then cosines and sines of rot / 2 pairs
+    int units;
+    int parts, tokens_per_unit, heads_per_unit;  // units a token, or tokens a unit
+    int stages, stage_bytes, sines_at;  // a stage: the unit's rows, then each token's rot / 2 cosines and sines
     float k_scale, v_scale, k_inv, v_inv;  // inv: 1 / scale, 0 where quotients are to be divided
 };
 
@@ -186,21 +186,22 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
 
 struct RopeBars {
     uint64_t full[kRopeMaxStages], empty[kRopeMaxStages];
-    long long slot[kRopeMaxStages];
-    int token[kRopeMaxStages], first[kRopeMaxStages], count[kRopeMaxStages];  // heads first .. first + count - 1
+    int slot[kRopeMaxStages][kRopeMaxTokens];  // of the unit's tokens, -1 where no K and V are written
 };
 
-// Persistent CTAs over units: a unit is a token, or heads_per_unit of its
-// heads (q, then k, then v heads, counted through). One warp brings the units'
-// rows into a ring of shared-memory stages by bulk copies, so that the bytes
-// in flight do not depend on registers; another computes each unit's sines
-// into its stage meanwhile; the others turn the heads and store.
+// Persistent CTAs over units: a unit is a few tokens, a token, or
+// heads_per_unit of its heads (q, then k, then v heads, counted through). One
+// warp brings the units' rows into a ring of shared-memory stages by bulk
+// copies, so that the bytes in flight do not depend on registers; another
+// computes the tokens' sines into the stage meanwhile; the others turn the
+// heads and store.
 //
 // A lane of those holds one place of a head: 16 bytes of it (adjacent pairs),
 // or two times 16 bytes that lie rot / 2 apart, or of the dimensions that
 // pass; `per` lanes a head and 32 / per heads side by side make a group, and
 // the warps take the groups of all units in turn.
-template <bool BF16, bool FP8, bool ADJ>
+// MANY: several tokens a unit.
+template <bool BF16, bool FP8, bool ADJ, bool MANY>
 __global__ void __launch_bounds__(kRopeThreads, 2) rope_and_cache_kernel(const RopeParams p)
 {
     constexpr int kPairs = ADJ ? 4 : 8;  // of a lane
@@ -224,41 +225,79 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_and_cache_kernel(const R
     grid_launch_dependents();
 
     const int hv = p.head_vecs, rv = p.rot_vecs, hq = p.num_q_heads, hk = hq + p.num_kv_heads, heads = hk + p.num_kv_heads;
-    const int pairs = rv * 4;
-    auto token_of = [&](long long u) { return (int)(p.units_per_token == 1 ? u : u / p.units_per_token); };
+    const int pairs = rv * 4, tokens = MANY ? p.tokens_per_unit : 1;
+    // Unit u: tokens t0 .. t0 + tokens - 1 (those below num_tokens), heads from h0 on.
+    auto unit_at = [&](int u, int &t0, int &h0) {
+        const int k = p.parts == 1 ? u : u / p.parts;
+        t0 = k * tokens;
+        h0 = (u - k * p.parts) * p.heads_per_unit;
+    };
+    const int grid = gridDim.x;
+    // From a unit to this CTA's next without a division.
+    const int t_step = (p.parts == 1 ? grid : grid / p.parts) * tokens, h_step = (p.parts == 1 ? 0 : grid % p.parts) * p.heads_per_unit;
+    const int h_end = p.parts * p.heads_per_unit;
+    auto next_unit = [&](int &t0, int &h0) {
+        t0 += t_step;
+        h0 += h_step;
+        if (h0 >= h_end) {
+            h0 -= h_end;
+            t0 += tokens;
+        }
+    };
+    const int window = 32 / tokens;  // units whose tokens' indexes a warp loads at a time, a token a lane
     if (warp == kRopeWarps) {
         // ---------------------------------------------------------- copies
-        long long slots = -1;  // of this CTA's units ahead, one a lane
+        // The slot of this lane's token in the window of units from u on.
+        auto window_slot = [&](int u) {
+            const int mine = u + (lane / tokens) * grid;
+            if (lane >= window * tokens || mine >= p.units)
+                return -1;
+            int t0, h0;
+            unit_at(mine, t0, h0);
+            const int t = t0 + lane % tokens;
+            return t < p.num_tokens ? p.slots[t] : -1;
+        };
+        int slot = -1, slot_next = window_slot(blockIdx.x);
         int st = 0, ahead = 0;
         uint32_t used = 0;  // rounds of the ring behind this stage
-        for (long long u = blockIdx.x; u < p.units; u += gridDim.x) {
+        int t0, h0;
+        unit_at(blockIdx.x, t0, h0);
+        for (int u = blockIdx.x; u < p.units; u += grid, next_unit(t0, h0)) {
             if (ahead == 0) {
-                const long long mine = u + (long long)lane * gridDim.x;
-                if (mine < p.units)
-                    slots = p.slots[token_of(mine)];
+                slot = slot_next;
+                slot_next = window_slot(u + window * grid);
+                if (slot >= p.num_slots) {
+                    rope_raise(PA_DEVERR_SLOT);
+                    slot = -1;
+                }
             }
-            const int t = token_of(u), h0 = (int)(u - (long long)t * p.units_per_token) * p.heads_per_unit;
-            const long long slot = __shfl_sync(kFull, slots, ahead);
-            const bool write = slot >= 0 && slot < p.num_slots;
-            const int h1 = min(h0 + p.heads_per_unit, write ? heads : hq), n = max(h1 - h0, 0);
+            const int j = lane - ahead * tokens;  // this lane's token of the unit
+            const bool mine = j >= 0 && j < tokens && t0 + j < p.num_tokens;
+            const int h1 = min(h0 + p.heads_per_unit, slot >= 0 ? heads : hq), n = mine ? max(h1 - h0, 0) : 0;
             const uint32_t full = smem_addr(&bars.full[st]), data = base + st * p.stage_bytes;
             if (used > 0 && !__all_sync(kFull, mbar_wait(smem_addr(&bars.empty[st]), (used - 1) & 1))) {
                 if (lane == 0)
                     rope_raise(PA_DEVERR_TIMEOUT);
                 return;  // the other warps wait (bounded) for what is in flight
             }
-            if (lane == 0) {
-                if (slot >= p.num_slots && h0 == 0)
-                    rope_raise(PA_DEVERR_SLOT);
-                bars.slot[st] = slot;
-                bars.token[st] = t;
-                bars.first[st] = h0;
-                bars.count[st] = n;
+            uint32_t bytes = (uint32_t)(n * hv) * 16u;
+            if (j >= 0 && j < tokens)
+                bars.slot[st][j] = slot;
+            if constexpr (MANY) {
+                __syncwarp();
+                bytes = __reduce_add_sync(kFull, bytes);
+            }
+            if (j == 0)
+                mbar_expect_tx(full, bytes);
+            if constexpr (MANY)
+                __syncwarp();
+            if (n > 0) {
                 fence_proxy_async();  // the stage's last reads, before it is written again
-                mbar_expect_tx(full, (uint32_t)(n * hv) * 16u);
+                const int t = t0 + j;
+                const uint32_t row_at = data + (uint32_t)(j * p.heads_per_unit * hv) * 16u;
                 auto load = [&](const void *row, long long stride, int a, int b, int from) {  // heads [a, b) of the unit's
                     if (a < b)
-                        bulk_load(data + (uint32_t)((a - h0) * hv) * 16u,
+                        bulk_load(row_at + (uint32_t)((a - h0) * hv) * 16u,
                                   static_cast<const uint4 *>(row) + t * stride + (long long)(a - from) * hv,
                                   (uint32_t)((b - a) * hv) * 16u, full);
                 };
@@ -267,7 +306,8 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_and_cache_kernel(const R
                 load(p.v, p.v_stride, max(h0, hk), h1, hk);
             }
             __syncwarp();
-            ahead = (ahead + 1) & 31;
+            if (++ahead == window)
+                ahead = 0;
             if (++st == p.stages) {
                 st = 0;
                 ++used;
@@ -281,44 +321,56 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_and_cache_kernel(const R
 #pragma unroll
         for (int k = 0; k < kRopeMaxDims / 64; ++k)
             words[k] = lane + 32 * k < pairs ? p.plan[lane + 32 * k] : 0;
-        int pos[kRopeMaxAxes] = {0, 0, 0, 0};  // of this CTA's units ahead, one a lane
-        int st = 0, ahead = 0;
-        uint32_t used = 0;
-        for (long long u = blockIdx.x; u < p.units; u += gridDim.x) {
-            if (ahead == 0) {
-                const long long mine = u + (long long)lane * gridDim.x;
-                if (mine < p.units) {
-                    const int t = token_of(mine);
-#pragma unroll
-                    for (int a = 0; a < kRopeMaxAxes; ++a)
-                        if (a < p.num_axes)
-                            pos[a] = p.positions[a * p.pos_stride + t];
-                }
-            }
-            int at[kRopeMaxAxes];
+        int pos[kRopeMaxAxes], pos_next[kRopeMaxAxes] = {0, 0, 0, 0};  // as the slots above
+        auto window_pos = [&](int u) {
+            const int mine = u + (lane / tokens) * grid;
+            if (lane >= window * tokens || mine >= p.units)
+                return;
+            int t0, h0;
+            unit_at(mine, t0, h0);
+            const int t = t0 + lane % tokens;
 #pragma unroll
             for (int a = 0; a < kRopeMaxAxes; ++a)
-                at[a] = __shfl_sync(kFull, pos[a], ahead);
+                if (a < p.num_axes && t < p.num_tokens)
+                    pos_next[a] = p.positions[a * p.pos_stride + t];
+        };
+        window_pos(blockIdx.x);
+        int st = 0, ahead = 0;
+        uint32_t used = 0;
+        for (int u = blockIdx.x; u < p.units; u += grid) {
+            if (ahead == 0) {
+#pragma unroll
+                for (int a = 0; a < kRopeMaxAxes; ++a)
+                    pos[a] = pos_next[a];
+                window_pos(u + window * grid);
+            }
             if (used > 0 && !__all_sync(kFull, mbar_wait(smem_addr(&bars.empty[st]), (used - 1) & 1))) {
                 if (lane == 0)
                     rope_raise(PA_DEVERR_TIMEOUT);
                 return;
             }
             float *cs = reinterpret_cast<float *>(rope_smem + st * p.stage_bytes + p.sines_at), *sn = cs + pairs;
+            for (int j = 0; j < tokens; ++j, cs += 2 * pairs, sn += 2 * pairs) {
+                int at[kRopeMaxAxes];
 #pragma unroll
-            for (int k = 0; k < kRopeMaxDims / 64; ++k) {
-                const int e = lane + 32 * k;
-                if (e < pairs) {
-                    const int axis = min((int)(words[k] & 3u), p.num_axes - 1);
-                    const long long x = axis == 0 ? at[0] : axis == 1 ? at[1] : axis == 2 ? at[2] : at[3];
-                    const uint64_t turn = (uint64_t)x * (words[k] & ~3ull);
-                    sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, sn + e, cs + e);
+                for (int a = 0; a < kRopeMaxAxes; ++a)
+                    at[a] = __shfl_sync(kFull, pos[a], ahead * tokens + j);
+#pragma unroll
+                for (int k = 0; k < kRopeMaxDims / 64; ++k) {
+                    const int e = lane + 32 * k;
+                    if (e < pairs) {
+                        const int axis = min((int)(words[k] & 3u), p.num_axes - 1);
+                        const long long x = axis == 0 ? at[0] : axis == 1 ? at[1] : axis == 2 ? at[2] : at[3];
+                        const uint64_t turn = (uint64_t)x * (words[k] & ~3ull);
+                        sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, sn + e, cs + e);
+                    }
                 }
             }
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(smem_addr(&bars.full[st]));
-            ahead = (ahead + 1) & 31;
+            if (++ahead == window)
+                ahead = 0;
             if (++st == p.stages) {
                 st = 0;
                 ++used;
@@ -337,85 +389,90 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_and_cache_kernel(const R
     int next = warp;  // this warp's next group, counted from the unit's first
     int st = 0;
     uint32_t phase = 0;
-    for (long long un = blockIdx.x; un < p.units; un += gridDim.x) {
+    int t0, first;
+    unit_at(blockIdx.x, t0, first);
+    for (int un = blockIdx.x; un < p.units; un += grid, next_unit(t0, first)) {
         if (!__all_sync(kFull, mbar_wait(smem_addr(&bars.full[st]), phase))) {
             if (lane == 0)
                 rope_raise(PA_DEVERR_TIMEOUT);
             return;
         }
-        const long long slot = bars.slot[st];
-        const int t = bars.token[st], first = bars.first[st], n = bars.count[st];
-        const uint32_t data = base + st * p.stage_bytes, sines = data + p.sines_at;
-        uint4 *q_out = static_cast<uint4 *>(p.q_out) + t * p.q_out_stride;
-        Out *k_out = static_cast<Out *>(p.kv) + slot * kv_row, *v_out = k_out + p.num_slots * kv_row;
-        const int across = (n + side - 1) / side, groups = across * segs;
-        for (; next < groups; next += kRopeWarps) {
-            const int seg = segs == 1 ? 0 : next / across;
-            const int h = (next - seg * across) * side + h_in;  // of the unit
-            const int u = seg * 32 + in;
-            if (h_in >= side || h >= n || u >= places)
-                continue;
-            const bool turns = u < turning;
-            const int v0 = turns ? u : rv + (u - turning), v1 = turns ? turning + u : v0 + passing;
-            const bool two = !ADJ && v1 < hv;  // the second may be missing among those that pass
-            const int head = first + h;
-            const bool turn = turns && head < hk, code = FP8 && head >= hq;
-            uint4 a[kVecs];
-            a[0] = lds128(data + (uint32_t)(h * hv + v0) * 16u);
-            if constexpr (!ADJ)
-                a[1] = two ? lds128(data + (uint32_t)(h * hv + v1) * 16u) : make_uint4(0u, 0u, 0u, 0u);
-            if (code) {  // codes8 takes negated values
+        const int count = min(p.heads_per_unit, heads - first);  // heads of the unit
+        const int across = (count + side - 1) / side, groups = across * segs;  // of a token
+        for (int j = 0; j < tokens; ++j, next -= groups) {  // next stays this warp's turn from token to token
+            const int t = t0 + j, slot = bars.slot[st][j];
+            const int n = t < p.num_tokens ? min(count, (slot >= 0 ? heads : hq) - first) : 0;
+            const uint32_t data = base + st * p.stage_bytes + (uint32_t)(j * p.heads_per_unit * hv) * 16u;
+            const uint32_t sines = base + st * p.stage_bytes + p.sines_at + (uint32_t)(j * pairs) * 8u;
+            uint4 *q_out = static_cast<uint4 *>(p.q_out) + t * p.q_out_stride;
+            Out *k_out = static_cast<Out *>(p.kv) + slot * kv_row, *v_out = k_out + p.num_slots * kv_row;
+            for (; next < groups; next += kRopeWarps) {
+                const int seg = segs == 1 ? 0 : next / across;
+                const int h = (next - seg * across) * side + h_in;  // of the unit
+                const int u = seg * 32 + in;
+                if (h_in >= side || h >= n || u >= places)
+                    continue;
+                const bool turns = u < turning;
+                const int v0 = turns ? u : rv + (u - turning), v1 = turns ? turning + u : v0 + passing;
+                const bool two = !ADJ && v1 < hv;  // the second may be missing among those that pass
+                const int head = first + h;
+                const bool turn = turns && head < hk, code = FP8 && head >= hq;
+                uint4 a[kVecs];
+                a[0] = lds128(data + (uint32_t)(h * hv + v0) * 16u);
+                if constexpr (!ADJ)
+                    a[1] = two ? lds128(data + (uint32_t)(h * hv + v1) * 16u) : make_uint4(0u, 0u, 0u, 0u);
+                if (code) {  // codes8 takes negated values
+#pragma unroll
+                    for (int c = 0; c < kVecs; ++c)
+                        a[c] = negated(a[c]);
+                }
+                F8 y[kVecs];
 #pragma unroll
                 for (int c = 0; c < kVecs; ++c)
-                    a[c] = negated(a[c]);
-            }
-            F8 y[kVecs];
+                    y[c] = unpack8<BF16>(a[c]);
+                if (turn) {
+                    float cs[kPairs], sn[kPairs];
 #pragma unroll
-            for (int c = 0; c < kVecs; ++c)
-                y[c] = unpack8<BF16>(a[c]);
-            if (turn) {
-                float cs[kPairs], sn[kPairs];
+                    for (int e = 0; e < kPairs; e += 4) {
+                        const uint4 c4 = lds128(sines + (uint32_t)(u * kPairs + e) * 4u);
+                        const uint4 s4 = lds128(sines + (uint32_t)(pairs + u * kPairs + e) * 4u);
+                        const uint32_t cw[4] = {c4.x, c4.y, c4.z, c4.w}, sw[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
-                for (int e = 0; e < kPairs; e += 4) {
-                    const uint4 c4 = lds128(sines + (uint32_t)(u * kPairs + e) * 4u);
-                    const uint4 s4 = lds128(sines + (uint32_t)(pairs + u * kPairs + e) * 4u);
-                    const uint32_t cw[4] = {c4.x, c4.y, c4.z, c4.w}, sw[4] = {s4.x, s4.y, s4.z, s4.w};
+                        for (int f = 0; f < 4; ++f) {
+                            cs[e + f] = __uint_as_float(cw[f]);
+                            sn[e + f] = __uint_as_float(sw[f]);
+                        }
+                    }
 #pragma unroll
-                    for (int f = 0; f < 4; ++f) {
-                        cs[e + f] = __uint_as_float(cw[f]);
-                        sn[e + f] = __uint_as_float(sw[f]);
+                    for (int e = 0; e < 4; ++e) {
+                        if constexpr (ADJ) {
+                            // (x0, x1) (c, c) + (x1, x0) (-s, s)
+                            const float2 x = lanes(y[0].p[e]);
+                            y[0].p[e] = fma2(y[0].p[e], pair(cs[e], cs[e]), mul2(pair(x.y, x.x), pair(-sn[e], sn[e])));
+                        } else {
+                            const uint64_t x = y[0].p[e], z = y[1].p[e], c = pair(cs[2 * e], cs[2 * e + 1]);
+                            y[0].p[e] = fma2(x, c, mul2(z, pair(-sn[2 * e], -sn[2 * e + 1])));
+                            y[1].p[e] = fma2(z, c, mul2(x, pair(sn[2 * e], sn[2 * e + 1])));
+                        }
                     }
                 }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if constexpr (ADJ) {
-                        // (x0, x1) (c, c) + (x1, x0) (-s, s)
-                        const float2 x = lanes(y[0].p[e]);
-                        y[0].p[e] = fma2(y[0].p[e], pair(cs[e], cs[e]), mul2(pair(x.y, x.x), pair(-sn[e], sn[e])));
-                    } else {
-                        const uint64_t x = y[0].p[e], z = y[1].p[e], c = pair(cs[2 * e], cs[2 * e + 1]);
-                        y[0].p[e] = fma2(x, c, mul2(z, pair(-sn[2 * e], -sn[2 * e + 1])));
-                        y[1].p[e] = fma2(z, c, mul2(x, pair(sn[2 * e], sn[2 * e + 1])));
-                    }
+                const long long row = (long long)(head < hq ? head : head < hk ? head - hq : head - hk) * hv;
+                if (code) {
+                    uint2 *to = reinterpret_cast<uint2 *>((head < hk ? k_out : v_out) + row);
+                    const float scale = head < hk ? p.k_scale : p.v_scale, inv = head < hk ? p.k_inv : p.v_inv;
+                    to[v0] = codes8(y[0], scale, inv);
+                    if constexpr (!ADJ)
+                        if (two)
+                            to[v1] = codes8(y[1], scale, inv);
+                } else {
+                    uint4 *to = head < hq ? q_out + row : reinterpret_cast<uint4 *>((head < hk ? k_out : v_out) + row);
+                    to[v0] = turn ? pack8<BF16>(y[0]) : a[0];
+                    if constexpr (!ADJ)
+                        if (two)
+                            to[v1] = turn ? pack8<BF16>(y[1]) : a[1];
                 }
-            }
-            const long long row = (long long)(head < hq ? head : head < hk ? head - hq : head - hk) * hv;
-            if (code) {
-                uint2 *to = reinterpret_cast<uint2 *>((head < hk ? k_out : v_out) + row);
-                const float scale = head < hk ? p.k_scale : p.v_scale, inv = head < hk ? p.k_inv : p.v_inv;
-                to[v0] = codes8(y[0], scale, inv);
-                if constexpr (!ADJ)
-                    if (two)
-                        to[v1] = codes8(y[1], scale, inv);
-            } else {
-                uint4 *to = head < hq ? q_out + row : reinterpret_cast<uint4 *>((head < hk ? k_out : v_out) + row);
-                to[v0] = turn ? pack8<BF16>(y[0]) : a[0];
-                if constexpr (!ADJ)
-                    if (two)
-                        to[v1] = turn ? pack8<BF16>(y[1]) : a[1];
             }
         }
-        next -= groups;  // >= 0: this warp's turn in the next unit
         __syncwarp();
         if (lane == 0)
             mbar_arrive(smem_addr(&bars.empty[st]));
@@ -506,21 +563,22 @@ int rope_impl(const char *who, void *query_out, const void *query, const void *k
     auto inverse = [](float scale) { return scale >= 0x1p-64f && scale <= 0x1p64f ? 1.f / scale : 0.f; };
     prm.k_inv = inverse(k_scale);
     prm.v_inv = inverse(v_scale);
-    static const void *const kernels[8] = {
-        reinterpret_cast<const void *>(&rope_and_cache_kernel<false, false, false>),
-        reinterpret_cast<const void *>(&rope_and_cache_kernel<true, false, false>),
-        reinterpret_cast<const void *>(&rope_and_cache_kernel<false, true, false>),
-        reinterpret_cast<const void *>(&rope_and_cache_kernel<true, true, false>),
-        reinterpret_cast<const void *>(&rope_and_cache_kernel<false, false, true>),
-        reinterpret_cast<const void *>(&rope_and_cache_kernel<true, false, true>),
-        reinterpret_cast<const void *>(&rope_and_cache_kernel<false, true, true>),
-        reinterpret_cast<const void *>(&rope_and_cache_kernel<true, true, true>)};
+#define PA_ROPE_INSTANCES(ADJ, MANY)                                                \
+    reinterpret_cast<const void *>(&rope_and_cache_kernel<false, false, ADJ, MANY>),    \
+        reinterpret_cast<const void *>(&rope_and_cache_kernel<true, false, ADJ, MANY>), \
+        reinterpret_cast<const void *>(&rope_and_cache_kernel<false, true, ADJ, MANY>), \
+        reinterpret_cast<const void *>(&rope_and_cache_kernel<true, true, ADJ, MANY>)
+    static const void *const kernels[16] = {PA_ROPE_INSTANCES(false, false), PA_ROPE_INSTANCES(true, false),
+                                            PA_ROPE_INSTANCES(false, true), PA_ROPE_INSTANCES(true, true)};
+#undef PA_ROPE_INSTANCES
     int dev = 0, sms = 0;
     int rc = rope_device(who, &dev, &sms);
     if (rc != PA_OK)
         return rc;
     // Units: a token, in equal parts if its rows are longer than a unit's, or
-    // if there are too few tokens for the CTAs; not below a group for each warp.
+    // if there are too few tokens for the CTAs (not below a group for each
+    // warp); several tokens if they are short and there are plenty (measured
+    // at 64703 tokens of 16/4 heads of 64: 126 us one at a time, 98 us four).
     const int heads = num_q_heads + 2 * num_kv_heads, head_bytes = head_size * 2;
     const int vecs = adjacent ? 1 : 2, places = rot_dim / 8 / vecs + ((head_size - rot_dim) / 8 + vecs - 1) / vecs;
     const int side = places < 32 ? 32 / places : 1;
@@ -530,19 +588,26 @@ int rope_impl(const char *who, void *query_out, const void *query, const void *k
     parts = (int)std::min<long long>(std::max<long long>(parts, wanted), most);
     parts = std::min(parts, heads);
     prm.heads_per_unit = ((heads + parts - 1) / parts + side - 1) / side * side;
-    prm.units_per_token = (heads + prm.heads_per_unit - 1) / prm.heads_per_unit;
-    prm.units = (long long)num_tokens * prm.units_per_token;
-    prm.sines_at = prm.heads_per_unit * head_bytes;
-    prm.stage_bytes = (prm.sines_at + rot_dim * 4 + 127) & ~127;
+    prm.parts = (heads + prm.heads_per_unit - 1) / prm.heads_per_unit;
+    const int rows = prm.heads_per_unit * head_bytes, sines = rot_dim * 4;
+    prm.tokens_per_unit = 1;
+    if (prm.parts == 1)
+        prm.tokens_per_unit = std::max(1, std::min({kRopeMaxTokens, kRopeUnitBytes / rows, num_tokens / (8 * sms)}));
+    const long long units = ((long long)num_tokens + prm.tokens_per_unit - 1) / prm.tokens_per_unit * prm.parts;
+    if (units > (1LL << 30))
+        return set_error(PA_ERR_UNSUPPORTED, "%s: too many tokens (%d)", who, num_tokens);
+    prm.units = (int)units;
+    prm.sines_at = prm.tokens_per_unit * rows;
+    prm.stage_bytes = (prm.sines_at + prm.tokens_per_unit * sines + 127) & ~127;
     prm.stages = std::max(1, std::min(kRopeMaxStages, kRopeSmemBytes / prm.stage_bytes));
     const int smem = prm.stages * prm.stage_bytes;
-    const void *fn = kernels[(adjacent ? 4 : 0) + (fp8 ? 2 : 0) + (dtype == PA_BF16 ? 1 : 0)];
+    const int variant = (prm.tokens_per_unit > 1 ? 8 : 0) + (adjacent ? 4 : 0) + (fp8 ? 2 : 0) + (dtype == PA_BF16 ? 1 : 0);
+    const void *fn = kernels[variant];
     // Allow the largest ring once per kernel and device, so that a call being
     // captured into a CUDA graph makes no attribute call.
     {
         static std::mutex mu;
-        static bool raised[8][64] = {};
-        const int variant = (adjacent ? 4 : 0) + (fp8 ? 2 : 0) + (dtype == PA_BF16 ? 1 : 0);
+        static bool raised[16][64] = {};
         std::lock_guard<std::mutex> lock(mu);
         if (dev >= 64 || !raised[variant][dev]) {
             cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kRopeSmemBytes);
@@ -554,7 +619,7 @@ int rope_impl(const char *who, void *query_out, const void *query, const void *k
     }
     void *args[] = {&prm};
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)std::min<long long>(prm.units, 2LL * sms));
+    cfg.gridDim = dim3((unsigned)std::min(prm.units, 2 * sms));
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.blockDim = dim3(kRopeThreads);
     cfg.stream = reinterpret_cast<cudaStream_t>(stream);

@@ -135,6 +135,20 @@ def test_every_layout_equals_the_definition(dev, dtype, fp8, T, hq, hkv, D, rot,
     RopeCase(dev, dtype, T, hq, hkv, D, rot, axes, adjacent, fp8, fused, seed=T + hq + D).run().check()
 
 
+@pytest.mark.parametrize("fp8", [False, True], ids=["16bit", "fp8"])
+@pytest.mark.parametrize("T,hq,hkv,D,rot,axes,adjacent,fused", [
+    (2500, 4, 1, 64, 64, 1, False, True),
+    (10001, 16, 4, 64, 32, 3, False, False),
+    (9990, 3, 1, 32, 16, 2, True, True),
+    (12289, 1, 1, 16, 16, 1, False, False),
+    (2600, 12, 2, 128, 64, 1, True, True),
+    (3000, 40, 40, 128, 128, 1, False, True),
+])
+def test_many_tokens(dev, fp8, T, hq, hkv, D, rot, axes, adjacent, fused):
+    """Enough tokens for every CTA's ring to go round many times, several short tokens a unit, odd counts at the end."""
+    RopeCase(dev, workloads.BF16, T, hq, hkv, D, rot, axes, adjacent, fp8, fused, seed=T, far=1 << 14).run().check()
+
+
 @pytest.mark.parametrize("adjacent", [False, True])
 def test_far_positions(dev, adjacent):
     """Positions over the whole 32-bit range, both signs."""
