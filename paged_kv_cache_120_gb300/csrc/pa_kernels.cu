@@ -25,6 +25,9 @@
 //    The split depends only on the sequence lengths and the grid size, never
 //    on physical block ids, so outputs are bit-identical under any
 //    permutation of block placement.
+//  * Cross attention of a few rows (pa_cross_attention) is the same kernel
+//    with ragged queries: a tile's columns are the (query, head) pairs of a
+//    sequence's one or few queries, up to 16.
 //  * reshape_and_cache and copy_blocks are bit copies with 16-byte accesses.
 //  * FP8 cache (OCP E4M3 codes with one scale for K and one for V; a reading
 //    of the book's "lower-precision KV cache", §4.8): the same pipeline moves
@@ -1136,9 +1139,9 @@ constexpr size_t reduce_smem_bytes()
 }
 
 // Finish the segments cut by warp-share boundaries. Warp j of reduce CTA r
-// serves main-grid warp
-// r * W + j: if that warp holds the last piece of a split segment,
-// the segment's pieces (one record per main-grid warp, ascending) are merged
+// serves main-grid warp r * W + j (with merge groups, (r * W + j) / groups and
+// one group of its columns): if that warp holds the last piece of a split
+// segment, the segment's pieces (one record per main-grid warp, ascending) are merged
 // with the online-softmax rule m = max m_p, l = sum l_p 2^(m_p - m),
 // O = sum O_p 2^(m_p - m). A task with few pieces is merged by its warp; a
 // task with many pieces by the whole CTA, pieces split across the warps and

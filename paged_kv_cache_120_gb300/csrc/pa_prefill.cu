@@ -41,6 +41,9 @@
 //    rounded to the element type (the reference maximum moves only when a
 //    score exceeds it by 2^8, so O is rarely rescaled), row sum of the
 //    rounded values, P into tensor memory. At the unit's end, O / l.
+//  * Cross attention of more rows (pa_cross_attention) is the same kernel
+//    without the causal limit; if no chunk passes one query tile, both halves
+//    of the tensor memory work on that tile (SOLO).
 //  * Every wait is bounded; K/V rows past a sequence's end (padding slots,
 //    possibly NaN) are zeroed before P V reads them.
 #include <cuda.h>

@@ -20,7 +20,10 @@
 // bandwidth. One cluster does it in one launch: every CTA scans all rows
 // itself (at most 4096 x 8 bytes, from L2), then takes its share of the new
 // table entries and tokens; the one barrier, between the last read of the
-// lengths and their in-place update, is the cluster's own.
+// lengths and their in-place update, is the cluster's own. Measured (GB300,
+// replayed from a graph): 5.3 us for 256 rows of one token, 12.3 us for 4096
+// mixed rows and 31000 tokens, 10.3 us for 16 prompts of 160000 tokens; one
+// CTA took 5.4, 65 and 118.
 #include <cuda_runtime.h>
 
 #include <cstdint>
