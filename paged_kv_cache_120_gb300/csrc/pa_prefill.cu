@@ -75,6 +75,7 @@ __device__ int g_prefill_sched[kSchedSlots][2];
 
 // Stream-K launches (few work units): at most this many units.
 constexpr int kMaxSplitUnits = 1024;
+constexpr int kOrderedSeqs = 128;       // cross batches of at most so many take their sequences longest first
 constexpr int kMergeRowsPerThread = 4;  // rows one merge thread combines
 
 namespace {
@@ -422,7 +423,11 @@ struct PrefillParams {
 // + s) * num_kv_heads + h) * head_tiles + ht, when each CTA takes whole
 // units from a counter; sequence-major, u = ((s * num_kv_heads + h) *
 // head_tiles + ht) * q_pairs + qr, when CTAs take equal shares of the
-// tiles (stream-K), so that a sequence's units lie side by side.
+// tiles (stream-K), so that a sequence's units lie side by side. Cross
+// attention always numbers sequence-major: its units of a sequence and head
+// are alike, and side by side they read that head's K/V from L2 (8 x 1024
+// queries over 6404 states, 8 kv heads: 637 - 677 us by machine heaviest query
+// pairs first, 638 - 656 us sequence-major; its FP8 form 780 and 745 us).
 struct Unit {
     int s, h, ht, q0, q_len, L;
     int t0[2];       // first query token of tile A / B
@@ -456,18 +461,21 @@ __device__ __forceinline__ int pair_tiles(const PrefillParams &p, int q_len, int
     return ((p.cross ? L : L - q_len + min(q_len, ta + 2 * p.rows_per_head)) + kN - 1) / kN;
 }
 
-// SK: the stream-K numbering (sequence-major).
+// SK: the stream-K numbering (sequence-major); cross attention has it too.
+// order: a cross batch's sequences by length, longest first, up to kOrderedSeqs of them.
 template <bool SK>
-__device__ __forceinline__ bool unit_of(const PrefillParams &p, int u, Unit &w, bool flag)
+__device__ __forceinline__ bool unit_of(const PrefillParams &p, const uint8_t *order, int u, Unit &w, bool flag)
 {
     int ht, h, s, qr;
-    if constexpr (SK) {
+    if (SK || p.cross) {
         qr = u % p.q_pairs;
         int r = u / p.q_pairs;
         ht = r % p.head_tiles;
         r /= p.head_tiles;
         h = r % p.num_kv_heads;
         s = r / p.num_kv_heads;
+        if (!SK && p.num_seqs <= kOrderedSeqs)
+            s = order[s];
     } else {
         ht = u % p.head_tiles;
         int r = u / p.head_tiles;
@@ -529,6 +537,7 @@ struct PrefillBars {
     int unit_ring[kUnitSlots];  // unit index, or -1 once the launch's units are all taken
     uint32_t tmem_base;
     int fail;
+    uint8_t order[kOrderedSeqs];  // cross, whole units: the sequences, longest first
     // Stream-K: the rest of each work item (first and end K/V tile, first
     // and last CTA holding a piece of the unit; equal: the whole unit).
     int item_ext[kUnitSlots][4];
@@ -726,6 +735,31 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                 done += __shfl_sync(kFull, incl, 31);
             }
         }
+        if (!SPLIT && p.cross && p.num_seqs <= kOrderedSeqs) {
+            // Longest sequences first, so that no long unit is left for the
+            // end (40 x up to 224 queries over 1 .. 1500 states, 20 heads of
+            // 64: 91 us as they come, 79 us so; 39 x 243 over up to 16941: 685
+            // and 539 us): a sequence's place is the number of longer ones.
+            int len[kOrderedSeqs / 32], place[kOrderedSeqs / 32];
+#pragma unroll
+            for (int k = 0; k < kOrderedSeqs / 32; ++k) {
+                len[k] = 32 * k + lane < p.num_seqs ? p.seq_lens[32 * k + lane] : 0;
+                place[k] = 0;
+            }
+#pragma unroll
+            for (int b = 0; b < kOrderedSeqs / 32; ++b)
+                for (int i = 0; i < min(32, p.num_seqs - 32 * b); ++i) {
+                    const int other = __shfl_sync(kFull, len[b], i);
+#pragma unroll
+                    for (int k = 0; k < kOrderedSeqs / 32; ++k)
+                        place[k] += other > len[k] || (other == len[k] && 32 * b + i < 32 * k + lane);
+                }
+#pragma unroll
+            for (int k = 0; k < kOrderedSeqs / 32; ++k)
+                if (32 * k + lane < p.num_seqs)
+                    bars.order[place[k]] = (uint8_t)(32 * k + lane);
+            __syncwarp();
+        }
         if (lane == 0) {
             int *next = p.cross ? p.counter : &g_prefill_sched[p.sched_slot][0];
             int dealt = blockIdx.x;
@@ -785,7 +819,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                             if (nu > 0)
                                 break;
                         }
-                        if (!unit_of<true>(p, it.u, w, false))
+                        if (!unit_of<true>(p, bars.order, it.u, w, false))
                             it.u = -1;
                         else if (it.j0 == 0 && it.chi > it.clo)  // this CTA holds the unit's first piece
                             p.jobs[blockIdx.x] = make_int4(it.chi, w.q0 + w.t0[0], w.q_len - w.t0[0],
@@ -796,7 +830,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                     do {
                         u = p.cross && !p.counter ? dealt : atomicAdd(next, 1);
                         dealt += gridDim.x;
-                    } while (u < p.num_units && !unit_of<false>(p, u, w, true));
+                    } while (u < p.num_units && !unit_of<false>(p, bars.order, u, w, true));
                     if (u < p.num_units) {
                         it.u = u;
                         it.j1 = 0x7fffffff;
@@ -846,7 +880,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                     if (!take_unit(i, group_mask, lane == leader, it) || it.u < 0)
                         break;
                     Unit w;
-                    unit_of<SPLIT>(p, it.u, w, false);
+                    unit_of<SPLIT>(p, bars.order, it.u, w, false);
                     const int n = SPLIT ? min(max(w.n[0], w.n[1]), it.j1) : max(w.n[0], w.n[1]);
                     const int32_t *table = p.block_tables + (long long)w.s * p.max_blocks_per_seq;
                     auto lookup = [&](int j) {
@@ -904,7 +938,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
             if (!take_unit(i, kFull, lane == 0, it) || it.u < 0)
                 break;
             Unit w;
-            unit_of<SPLIT>(p, it.u, w, false);
+            unit_of<SPLIT>(p, bars.order, it.u, w, false);
             const int n = SPLIT ? min(max(w.n[0], w.n[1]), it.j1) : max(w.n[0], w.n[1]);
             const int32_t *table = p.block_tables + (long long)w.s * p.max_blocks_per_seq;
             auto issue = [&](int j) {
@@ -1003,7 +1037,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                 if (!take_unit(i, 1u, true, it) || it.u < 0)
                     break;
                 Unit w;
-                unit_of<SPLIT>(p, it.u, w, false);
+                unit_of<SPLIT>(p, bars.order, it.u, w, false);
                 // Tiles j0 <= j < j1 of the unit; tile x reads those below its ne[x].
                 const int j0 = SPLIT ? it.j0 : 0;
                 const int j1 = SPLIT ? min(max(w.n[0], w.n[1]), it.j1) : max(w.n[0], w.n[1]);
@@ -1151,7 +1185,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
             if (!take_unit(i, kFull, lane == 0, it) || it.u < 0)
                 break;
             Unit w;
-            unit_of<SPLIT>(p, it.u, w, false);
+            unit_of<SPLIT>(p, bars.order, it.u, w, false);
             // This tile reads K/V tiles j0 <= j < nx of the item's j0 .. j1.
             const int j0 = SPLIT ? it.j0 : 0;
             const int j1 = SPLIT ? min(max(w.n[0], w.n[1]), it.j1) : max(w.n[0], w.n[1]);
@@ -1674,9 +1708,12 @@ int encode_kv_map(CUtensorMap *m, const void *kv, int num_blocks, int block_size
                              (cuuint64_t)num_blocks * block_size * num_kv_heads * hd * e};
     cuuint32_t box[5] = {64, 1, (cuuint32_t)kBoxTokens, 1, 1};
     cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    // A row of a 64-wide head is 128 bytes: promoted to 256, its load would pull
+    // the next head's row from DRAM as well.
     CUresult r = encoder()(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 5, const_cast<void *>(kv), dims, strides, box,
                            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                           d == kD ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? PA_OK : set_error(PA_ERR_CUDA, "pa_prefill: K/V tensor map (%d)", (int)r);
 }
 

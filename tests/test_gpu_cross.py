@@ -192,6 +192,17 @@ def test_many_short_sequences(dev):
     CrossCase(dev, workloads.F16, 4, 2, 64, np.ones(4096, int), rng.integers(0, 30, 4096), seed=7).both()
 
 
+@pytest.mark.parametrize("n", [1, 31, 33, 64, 127, 128, 129, 200])
+def test_batches_taken_longest_first(dev, n):
+    """Around the batch size up to which whole units go by length: equal lengths, zeros, one far longer than the rest."""
+    rng = np.random.default_rng(n)
+    kv = rng.choice([0, 7, 7, 40, 129, 300], n)
+    kv[n // 2] = 2500
+    qlen = rng.integers(0, 150, n)
+    qlen[-1] = 140
+    CrossCase(dev, workloads.F16, 8, 4, 64, qlen, kv, seed=n).both()
+
+
 @pytest.mark.parametrize("qlen", [[1, 1, 1], [4, 3, 2], [150, 20, 9]])
 def test_without_any_states(dev, qlen):
     CrossCase(dev, workloads.F16, 8, 2, 128, qlen, [0, 0, 0]).both()
