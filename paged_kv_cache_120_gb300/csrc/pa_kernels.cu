@@ -202,6 +202,14 @@ constexpr int decode_warps()
         return 12;
     return NT == 1 ? (FP8 ? PA_DECODE_WARPS_FP8 : PA_DECODE_WARPS) : PA_DECODE_WARPS_WIDE;
 }
+// 16-column tiles at head size 128 fit one CTA an SM whatever registers they
+// take; said so, the compiler spends more of them on loads in flight (64/4
+// heads, 16 sequences up to 9000 tokens, FP8: 46.7 us unsaid, 45.0 us so).
+template <int D, int NT>
+constexpr int decode_min_ctas()
+{
+    return D == 128 && NT == 2 ? 1 : 0;  // 0: unsaid
+}
 // TMA ring depth per warp. An FP8 tile is half the bytes of a 16-bit one, so
 // the FP8 pipelines keep two in flight to hold the same bytes in flight.
 template <int D, int NT, bool FP8, bool RAGGED>
@@ -349,7 +357,7 @@ __device__ __forceinline__ int owner_of(long long u, long long N, long long K)
 // element type of Q and the output, FP8 cache or not, one query per sequence
 // or a ragged few. One CTA = decode_warps<NT>() independent warp pipelines.
 template <int D, int NT, bool BF16, bool FP8, bool RAGGED>
-__global__ void __launch_bounds__(decode_warps<D, NT, FP8, RAGGED>() * 32)
+__global__ void __launch_bounds__(decode_warps<D, NT, FP8, RAGGED>() * 32, decode_min_ctas<D, NT>())
     paged_decode_kernel(const __grid_constant__ CUtensorMap kv_map, const DecodeParams p)
 {
     using Geo = TileGeo<D, FP8>;
@@ -808,15 +816,18 @@ __global__ void __launch_bounds__(decode_warps<D, NT, FP8, RAGGED>() * 32)
         // MMA chain is half as long as the head dimension. V^T fragments do
         // not depend on P: they are loaded up front as well.
         float sc[NT][4], sc2[NT][4];
+        auto zero_scores = [&] {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-                sc[nt][c] = sc2[nt][c] = 0.f;
+                for (int c = 0; c < 4; ++c)
+                    sc[nt][c] = sc2[nt][c] = 0.f;
+        };
         uint32_t kf[kLate ? 4 : KS][4];
         uint32_t vf[kLate ? 1 : KS][4];
         if constexpr (kLate) {
             // Four k-steps at a time: their fragments, then their MMAs.
+            zero_scores();
 #pragma unroll
             for (int k0 = 0; k0 < KS; k0 += 4) {
                 const int c = CPT * tig + k0 / 4;
@@ -907,6 +918,7 @@ __global__ void __launch_bounds__(decode_warps<D, NT, FP8, RAGGED>() * 32)
             }
         }
 
+        zero_scores();
 #pragma unroll
         for (int kk = 0; kk < KS; kk += 2)
 #pragma unroll
@@ -1056,6 +1068,8 @@ __device__ void fold_pieces(const float *recs, int o_first, int ostep, int o_hi,
 {
     constexpr int RP = NT * 8, GP = CN * 8, KD = D / 32, REC = record_floats<D, NT>();
     constexpr int PPR = CN == 1 ? 2 : 1;
+    if (CN == NT)
+        c0 = 0;  // known here even where the call is not inlined
     const int lane = threadIdx.x & 31;
     for (int o0 = o_first; o0 <= o_hi; o0 += PPR * ostep) {
         float mp[PPR][GP], lp[PPR][GP], x[PPR][GP][KD];
@@ -1161,8 +1175,8 @@ __global__ void __launch_bounds__(W * 32) paged_decode_reduce_kernel(const Decod
     const int tq = p.tile_q;
     const int segs_per_seq = p.num_kv_heads * p.qtiles;
     uint16_t *out_base = static_cast<uint16_t *>(p.out);
-    // Column c's output row of a segment, or null if it is none of the
-    // sequence's (a task exists only for a consistent sequence with queries).
+    // A segment's output: whether column c is a row of the sequence's, and
+    // which (a task exists only for a consistent sequence with queries).
     struct OutRows {
         uint16_t *first;
         int n;  // ragged: queries
@@ -1174,18 +1188,25 @@ __global__ void __launch_bounds__(W * 32) paged_decode_reduce_kernel(const Decod
         return OutRows{out_base + ((long long)q0 * p.num_q_heads + h * p.group + qt * 16) * D,
                        RAGGED ? p.cu_q[s + 1] - q0 : 1};
     };
-    auto out_row = [&](const OutRows &o, int c) -> uint16_t * {
+    auto has_row = [&](const OutRows &o, int c) {
+        if constexpr (RAGGED)
+            return c / p.tile_heads < o.n;
+        else
+            return c < tq;
+    };
+    auto out_row = [&](const OutRows &o, int c) {
         if constexpr (RAGGED) {
             const int q = c / p.tile_heads;
-            return q < o.n ? o.first + ((long long)q * p.num_q_heads + (c - q * p.tile_heads)) * D : nullptr;
+            return o.first + ((long long)q * p.num_q_heads + (c - q * p.tile_heads)) * D;
         } else {
-            return c < tq ? o.first + (long long)c * D : nullptr;
+            return o.first + (long long)c * D;
         }
     };
     auto store = [&](const OutRows &o, const MergeState<D, CN> &st) {
 #pragma unroll
         for (int c = 0; c < GP; ++c)
-            if (uint16_t *out = out_row(o, c0 + c)) {
+            if (has_row(o, c0 + c)) {
+                uint16_t *out = out_row(o, c0 + c);
                 const float inv = 1.f / st.l[c];
 #pragma unroll
                 for (int k = 0; k < KD; ++k)
@@ -1230,8 +1251,7 @@ __global__ void __launch_bounds__(W * 32) paged_decode_reduce_kernel(const Decod
         const OutRows o = out_rows(t.x);
         for (int e = threadIdx.x; e < min(tq - cj, GP) * D; e += W * 32) {
             const int c = e / D, d = e - (e / D) * D;
-            uint16_t *out = out_row(o, cj + c);
-            if (!out)
+            if (RAGGED && !has_row(o, cj + c))
                 continue;
             float Mx = -INFINITY;
             for (int v = 0; v < W; ++v)
@@ -1243,7 +1263,7 @@ __global__ void __launch_bounds__(W * 32) paged_decode_reduce_kernel(const Decod
                 lt += f * pv[GP + c];
                 ot += f * pv[2 * GP + c * D + d];
             }
-            out[d] = to_elem<BF16>(ot / lt);
+            out_row(o, cj + c)[d] = to_elem<BF16>(ot / lt);
         }
         __syncthreads();
     }

@@ -412,7 +412,6 @@ struct PrefillParams {
                         //  first query head}
     float scale_log2;   // scale * log2(e) (* k_scale with an FP8 cache)
     float v_scale;      // 1, or the FP8 cache's V scale
-    int cross;          // 1: every query sees all L cached tokens (cross attention); 0: causally
     int *counter;       // cross, whole units: the next unit, in the caller's workspace (null: dealt out in turn)
 };
 
@@ -444,38 +443,42 @@ struct Item {
 // offsets or lengths (flagged once, by the unit of the sequence's first
 // heads and last query pair, when `flag`).
 // A sequence's offsets and length are consistent.
+template <bool CROSS>
 __device__ __forceinline__ bool seq_ok(const PrefillParams &p, int q0, int q_len, int L)
 {
-    return !(q_len < 0 || q_len > p.max_q || q0 < 0 || q0 > p.total_q - q_len || L < (p.cross ? 0 : q_len) ||
+    return !(q_len < 0 || q_len > p.max_q || q0 < 0 || q0 > p.total_q - q_len || L < (CROSS ? 0 : q_len) ||
              L > p.max_len);
 }
 
 // K/V tiles the unit of query pair qr of a sequence reads (those its tile
 // B's last query sees, or tile A's when B has no queries); 0 when tile A
 // has no queries.
+template <bool CROSS>
 __device__ __forceinline__ int pair_tiles(const PrefillParams &p, int q_len, int L, int qr)
 {
     const int ta = 2 * (p.q_pairs - 1 - qr) * p.rows_per_head;
     if (ta >= q_len)
         return 0;
-    return ((p.cross ? L : L - q_len + min(q_len, ta + 2 * p.rows_per_head)) + kN - 1) / kN;
+    return ((CROSS ? L : L - q_len + min(q_len, ta + 2 * p.rows_per_head)) + kN - 1) / kN;
 }
 
 // SK: the stream-K numbering (sequence-major); cross attention has it too.
 // order: a cross batch's sequences by length, longest first, up to kOrderedSeqs of them.
-template <bool SK>
+template <bool SK, bool CROSS>
 __device__ __forceinline__ bool unit_of(const PrefillParams &p, const uint8_t *order, int u, Unit &w, bool flag)
 {
     int ht, h, s, qr;
-    if (SK || p.cross) {
+    if constexpr (SK || CROSS) {
         qr = u % p.q_pairs;
         int r = u / p.q_pairs;
         ht = r % p.head_tiles;
         r /= p.head_tiles;
         h = r % p.num_kv_heads;
         s = r / p.num_kv_heads;
-        if (!SK && p.num_seqs <= kOrderedSeqs)
-            s = order[s];
+        if constexpr (!SK) {
+            if (p.num_seqs <= kOrderedSeqs)
+                s = order[s];
+        }
     } else {
         ht = u % p.head_tiles;
         int r = u / p.head_tiles;
@@ -485,14 +488,14 @@ __device__ __forceinline__ bool unit_of(const PrefillParams &p, const uint8_t *o
         qr = r / p.num_seqs;
     }
     const int q0 = p.cu_q[s], q_len = p.cu_q[s + 1] - q0, L = p.seq_lens[s];
-    if (!seq_ok(p, q0, q_len, L)) {
+    if (!seq_ok<CROSS>(p, q0, q_len, L)) {
         if (flag && h == 0 && ht == 0 && qr == 0)
             prefill_raise(PA_DEVERR_SEQ_LEN);
         return false;
     }
     const int T = p.rows_per_head;
     const int ta = 2 * (p.q_pairs - 1 - qr) * T;
-    if (ta >= q_len || L == 0)  // L == 0: cross attention to nothing, zero rows (written by zero_rows)
+    if (ta >= q_len || (CROSS && L == 0))  // L == 0: cross attention to nothing, zero rows (written by zero_rows)
         return false;
     w.s = s;
     w.h = h;
@@ -503,7 +506,7 @@ __device__ __forceinline__ bool unit_of(const PrefillParams &p, const uint8_t *o
     for (int x = 0; x < 2; ++x) {
         w.t0[x] = ta + x * T;
         const int t_end = min(q_len, w.t0[x] + T);
-        w.n[x] = w.t0[x] < q_len ? ((p.cross ? L : L - q_len + t_end) + kN - 1) / kN : 0;  // tiles its last query sees
+        w.n[x] = w.t0[x] < q_len ? ((CROSS ? L : L - q_len + t_end) + kN - 1) / kN : 0;  // tiles its last query sees
     }
     return true;
 }
@@ -516,7 +519,7 @@ __device__ __forceinline__ void zero_rows(const PrefillParams &p, int tid)
 {
     for (int s = blockIdx.x; s < p.num_seqs; s += gridDim.x) {
         const int q0 = p.cu_q[s], q_len = p.cu_q[s + 1] - q0, L = p.seq_lens[s];
-        if (L != 0 || !seq_ok(p, q0, q_len, L))
+        if (L != 0 || !seq_ok<true>(p, q0, q_len, L))
             continue;
         const long long row = (long long)p.num_q_heads * (D / 8);
         uint4 *out = static_cast<uint4 *>(p.out) + q0 * row;
@@ -527,7 +530,6 @@ __device__ __forceinline__ void zero_rows(const PrefillParams &p, int tid)
 
 struct PrefillBars {
     uint64_t q_full, q_empty, k_full[kKStagesMax], k_empty[kKStagesMax], v_full[kVStagesMax], v_empty[kVStagesMax];
-    uint64_t solo_full, solo_done;  // solo: B's state is there, A has read it and B's O
     uint64_t q_ready;  // FP8 cache, bf16 queries: the softmax threads have moved Q to fp16
     uint64_t stg_full[2][2];  // FP8 cache: K / V staging half 0 / 1 has landed
     // Per query tile x: s_full[x] its S is in TMEM, p_full[x] its P is,
@@ -537,7 +539,6 @@ struct PrefillBars {
     int unit_ring[kUnitSlots];  // unit index, or -1 once the launch's units are all taken
     uint32_t tmem_base;
     int fail;
-    uint8_t order[kOrderedSeqs];  // cross, whole units: the sequences, longest first
     // Stream-K: the rest of each work item (first and end K/V tile, first
     // and last CTA holding a piece of the unit; equal: the whole unit).
     int item_ext[kUnitSlots][4];
@@ -545,20 +546,28 @@ struct PrefillBars {
 
 // SPLIT: the stream-K instance (few units, K/V ranges shared out evenly);
 // otherwise whole units from a counter.
-// SOLO: cross attention with chunks of at most one query tile, so that no
+// KIND: what a query sees, its position's causal prefix or (cross attention)
+// all L cached tokens, and whether the chunks fit one query tile. A template
+// parameter because a runtime flag costs the causal kernel 1 - 8 %.
+enum : int { kCausal = 0, kCross = 1, kCrossSolo = 2 };
+
+// kCrossSolo: cross attention with chunks of at most one query tile, so that no
 // unit has a tile B. B then takes A's queries as well, A the even and B the
 // odd K/V tiles of the item, so that one's matrix work still overlaps the
 // other's softmax, and A folds B's state into its own at the end (disjoint
 // token ranges, [book] §4.6). Measured (76 sequences x 100 queries over 4000
 // states, 2 heads of 64): 53 us with tile A alone, 41 us.
-template <bool BF16, bool FP8, int D, bool SPLIT, bool SOLO>
+template <bool BF16, bool FP8, int D, bool SPLIT, int KIND>
 __global__ void __launch_bounds__(threads_for(FP8), 1)
     paged_prefill_kernel(const __grid_constant__ CUtensorMap kv_map,
                          const __grid_constant__ CUtensorMap q_map, const PrefillParams p)
 {
     extern __shared__ uint8_t smem_raw[];
     __shared__ PrefillBars bars;
+    constexpr bool CROSS = KIND != kCausal, SOLO = KIND == kCrossSolo;
+    __shared__ uint8_t order[CROSS && !SPLIT ? kOrderedSeqs : 1];  // the sequences, longest first
     __shared__ float2 solo_ml[SOLO ? kM : 1];  // (reference maximum, row sum) of B's rows
+    __shared__ uint64_t solo_bars[SOLO ? 2 : 1];  // B's state is there, A has read it and B's O
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int T = p.rows_per_head, HPC = p.heads_per_cta;
@@ -598,8 +607,10 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
         mbar_init(b_q, 1);
         mbar_init(b_qr, 256);  // the 8 softmax warps
         mbar_init(b_qe, 1);
-        mbar_init(smem_addr(&bars.solo_full), 128);
-        mbar_init(smem_addr(&bars.solo_done), 128);
+        if constexpr (SOLO) {
+            mbar_init(smem_addr(&solo_bars[0]), 128);
+            mbar_init(smem_addr(&solo_bars[1]), 128);
+        }
         for (int st = 0; st < kKStages; ++st) {
             mbar_init(b_kf(st), FP8 ? 2 : 1);  // FP8: the two widening warps of the tile
             mbar_init(b_ke(st), 1);
@@ -689,14 +700,14 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
         const int H = p.num_kv_heads * p.head_tiles;  // units of one query pair of a sequence
         auto seq_tiles = [&](int s, bool flag) {     // K/V tiles of one head tile of sequence s
             const int q0 = p.cu_q[s], q_len = p.cu_q[s + 1] - q0, L = p.seq_lens[s];
-            if (!seq_ok(p, q0, q_len, L)) {
+            if (!seq_ok<CROSS>(p, q0, q_len, L)) {
                 if (flag)
                     prefill_raise(PA_DEVERR_SEQ_LEN);
                 return 0LL;
             }
             long long a = 0;
             for (int qr = 0; qr < p.q_pairs; ++qr)
-                a += pair_tiles(p, q_len, L, qr);
+                a += pair_tiles<CROSS>(p, q_len, L, qr);
             return a;
         };
         long long lo = 0, hi = 0, W = 0, Ts = 0;  // this CTA's tiles [lo, hi); sequence ws starts at tile Ts
@@ -735,7 +746,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                 done += __shfl_sync(kFull, incl, 31);
             }
         }
-        if (!SPLIT && p.cross && p.num_seqs <= kOrderedSeqs) {
+        if (!SPLIT && CROSS && p.num_seqs <= kOrderedSeqs) {
             // Longest sequences first, so that no long unit is left for the
             // end (40 x up to 224 queries over 1 .. 1500 states, 20 heads of
             // 64: 91 us as they come, 79 us so; 39 x 243 over up to 16941: 685
@@ -757,11 +768,11 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
 #pragma unroll
             for (int k = 0; k < kOrderedSeqs / 32; ++k)
                 if (32 * k + lane < p.num_seqs)
-                    bars.order[place[k]] = (uint8_t)(32 * k + lane);
+                    order[place[k]] = (uint8_t)(32 * k + lane);
             __syncwarp();
         }
         if (lane == 0) {
-            int *next = p.cross ? p.counter : &g_prefill_sched[p.sched_slot][0];
+            int *next = CROSS ? p.counter : &g_prefill_sched[p.sched_slot][0];
             int dealt = blockIdx.x;
             // Stream-K walk: unit (ws, hh, qr) holds tiles [Tu, Tu + nu).
             int hh = 0, qr = 0, wq_len = 0, wL = 0, nu = 0;
@@ -771,9 +782,9 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                 const int q0 = p.cu_q[ws];
                 wq_len = p.cu_q[ws + 1] - q0;
                 wL = p.seq_lens[ws];
-                wok = seq_ok(p, q0, wq_len, wL);
+                wok = seq_ok<CROSS>(p, q0, wq_len, wL);
             };
-            auto tiles_here = [&]() { return wok ? pair_tiles(p, wq_len, wL, qr) : 0; };
+            auto tiles_here = [&]() { return wok ? pair_tiles<CROSS>(p, wq_len, wL, qr) : 0; };
             if (SPLIT && lo < hi) {
                 enter_seq();
                 const long long a = seq_tiles(ws, false);
@@ -819,7 +830,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                             if (nu > 0)
                                 break;
                         }
-                        if (!unit_of<true>(p, bars.order, it.u, w, false))
+                        if (!unit_of<true, CROSS>(p, order, it.u, w, false))
                             it.u = -1;
                         else if (it.j0 == 0 && it.chi > it.clo)  // this CTA holds the unit's first piece
                             p.jobs[blockIdx.x] = make_int4(it.chi, w.q0 + w.t0[0], w.q_len - w.t0[0],
@@ -828,9 +839,9 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                 } else {
                     int u;
                     do {
-                        u = p.cross && !p.counter ? dealt : atomicAdd(next, 1);
+                        u = CROSS && !p.counter ? dealt : atomicAdd(next, 1);
                         dealt += gridDim.x;
-                    } while (u < p.num_units && !unit_of<false>(p, bars.order, u, w, true));
+                    } while (u < p.num_units && !unit_of<false, CROSS>(p, order, u, w, true));
                     if (u < p.num_units) {
                         it.u = u;
                         it.j1 = 0x7fffffff;
@@ -880,7 +891,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                     if (!take_unit(i, group_mask, lane == leader, it) || it.u < 0)
                         break;
                     Unit w;
-                    unit_of<SPLIT>(p, bars.order, it.u, w, false);
+                    unit_of<SPLIT, CROSS>(p, order, it.u, w, false);
                     const int n = SPLIT ? min(max(w.n[0], w.n[1]), it.j1) : max(w.n[0], w.n[1]);
                     const int32_t *table = p.block_tables + (long long)w.s * p.max_blocks_per_seq;
                     auto lookup = [&](int j) {
@@ -938,7 +949,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
             if (!take_unit(i, kFull, lane == 0, it) || it.u < 0)
                 break;
             Unit w;
-            unit_of<SPLIT>(p, bars.order, it.u, w, false);
+            unit_of<SPLIT, CROSS>(p, order, it.u, w, false);
             const int n = SPLIT ? min(max(w.n[0], w.n[1]), it.j1) : max(w.n[0], w.n[1]);
             const int32_t *table = p.block_tables + (long long)w.s * p.max_blocks_per_seq;
             auto issue = [&](int j) {
@@ -1037,7 +1048,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                 if (!take_unit(i, 1u, true, it) || it.u < 0)
                     break;
                 Unit w;
-                unit_of<SPLIT>(p, bars.order, it.u, w, false);
+                unit_of<SPLIT, CROSS>(p, order, it.u, w, false);
                 // Tiles j0 <= j < j1 of the unit; tile x reads those below its ne[x].
                 const int j0 = SPLIT ? it.j0 : 0;
                 const int j1 = SPLIT ? min(max(w.n[0], w.n[1]), it.j1) : max(w.n[0], w.n[1]);
@@ -1174,7 +1185,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
         const int r = quarter * 32 + lane;  // this thread's TMEM lane (row)
         const int g = r / T, t = r - g * T;
         const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-        if (p.cross)
+        if constexpr (CROSS)
             zero_rows<D>(p, tid);
         float sc = p.scale_log2;  // this row's score factor (base 2)
         const bool sc_pos = sc >= 0.f;
@@ -1185,7 +1196,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
             if (!take_unit(i, kFull, lane == 0, it) || it.u < 0)
                 break;
             Unit w;
-            unit_of<SPLIT>(p, bars.order, it.u, w, false);
+            unit_of<SPLIT, CROSS>(p, order, it.u, w, false);
             // This tile reads K/V tiles j0 <= j < nx of the item's j0 .. j1.
             const int j0 = SPLIT ? it.j0 : 0;
             const int j1 = SPLIT ? min(max(w.n[0], w.n[1]), it.j1) : max(w.n[0], w.n[1]);
@@ -1199,7 +1210,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                                 (SOLO ? ((jp - j0) & 1) == x : x == 0 || jp >= (SPLIT ? min(w.n[0], j1) : w.n[0]));
             const bool valid = g < HPC && w.t0[SOLO ? 0 : x] + t < w.q_len;
             // Last token this row sees (cross: rows without a query run on, unread).
-            const int pos = p.cross ? w.L - 1 : valid ? w.L - w.q_len + w.t0[x] + t : -1;
+            const int pos = CROSS ? w.L - 1 : valid ? w.L - w.q_len + w.t0[x] + t : -1;
             if constexpr (kQToF16) {
                 // Move Q row r of this tile to fp16 in place, scaled by 2^-e
                 // so that the row's largest magnitude lies in [2^14, 2^15):
@@ -1429,9 +1440,9 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                 if (x == 1) {
                     solo_ml[r] = work ? make_float2(m_run, l_run) : make_float2(-INFINITY, 0.f);
                     tc_fence_before();
-                    mbar_arrive(smem_addr(&bars.solo_full));
+                    mbar_arrive(smem_addr(&solo_bars[0]));
                 }
-                if (!__all_sync(kFull, wait_or_fail(smem_addr(x == 1 ? &bars.solo_done : &bars.solo_full), i & 1))) {
+                if (!__all_sync(kFull, wait_or_fail(smem_addr(&solo_bars[x]), i & 1))) {
                     alive = false;
                     break;
                 }
@@ -1450,7 +1461,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
             auto solo_read = [&] {  // A has read B's O
                 if constexpr (SOLO) {
                     tc_fence_before();
-                    mbar_arrive(smem_addr(&bars.solo_done));
+                    mbar_arrive(smem_addr(&solo_bars[1]));
                 }
             };
             // 32 columns of the row's O (solo: with B's share).
@@ -1525,7 +1536,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
     // Every role has left its loop, so this CTA takes no more units; the
     // last CTA to get here resets the launch's counters for the next use
     // (a stream-K launch uses none).
-    if (!SPLIT && tid == 0 && !p.cross) {
+    if (!SPLIT && !CROSS && tid == 0) {
         __threadfence();
         if (atomicAdd(&g_prefill_sched[p.sched_slot][1], 1) == (int)gridDim.x - 1) {
             g_prefill_sched[p.sched_slot][0] = 0;
@@ -1944,7 +1955,6 @@ int prefill_impl(const char *who, void *out, const void *query, const void *kv_c
     prm.max_len = max_blocks_per_seq * block_size;
     prm.scale_log2 = scale * 1.4426950408889634f * (fp8 ? k_scale : 1.f);
     prm.v_scale = fp8 ? v_scale : 1.f;
-    prm.cross = cross ? 1 : 0;
     prm.counter = cross && !split ? static_cast<int *>(workspace) : nullptr;
     prm.num_kv_heads = num_kv_heads;
     prm.num_units = (int)lp.units;
@@ -1971,28 +1981,28 @@ int prefill_impl(const char *who, void *out, const void *query, const void *kv_c
         return rc;
 
     const bool bf = dtype == PA_BF16, d64 = head_size == 64;
-    // Cross attention whose chunks all fit one query tile runs solo.
-    const bool solo = cross && max_seqlen_q <= lp.rows_per_head;
-    // Instances by (solo, stream-K, FP8 cache, head size 64, bf16).
-#define PA_PREFILL_INSTANCES(SK, SO)                                                            \
-    reinterpret_cast<const void *>(&paged_prefill_kernel<false, false, 128, SK, SO>),          \
-        reinterpret_cast<const void *>(&paged_prefill_kernel<true, false, 128, SK, SO>),       \
-        reinterpret_cast<const void *>(&paged_prefill_kernel<false, false, 64, SK, SO>),       \
-        reinterpret_cast<const void *>(&paged_prefill_kernel<true, false, 64, SK, SO>),        \
-        reinterpret_cast<const void *>(&paged_prefill_kernel<false, true, 128, SK, SO>),       \
-        reinterpret_cast<const void *>(&paged_prefill_kernel<true, true, 128, SK, SO>),        \
-        reinterpret_cast<const void *>(&paged_prefill_kernel<false, true, 64, SK, SO>),        \
-        reinterpret_cast<const void *>(&paged_prefill_kernel<true, true, 64, SK, SO>)
-    static const void *const kernels[32] = {PA_PREFILL_INSTANCES(false, false), PA_PREFILL_INSTANCES(true, false),
-                                            PA_PREFILL_INSTANCES(false, true), PA_PREFILL_INSTANCES(true, true)};
+    // Instances by (kind, stream-K, FP8 cache, head size 64, bf16).
+#define PA_PREFILL_INSTANCES(SK, KIND)                                                          \
+    reinterpret_cast<const void *>(&paged_prefill_kernel<false, false, 128, SK, KIND>),          \
+        reinterpret_cast<const void *>(&paged_prefill_kernel<true, false, 128, SK, KIND>),       \
+        reinterpret_cast<const void *>(&paged_prefill_kernel<false, false, 64, SK, KIND>),       \
+        reinterpret_cast<const void *>(&paged_prefill_kernel<true, false, 64, SK, KIND>),        \
+        reinterpret_cast<const void *>(&paged_prefill_kernel<false, true, 128, SK, KIND>),       \
+        reinterpret_cast<const void *>(&paged_prefill_kernel<true, true, 128, SK, KIND>),        \
+        reinterpret_cast<const void *>(&paged_prefill_kernel<false, true, 64, SK, KIND>),        \
+        reinterpret_cast<const void *>(&paged_prefill_kernel<true, true, 64, SK, KIND>)
+    static const void *const kernels[48] = {PA_PREFILL_INSTANCES(false, kCausal), PA_PREFILL_INSTANCES(true, kCausal),
+                                            PA_PREFILL_INSTANCES(false, kCross), PA_PREFILL_INSTANCES(true, kCross),
+                                            PA_PREFILL_INSTANCES(false, kCrossSolo), PA_PREFILL_INSTANCES(true, kCrossSolo)};
 #undef PA_PREFILL_INSTANCES
-    const int variant = (solo ? 16 : 0) + (split ? 8 : 0) + (fp8 ? 4 : 0) + (d64 ? 2 : 0) + (bf ? 1 : 0);
+    const int kind = !cross ? kCausal : max_seqlen_q <= lp.rows_per_head ? kCrossSolo : kCross;
+    const int variant = kind * 16 + (split ? 8 : 0) + (fp8 ? 4 : 0) + (d64 ? 2 : 0) + (bf ? 1 : 0);
     const void *fn = kernels[variant];
     // Raise the kernel's shared-memory limit once per device (a call being
     // captured into a CUDA graph then makes no attribute call; the SM count
     // is cached likewise).
     static std::mutex mu;
-    static bool raised[32][64] = {};
+    static bool raised[48][64] = {};
     cudaError_t e;
     {
         std::lock_guard<std::mutex> lock(mu);
