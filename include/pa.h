@@ -466,7 +466,7 @@ int pa_rope_plan(const double *inv_freq, const int32_t *pair_axes, int num_pairs
  *   rot_dim        a multiple of 16, <= head_size and <= 512: the leading
  *                  dimensions that turn; the rest of a head passes unchanged
  *   adjacent       0: pair i is dimensions (i, i + rot_dim / 2); else (2i, 2i + 1)
- *   head_size      a multiple of 8, <= 1024
+ *   head_size      a multiple of 8, <= 1024; num_tokens <= 2^30
  * Result: (x1, x2) becomes (x1 cos a - x2 sin a, x1 sin a + x2 cos a) in fp32,
  * rounded once to dtype (values that pass are bit copies); a is reduced exactly
  * (to 2^-31 turns) at any 32-bit position. Two tokens with the same slot race. Launched

@@ -513,6 +513,8 @@ int rope_impl(const char *who, void *query_out, const void *query, const void *k
     if (num_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads > 65535 || num_kv_heads > 65535 ||
         num_blocks <= 0 || block_size < 16 || block_size % 16 != 0)
         return set_error(PA_ERR_INVALID_ARG, "%s: bad sizes", who);
+    if (num_tokens > (1 << 30))
+        return set_error(PA_ERR_UNSUPPORTED, "%s: too many tokens (%d)", who, num_tokens);
     if (head_size <= 0 || head_size % 8 != 0 || head_size > 1024)
         return set_error(PA_ERR_UNSUPPORTED, "%s: head_size %d (want a multiple of 8, at most 1024)", who, head_size);
     if (rot_dim <= 0 || rot_dim % 16 != 0 || rot_dim > head_size || rot_dim > kRopeMaxDims)

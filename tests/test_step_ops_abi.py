@@ -83,6 +83,15 @@ def test_rope_refusals(lib):
         assert "k_scale" in binding.pa_last_error()
 
 
+def test_rope_refuses_more_tokens_than_its_indexes_count(lib):
+    """Unit, token and window indexes are 32-bit and run past the last token: 2^30 tokens at most."""
+    for T in (2 ** 30 + 1, 2 ** 31 - 8, 2 ** 31 - 1):
+        for axes in (1, 2):
+            args = rope_args(T=T, pstride=T, axes=axes)
+            assert lib.pa_rope_and_cache(*args, None) == UNSUPPORTED and "tokens" in binding.pa_last_error()
+            assert lib.pa_rope_and_cache_fp8(*args, 0.5, 0.5, None) == UNSUPPORTED
+
+
 def test_rope_plan_words(lib):
     """Turns per position as a fraction of 2^64 (to 2 units of its 62 bits), the axis in the low two bits."""
     from fractions import Fraction
