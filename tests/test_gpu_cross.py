@@ -192,6 +192,16 @@ def test_many_short_sequences(dev):
     CrossCase(dev, workloads.F16, 4, 2, 64, np.ones(4096, int), rng.integers(0, 30, 4096), seed=7).both()
 
 
+@pytest.mark.parametrize("fp8", [False, True], ids=["16bit", "fp8"])
+@pytest.mark.parametrize("heads,most", [((8, 2, 128), 2), ((8, 2, 128), 4), ((16, 1, 64), 1)])
+def test_the_largest_batch_of_short_queries(dev, heads, most, fp8):
+    """4096 sequences: their lengths, offsets and tile counts fill what the tiles leave of the shared memory."""
+    rng = np.random.default_rng(most)
+    qlen = rng.integers(0, most + 1, 4096)
+    qlen[7] = most
+    CrossCase(dev, workloads.BF16, *heads, qlen, rng.integers(0, 40, 4096), fp8=fp8, seed=most).both()
+
+
 @pytest.mark.parametrize("n", [1, 31, 33, 64, 127, 128, 129, 200])
 def test_batches_taken_longest_first(dev, n):
     """Around the batch size up to which whole units go by length: equal lengths, zeros, one far longer than the rest."""
