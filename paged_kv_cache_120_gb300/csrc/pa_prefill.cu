@@ -511,6 +511,33 @@ __device__ __forceinline__ bool unit_of(const PrefillParams &p, const uint8_t *o
     return true;
 }
 
+// Cross attention hands each unit's fields around with its index, so that the
+// roles neither divide nor load lengths between two units (XXX).
+struct UnitFields {
+    int s, h, ht, q0, q_len, L, ta, pad;
+};
+
+__device__ __forceinline__ void put_unit(UnitFields *to, const Unit &w)
+{
+    reinterpret_cast<int4 *>(to)[0] = make_int4(w.s, w.h, w.ht, w.q0);
+    reinterpret_cast<int4 *>(to)[1] = make_int4(w.q_len, w.L, w.t0[0], 0);
+}
+
+__device__ __forceinline__ void get_unit(const UnitFields *from, int T, Unit &w)
+{
+    const int4 a = reinterpret_cast<const int4 *>(from)[0], b = reinterpret_cast<const int4 *>(from)[1];
+    w.s = a.x;
+    w.h = a.y;
+    w.ht = a.z;
+    w.q0 = a.w;
+    w.q_len = b.x;
+    w.L = b.y;
+    w.t0[0] = b.z;
+    w.t0[1] = b.z + T;
+    w.n[0] = (w.L + kN - 1) / kN;
+    w.n[1] = w.t0[1] < w.q_len ? w.n[0] : 0;
+}
+
 // Cross attention to a sequence without cached tokens gives zero rows: they
 // have no work unit, so the CTAs' softmax threads (tid < 256) write them,
 // sequence by sequence, before they wait for their first unit.
@@ -565,6 +592,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
     extern __shared__ uint8_t smem_raw[];
     __shared__ PrefillBars bars;
     constexpr bool CROSS = KIND != kCausal, SOLO = KIND == kCrossSolo;
+    __shared__ __align__(16) UnitFields fields[CROSS ? kUnitSlots : 1];
     __shared__ uint8_t order[CROSS && !SPLIT ? kOrderedSeqs : 1];  // the sequences, longest first
     __shared__ float2 solo_ml[SOLO ? kM : 1];  // (reference maximum, row sum) of B's rows
     __shared__ uint64_t solo_bars[SOLO ? 2 : 1];  // B's state is there, A has read it and B's O
@@ -659,7 +687,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
     // The i-th item handed to this CTA (unit -1: no more). Every lane in
     // `mask` calls it; `leader` arrives once the warp has read the slot.
     // False if the wait ran out.
-    auto take_unit = [&](int i, unsigned mask, bool leader, Item &it) {
+    auto take_unit = [&](int i, unsigned mask, bool leader, Item &it, Unit &w) {
         const int sl = i % kUnitSlots;
         if (!__all_sync(mask, wait_or_fail(b_uf(sl), (i / kUnitSlots) & 1)))
             return false;
@@ -675,9 +703,15 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
             it.j1 = 0x7fffffff;
             it.clo = it.chi = 0;
         }
+        if constexpr (CROSS)
+            get_unit(&fields[sl], T, w);
         __syncwarp(mask);
         if (leader)
             mbar_arrive(b_ue(sl));
+        if constexpr (!CROSS) {
+            if (it.u >= 0)
+                unit_of<SPLIT, CROSS>(p, order, it.u, w, false);
+        }
         return true;
     };
 
@@ -851,6 +885,8 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                 if (i >= kUnitSlots && !wait_or_fail(b_ue(sl), ((i / kUnitSlots) - 1) & 1))
                     break;
                 bars.unit_ring[sl] = it.u;
+                if (CROSS && it.u >= 0)
+                    put_unit(&fields[sl], w);
                 if constexpr (SPLIT) {
                     bars.item_ext[sl][0] = it.j0;
                     bars.item_ext[sl][1] = it.j1;
@@ -888,10 +924,9 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                 bool go = true;
                 for (int i = 0; go; ++i) {
                     Item it;
-                    if (!take_unit(i, group_mask, lane == leader, it) || it.u < 0)
-                        break;
                     Unit w;
-                    unit_of<SPLIT, CROSS>(p, order, it.u, w, false);
+                    if (!take_unit(i, group_mask, lane == leader, it, w) || it.u < 0)
+                        break;
                     const int n = SPLIT ? min(max(w.n[0], w.n[1]), it.j1) : max(w.n[0], w.n[1]);
                     const int32_t *table = p.block_tables + (long long)w.s * p.max_blocks_per_seq;
                     auto lookup = [&](int j) {
@@ -946,10 +981,9 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
         bool go = true;
         for (int i = 0; go; ++i) {
             Item it;
-            if (!take_unit(i, kFull, lane == 0, it) || it.u < 0)
-                break;
             Unit w;
-            unit_of<SPLIT, CROSS>(p, order, it.u, w, false);
+            if (!take_unit(i, kFull, lane == 0, it, w) || it.u < 0)
+                break;
             const int n = SPLIT ? min(max(w.n[0], w.n[1]), it.j1) : max(w.n[0], w.n[1]);
             const int32_t *table = p.block_tables + (long long)w.s * p.max_blocks_per_seq;
             auto issue = [&](int j) {
@@ -1045,10 +1079,9 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
             bool go = true;
             for (int i = 0; go; ++i) {
                 Item it;
-                if (!take_unit(i, 1u, true, it) || it.u < 0)
-                    break;
                 Unit w;
-                unit_of<SPLIT, CROSS>(p, order, it.u, w, false);
+                if (!take_unit(i, 1u, true, it, w) || it.u < 0)
+                    break;
                 // Tiles j0 <= j < j1 of the unit; tile x reads those below its ne[x].
                 const int j0 = SPLIT ? it.j0 : 0;
                 const int j1 = SPLIT ? min(max(w.n[0], w.n[1]), it.j1) : max(w.n[0], w.n[1]);
@@ -1193,10 +1226,9 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
         bool alive = true;
         for (int i = 0; alive; ++i) {
             Item it;
-            if (!take_unit(i, kFull, lane == 0, it) || it.u < 0)
-                break;
             Unit w;
-            unit_of<SPLIT, CROSS>(p, order, it.u, w, false);
+            if (!take_unit(i, kFull, lane == 0, it, w) || it.u < 0)
+                break;
             // This tile reads K/V tiles j0 <= j < nx of the item's j0 .. j1.
             const int j0 = SPLIT ? it.j0 : 0;
             const int j1 = SPLIT ? min(max(w.n[0], w.n[1]), it.j1) : max(w.n[0], w.n[1]);
