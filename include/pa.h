@@ -513,12 +513,11 @@ int pa_rope_and_cache_fp8(void *query_out, const void *query, const void *key, c
  *                  block_size], longer or shorter than the queries
  *   workspace      device, NULL or >= pa_cross_attention_workspace_size(...)
  *                  bytes for this shape, 256-byte aligned: split K/V ranges'
- *                  partial results, or with many work units their counter. Its
- *                  contents need no initialisation and are not preserved; calls
- *                  that share it must not overlap on the GPU. NULL: K/V ranges
- *                  stay whole and work is dealt out in a fixed order (same
- *                  result up to fp32 rounding, slower). Too small or misaligned:
- *                  PA_ERR_WORKSPACE.
+ *                  partial results. Its contents need no initialisation and are
+ *                  not preserved; calls that share it must not overlap on the
+ *                  GPU. NULL: K/V ranges stay whole (same result up to fp32
+ *                  rounding, slower where the size is not 0). Too small or
+ *                  misaligned: PA_ERR_WORKSPACE.
  *   flags          0 or PA_DECODE_SHARED_BLOCKS (tables share blocks)
  * Bad offsets, lengths and block ids are handled as pa_prefill handles them
  * (PA_DEVERR_SEQ_LEN, rows not written; PA_DEVERR_BLOCK_ID, read as zeros).
@@ -548,7 +547,8 @@ int pa_cross_attention_fp8(void *out, const void *query, const void *kv_cache,
 
 /*
  * pa_cross_attention_workspace_size — bytes of workspace the cross attention
- * calls want for this shape on the current device (0 only for an empty one).
+ * calls want for this shape on the current device (0: with many work units,
+ * or none, K/V ranges stay whole).
  * A larger one serves too. cache_dtype: dtype, or PA_FP8_E4M3 for
  * pa_cross_attention_fp8. Writes *bytes.
  */

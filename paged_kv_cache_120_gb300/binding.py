@@ -486,7 +486,8 @@ def pa_cross_attention_workspace_size(num_seqs, max_seqlen_q, num_q_heads, num_k
 
 
 def cross_attention_workspace(query, kv_cache, num_seqs, max_seqlen_q):
-    """A uint8 workspace tensor for the cross attention calls of this shape, or None for an empty one."""
+    """A uint8 workspace tensor with which the cross attention calls split the K/V ranges of this shape, or None when
+    they would not."""
     import torch
     _, hq, d = query.shape
     _, _, bs, hkv, _ = kv_cache.shape

@@ -412,7 +412,6 @@ struct PrefillParams {
                         //  first query head}
     float scale_log2;   // scale * log2(e) (* k_scale with an FP8 cache)
     float v_scale;      // 1, or the FP8 cache's V scale
-    int *counter;       // cross, whole units: the next unit, in the caller's workspace (null: dealt out in turn)
 };
 
 // One work unit: the two adjacent query tiles A = 2 qp and B = 2 qp + 1 of
@@ -495,7 +494,7 @@ __device__ __forceinline__ bool unit_of(const PrefillParams &p, const uint8_t *o
     }
     const int T = p.rows_per_head;
     const int ta = 2 * (p.q_pairs - 1 - qr) * T;
-    if (ta >= q_len || (CROSS && L == 0))  // L == 0: cross attention to nothing, zero rows (written by zero_rows)
+    if (ta >= q_len || (CROSS && SK && L == 0))  // cross attention to nothing: zero_rows
         return false;
     w.s = s;
     w.h = h;
@@ -511,8 +510,33 @@ __device__ __forceinline__ bool unit_of(const PrefillParams &p, const uint8_t *o
     return true;
 }
 
+// Claim a CTA of this grid that has not started: the answer, 16 bytes at dst,
+// completes bar's transaction; the claimed CTA will not run.
+__device__ __forceinline__ void claim_cta(uint32_t dst, uint32_t bar)
+{
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(dst),
+                 "r"(bar)
+                 : "memory");
+}
+
+// The claimed CTA's index, -1 if none was left (no claim may follow then).
+__device__ __forceinline__ int claimed_cta(uint32_t answer)
+{
+    int cta;
+    asm volatile(
+        "{\n\t.reg .b128 a;\n\t.reg .b64 lo, hi;\n\t.reg .pred p;\n\t"
+        "ld.shared.v2.b64 {lo, hi}, [%1];\n\tmov.b128 a, {lo, hi};\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\tmov.b32 %0, -1;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, a;\n\t}"
+        : "=r"(cta)
+        : "r"(answer)
+        : "memory");
+    return cta;
+}
+
 // Cross attention hands each unit's fields around with its index, so that the
-// roles neither divide nor load lengths between two units (XXX).
+// roles neither divide nor load lengths between two units (800 units of one K/V
+// tile: 32.5 us dividing and loading, 29.1 us so).
 struct UnitFields {
     int s, h, ht, q0, q_len, L, ta, pad;
 };
@@ -538,9 +562,10 @@ __device__ __forceinline__ void get_unit(const UnitFields *from, int T, Unit &w)
     w.n[1] = w.t0[1] < w.q_len ? w.n[0] : 0;
 }
 
-// Cross attention to a sequence without cached tokens gives zero rows: they
-// have no work unit, so the CTAs' softmax threads (tid < 256) write them,
-// sequence by sequence, before they wait for their first unit.
+// Cross attention to a sequence without cached tokens gives zero rows. Whole
+// units of it are items without tiles, whose rows the softmax threads write;
+// under stream-K, which shares out tiles, the CTAs' softmax threads (tid < 256)
+// write them, sequence by sequence, before they wait for their first item.
 template <int D>
 __device__ __forceinline__ void zero_rows(const PrefillParams &p, int tid)
 {
@@ -592,6 +617,9 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
     extern __shared__ uint8_t smem_raw[];
     __shared__ PrefillBars bars;
     constexpr bool CROSS = KIND != kCausal, SOLO = KIND == kCrossSolo;
+    constexpr bool kEmptyItems = CROSS && !SPLIT;  // items of sequences without tokens
+    __shared__ __align__(16) uint4 claim[1];  // cross, whole units: the answer to a claim
+    __shared__ uint64_t claim_bar;
     __shared__ __align__(16) UnitFields fields[CROSS ? kUnitSlots : 1];
     __shared__ uint8_t order[CROSS && !SPLIT ? kOrderedSeqs : 1];  // the sequences, longest first
     __shared__ float2 solo_ml[SOLO ? kM : 1];  // (reference maximum, row sum) of B's rows
@@ -635,6 +663,8 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
         mbar_init(b_q, 1);
         mbar_init(b_qr, 256);  // the 8 softmax warps
         mbar_init(b_qe, 1);
+        if constexpr (CROSS && !SPLIT)
+            mbar_init(smem_addr(&claim_bar), 1);
         if constexpr (SOLO) {
             mbar_init(smem_addr(&solo_bars[0]), 128);
             mbar_init(smem_addr(&solo_bars[1]), 128);
@@ -806,8 +836,27 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
             __syncwarp();
         }
         if (lane == 0) {
-            int *next = CROSS ? p.counter : &g_prefill_sched[p.sched_slot][0];
-            int dealt = blockIdx.x;
+            int *next = &g_prefill_sched[p.sched_slot][0];
+            // Cross, whole units: the grid has a CTA per unit; this one starts
+            // with its own and then takes over CTAs that have not started, one
+            // at a time, until none is left. Nothing outlives the launch: no
+            // counter to clear, and captured launches share none (40 x up to
+            // 224 queries over 1 .. 1500 states: 76.8 us with a counter cleared
+            // before the launch, 81 us dealt out in turn, 71 us so; 39 x 243
+            // over up to 16941: 557, 632 and 530 us; 8 x 1024 over 6404: 626,
+            // 628 and 645 us).
+            int taken = 0;
+            auto next_cross = [&]() {
+                if (taken++ == 0)
+                    return (int)blockIdx.x;
+                fence_proxy_async();  // the last answer has been read
+                mbar_expect_tx(smem_addr(&claim_bar), 16);
+                claim_cta(smem_addr(claim), smem_addr(&claim_bar));
+                if (!wait_or_fail(smem_addr(&claim_bar), (taken & 1)))
+                    return p.num_units;
+                const int cta = claimed_cta(smem_addr(claim));
+                return cta < 0 ? p.num_units : cta;
+            };
             // Stream-K walk: unit (ws, hh, qr) holds tiles [Tu, Tu + nu).
             int hh = 0, qr = 0, wq_len = 0, wL = 0, nu = 0;
             bool wok = false;
@@ -834,6 +883,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
             auto cta_of = [&](long long t) { return (int)(((t + 1) * G - 1) / W); };
             if constexpr (SPLIT)
                 p.jobs[blockIdx.x] = make_int4(-1, 0, 0, 0);
+            [[maybe_unused]] int loaded = 0;
             for (int i = 0;; ++i) {
                 Unit w;
                 Item it = {-1, 0, 0, 0, 0};
@@ -873,8 +923,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                 } else {
                     int u;
                     do {
-                        u = CROSS && !p.counter ? dealt : atomicAdd(next, 1);
-                        dealt += gridDim.x;
+                        u = CROSS ? next_cross() : atomicAdd(next, 1);
                     } while (u < p.num_units && !unit_of<false, CROSS>(p, order, u, w, true));
                     if (u < p.num_units) {
                         it.u = u;
@@ -896,7 +945,10 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                 mbar_arrive(b_uf(sl));
                 if (it.u < 0)
                     break;
-                if (i > 0 && !wait_or_fail(b_qe, (i - 1) & 1))
+                if (kEmptyItems && w.L == 0)
+                    continue;  // no queries to bring
+                const int qi = kEmptyItems ? loaded++ : i;  // items whose queries were brought before
+                if (qi > 0 && !wait_or_fail(b_qe, (qi - 1) & 1))
                     break;
                 const int head0 = w.h * p.group + w.ht * HPC;
                 const int tiles = SOLO || w.n[1] > 0 ? 2 : 1;
@@ -1003,6 +1055,8 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                                 is_k ? 0 : 1);
                 }
             };
+            if (kEmptyItems && n == 0)
+                continue;
             issue(it.j0);
             for (int j = it.j0; j < n; ++j, ++gc) {
                 const int st = gc % stages;
@@ -1082,6 +1136,8 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                 Unit w;
                 if (!take_unit(i, 1u, true, it, w) || it.u < 0)
                     break;
+                if (kEmptyItems && w.L == 0)
+                    continue;
                 // Tiles j0 <= j < j1 of the unit; tile x reads those below its ne[x].
                 const int j0 = SPLIT ? it.j0 : 0;
                 const int j1 = SPLIT ? min(max(w.n[0], w.n[1]), it.j1) : max(w.n[0], w.n[1]);
@@ -1218,17 +1274,31 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
         const int r = quarter * 32 + lane;  // this thread's TMEM lane (row)
         const int g = r / T, t = r - g * T;
         const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-        if constexpr (CROSS)
+        if constexpr (CROSS && SPLIT)
             zero_rows<D>(p, tid);
         float sc = p.scale_log2;  // this row's score factor (base 2)
         const bool sc_pos = sc >= 0.f;
         int gx = 0, vbase = 0;  // tiles of this query tile, and V tiles of the CTA, so far
         bool alive = true;
+        int empty = 0;  // items without tiles so far
         for (int i = 0; alive; ++i) {
             Item it;
             Unit w;
             if (!take_unit(i, kFull, lane == 0, it, w) || it.u < 0)
                 break;
+            if constexpr (kEmptyItems) {
+                if (w.L == 0) {
+                    if ((!SOLO || x == 0) && g < HPC && w.t0[x] + t < w.q_len) {
+                        uint4 *row = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) +
+                            ((long long)(w.q0 + w.t0[x] + t) * p.num_q_heads + w.h * p.group + w.ht * HPC + g) * D);
+                        for (int k = 0; k < D / 8; ++k)
+                            row[k] = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    ++empty;
+                    continue;
+                }
+            }
+            const int ni = i - empty;  // items with tiles before this one
             // This tile reads K/V tiles j0 <= j < nx of the item's j0 .. j1.
             const int j0 = SPLIT ? it.j0 : 0;
             const int j1 = SPLIT ? min(max(w.n[0], w.n[1]), it.j1) : max(w.n[0], w.n[1]);
@@ -1250,7 +1320,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                 // no overflow. This thread also owns score row r, so 2^e
                 // joins its score factor. A row holding Inf or NaN keeps
                 // e = 0 (and yields NaN, as the definition does).
-                if (!__all_sync(kFull, wait_or_fail(b_q, i & 1))) {
+                if (!__all_sync(kFull, wait_or_fail(b_q, ni & 1))) {
                     alive = false;
                     break;
                 }
@@ -1474,7 +1544,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                     tc_fence_before();
                     mbar_arrive(smem_addr(&solo_bars[0]));
                 }
-                if (!__all_sync(kFull, wait_or_fail(smem_addr(&solo_bars[x]), i & 1))) {
+                if (!__all_sync(kFull, wait_or_fail(smem_addr(&solo_bars[x]), ni & 1))) {
                     alive = false;
                     break;
                 }
@@ -1821,7 +1891,6 @@ namespace {
 // one CTA per SM, however many pieces that cuts a unit into (the merge
 // spreads a unit's pieces over several threads per row).
 constexpr int kSplitUnitsPerSm = 4;
-constexpr size_t kCounterBytes = 256;  // cross attention's workspace for its unit counter
 
 struct LaunchPlan {
     int heads_per_cta, head_tiles, rows_per_head, q_pairs;
@@ -1988,13 +2057,8 @@ int prefill_impl(const char *who, void *out, const void *query, const void *kv_c
     prm.max_len = max_blocks_per_seq * block_size;
     prm.scale_log2 = scale * 1.4426950408889634f * (fp8 ? k_scale : 1.f);
     prm.v_scale = fp8 ? v_scale : 1.f;
-    prm.counter = cross && !split ? static_cast<int *>(workspace) : nullptr;
     prm.num_kv_heads = num_kv_heads;
     prm.num_units = (int)lp.units;
-    if (cross && !split && workspace &&
-        (workspace_bytes < kCounterBytes || (reinterpret_cast<uintptr_t>(workspace) & 255)))
-        return set_error(PA_ERR_WORKSPACE, "%s: workspace of %zu bytes at %p (need %zu, 256-byte aligned)", who,
-                         workspace_bytes, workspace, kCounterBytes);
     prm.part_o = split ? static_cast<float *>(workspace) : nullptr;
     prm.part_ml = split ? reinterpret_cast<float2 *>(static_cast<float *>(workspace) +
                                                      (size_t)lp.split_grid * 2 * 2 * kM * head_size)
@@ -2048,13 +2112,10 @@ int prefill_impl(const char *who, void *out, const void *query, const void *kv_c
         }
     }
     // Persistent grid: one CTA per SM (the CTA holds 225 KB of shared
-    // memory), never more CTAs than units; G CTAs under stream-K.
-    const dim3 grid(split ? (unsigned)lp.split_grid : (unsigned)std::min<long long>(lp.units, sms));
-    if (prm.counter) {
-        e = cudaMemsetAsync(prm.counter, 0, sizeof(int), reinterpret_cast<cudaStream_t>(stream));
-        if (e != cudaSuccess)
-            return set_error(PA_ERR_CUDA, "%s: unit counter: %s", who, cudaGetErrorString(e));
-    }
+    // memory), never more CTAs than units; G CTAs under stream-K. Cross
+    // attention's whole units are a CTA each, claimed by those that run.
+    const dim3 grid(split ? (unsigned)lp.split_grid
+                          : (unsigned)std::min<long long>(lp.units, cross ? lp.units : (long long)sms));
     void *args[] = {&kv_map, &q_map, &prm};
     e = cudaLaunchKernel(fn, grid, dim3(threads_for(fp8)), args, kSmemBytes, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess)
@@ -2212,8 +2273,5 @@ extern "C" int pa_cross_attention_workspace_size(int num_seqs, int max_seqlen_q,
     if (num_seqs > 0 && max_seqlen_q > 0 && cross_rows_fit(num_seqs, max_seqlen_q, num_q_heads, num_kv_heads, block_size))
         return cross_rows_workspace(num_seqs, max_seqlen_q, num_q_heads, num_kv_heads, head_size, dtype,
                                     cache_dtype == PA_FP8_E4M3, bytes);
-    const int rc2 = pa_prefill_workspace_size(num_seqs, max_seqlen_q, num_q_heads, num_kv_heads, head_size, bytes);
-    if (rc2 == PA_OK && num_seqs > 0 && max_seqlen_q > 0)
-        *bytes = std::max(*bytes, kCounterBytes);
-    return rc2;
+    return pa_prefill_workspace_size(num_seqs, max_seqlen_q, num_q_heads, num_kv_heads, head_size, bytes);
 }

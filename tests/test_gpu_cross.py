@@ -370,8 +370,8 @@ def test_a_pool_past_2_to_the_32_bytes(dev):
 
 
 def test_two_graphs_at_once_share_nothing(dev):
-    """Two captured calls of many work units each, replayed on two streams at once, over and over: each takes its units
-    from its own workspace."""
+    """Two captured calls of many work units each, replayed on two streams at once, over and over: each takes only its
+    own units."""
     import torch
     rng = np.random.default_rng(19)
     cases = [CrossCase(dev, workloads.F16, 8, 8, 64, rng.integers(100, 400, 60), rng.integers(1, 600, 60), seed=20 + k)
@@ -401,8 +401,8 @@ def test_two_graphs_at_once_share_nothing(dev):
 def test_workspace_rules(dev):
     """The size asked for serves; less, or a misaligned one, is refused, whichever form the shape takes."""
     import torch
-    for qlen, kv in (([1, 1], [100, 200]), ([40, 30], [100, 200]), ([400] * 130, [64] * 130)):
-        c = CrossCase(dev, workloads.F16, 8, 2 if len(qlen) == 2 else 8, 64, qlen, kv, seed=25)
+    for qlen, kv in (([1, 1], [100, 200]), ([40, 30], [100, 200])):
+        c = CrossCase(dev, workloads.F16, 8, 2, 64, qlen, kv, seed=25)
         n = binding.pa_cross_attention_workspace_size(len(qlen), c.max_q, c.hq, c.hkv, 64, 16, binding.PA_F16, binding.PA_F16)
         big = torch.empty(n + 512, dtype=torch.uint8, device=dev)
         c.check(c.run(big[:n]))
@@ -411,4 +411,10 @@ def test_workspace_rules(dev):
             with pytest.raises(binding.PAError) as e:
                 c.run(bad)
             assert e.value.code == binding.PA_ERR_WORKSPACE
+    # Many work units: no workspace is wanted, one given all the same is left alone.
+    c = CrossCase(dev, workloads.F16, 8, 8, 64, [400] * 130, [64] * 130, seed=25)
+    assert c.workspace() is None
+    other = torch.full((512,), 7, dtype=torch.uint8, device=dev)
+    c.check(c.run(other))
+    assert bool((other == 7).all())
     assert binding.pa_get_device_error() == 0
