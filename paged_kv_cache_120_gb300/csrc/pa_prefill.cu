@@ -42,8 +42,10 @@
 //    score exceeds it by 2^8, so O is rarely rescaled), row sum of the
 //    rounded values, P into tensor memory. At the unit's end, O / l.
 //  * Cross attention of more rows (pa_cross_attention) is the same kernel
-//    without the causal limit; if no chunk passes one query tile, both halves
-//    of the tensor memory work on that tile (SOLO).
+//    without the causal limit; its whole units are CTAs of the grid, longest
+//    sequences first, that running CTAs take over (cluster launch control); if
+//    no chunk passes one query tile, both halves of the tensor memory work on
+//    that tile (SOLO).
 //  * Every wait is bounded; K/V rows past a sequence's end (padding slots,
 //    possibly NaN) are zeroed before P V reads them.
 #include <cuda.h>
@@ -597,7 +599,7 @@ struct PrefillBars {
 };
 
 // SPLIT: the stream-K instance (few units, K/V ranges shared out evenly);
-// otherwise whole units from a counter.
+// otherwise whole units from a counter (cross attention: from the grid).
 // KIND: what a query sees, its position's causal prefix or (cross attention)
 // all L cached tokens, and whether the chunks fit one query tile. A template
 // parameter because a runtime flag costs the causal kernel 1 - 8 %.
@@ -627,8 +629,8 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int T = p.rows_per_head, HPC = p.heads_per_cta;
-    // Persistent: the Q warp takes the next unit from the launch's counter
-    // (skipping units without queries) and hands it to every role through
+    // Persistent: the Q warp takes the next unit from the launch's counter or
+    // grid (skipping units without queries) and hands it to every role through
     // a small ring; the TMA rings and barrier phases run on across units.
 
     const uint32_t raw = smem_addr(smem_raw);
