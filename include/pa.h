@@ -516,7 +516,7 @@ int pa_rope_and_cache_fp8(void *query_out, const void *query, const void *key, c
  *                  partial results. Its contents need no initialisation and are
  *                  not preserved; calls that share it must not overlap on the
  *                  GPU. NULL: K/V ranges stay whole (same result up to fp32
- *                  rounding, slower where the size is not 0). Too small or
+ *                  rounding, may be slower where the size is not 0). Too small or
  *                  misaligned: PA_ERR_WORKSPACE.
  *   flags          0 or PA_DECODE_SHARED_BLOCKS (tables share blocks)
  * Bad offsets, lengths and block ids are handled as pa_prefill handles them

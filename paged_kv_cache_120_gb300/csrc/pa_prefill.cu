@@ -764,7 +764,13 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
         // stream-K, CTA c takes tiles [c W / G, (c + 1) W / G) of the W K/V
         // tiles of all units laid end to end (G CTAs), cut at unit ends.
         const int H = p.num_kv_heads * p.head_tiles;  // units of one query pair of a sequence
-        auto seq_tiles = [&](int s, bool flag) {     // K/V tiles of one head tile of sequence s
+        // Stream-K lays the units end to end by weight: their tiles, and for
+        // cross attention, whose units may have as little as one, kUnitCost
+        // more in front of them for the time between two units (8 sequences x 1024
+        // queries over 1 .. 6404 states, 8 heads, FP8: 252 us by tiles alone, 133 so).
+        constexpr int kUnitCost = CROSS ? 2 : 0;
+        auto weight = [](int tiles) { return tiles > 0 ? tiles + kUnitCost : 0; };
+        auto seq_tiles = [&](int s, bool flag) {     // weight of one head tile of sequence s
             const int q0 = p.cu_q[s], q_len = p.cu_q[s + 1] - q0, L = p.seq_lens[s];
             if (!seq_ok<CROSS>(p, q0, q_len, L)) {
                 if (flag)
@@ -773,7 +779,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
             }
             long long a = 0;
             for (int qr = 0; qr < p.q_pairs; ++qr)
-                a += pair_tiles<CROSS>(p, q_len, L, qr);
+                a += weight(pair_tiles<CROSS>(p, q_len, L, qr));
             return a;
         };
         long long lo = 0, hi = 0, W = 0, Ts = 0;  // this CTA's tiles [lo, hi); sequence ws starts at tile Ts
@@ -869,7 +875,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                 wL = p.seq_lens[ws];
                 wok = seq_ok<CROSS>(p, q0, wq_len, wL);
             };
-            auto tiles_here = [&]() { return wok ? pair_tiles<CROSS>(p, wq_len, wL, qr) : 0; };
+            auto tiles_here = [&]() { return wok ? weight(pair_tiles<CROSS>(p, wq_len, wL, qr)) : 0; };
             if (SPLIT && lo < hi) {
                 enter_seq();
                 const long long a = seq_tiles(ws, false);
@@ -893,9 +899,9 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                     if (pos < hi && nu > 0 && Tu <= pos && pos < Tu + nu) {
                         it.u = ((ws * H) + hh) * p.q_pairs + qr;
                         const long long end = min(Tu + nu, hi);
-                        it.j0 = (int)(pos - Tu);
-                        it.j1 = (int)(end - Tu);
-                        it.clo = cta_of(Tu);
+                        it.j0 = max((int)(pos - Tu) - kUnitCost, 0);
+                        it.j1 = (int)(end - Tu) - kUnitCost;
+                        it.clo = cta_of(Tu + kUnitCost);
                         it.chi = cta_of(Tu + nu - 1);
                         pos = end;
                         // On to the next unit with tiles (bounded: every step
@@ -916,7 +922,9 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                             if (nu > 0)
                                 break;
                         }
-                        if (!unit_of<true, CROSS>(p, order, it.u, w, false))
+                        if (CROSS && it.j1 <= 0)
+                            it.u = -1;  // the share ends before the unit's first tile
+                        else if (!unit_of<true, CROSS>(p, order, it.u, w, false))
                             it.u = -1;
                         else if (it.j0 == 0 && it.chi > it.clo)  // this CTA holds the unit's first piece
                             p.jobs[blockIdx.x] = make_int4(it.chi, w.q0 + w.t0[0], w.q_len - w.t0[0],
@@ -2011,6 +2019,21 @@ int check_call(const char *who, const void *out, const void *query, const void *
     return PA_OK;
 }
 
+// Whether a cross batch of few units shares their tiles out or takes them
+// whole. Whole units leave SMs idle in the last round: ceil(u) - 0.75 u units
+// an SM (u: units per SM; 0.75: sequences are rarely all of the longest
+// length), of the longest sequence's tiles and the two that a unit costs
+// itself. Sharing costs about 9 + 5 u tiles (partial results, their merge, the
+// cut units). Measured, 8 heads of 128, FP8 cache, shared against whole: 0.8
+// units an SM over 400 / 1404 / 6404 states 35 / 51 / 117 and 18 / 31 / 118 us
+// (78 and 102 over 1 .. 6404), 0.1 an SM 20 / 23 / 33 and 17 / 29 / 100, 2.1 an
+// SM 57 / 91 / 262 and 45 / 87 / 336.
+bool cross_splits(long long units, int sms, long long max_len)
+{
+    const double u = (double)units / sms, tiles = (double)((max_len + kN - 1) / kN) + 2.0;
+    return (std::ceil(u) - 0.75 * u) * tiles > 9.0 + 5.0 * u;
+}
+
 int prefill_impl(const char *who, void *out, const void *query, const void *kv_cache, const int32_t *block_tables,
                  int max_blocks_per_seq, const int32_t *cu_seqlens_q, const int32_t *seq_lens, int num_seqs,
                  int total_q, int max_seqlen_q, float scale, int num_q_heads, int num_kv_heads, int head_size,
@@ -2034,10 +2057,12 @@ int prefill_impl(const char *who, void *out, const void *query, const void *kv_c
     if (lp.units > 0x7fffffffLL)
         return set_error(PA_ERR_UNSUPPORTED, "%s: too many query tiles", who);
     // Stream-K needs the workspace; without one the launch takes whole units.
-    const bool split = lp.split_grid > 0 && workspace != nullptr;
+    bool split = lp.split_grid > 0 && workspace != nullptr;
     if (split && (workspace_bytes < lp.split_bytes || (reinterpret_cast<uintptr_t>(workspace) & 255)))
         return set_error(PA_ERR_WORKSPACE, "%s: workspace of %zu bytes at %p (need %zu, 256-byte aligned)", who,
                          workspace_bytes, workspace, lp.split_bytes);
+    if (cross)
+        split = split && cross_splits(lp.units, sms, (long long)max_blocks_per_seq * block_size);
 
     PrefillParams prm;
     prm.out = out;

@@ -202,6 +202,20 @@ def test_the_largest_batch_of_short_queries(dev, heads, most, fp8):
     CrossCase(dev, workloads.BF16, *heads, qlen, rng.integers(0, 40, 4096), fp8=fp8, seed=most).both()
 
 
+@pytest.mark.parametrize("fp8", [False, True], ids=["16bit", "fp8"])
+@pytest.mark.parametrize("heads,qlen,kv", [
+    ((8, 8, 128), [300] * 6, [4000, 1, 1, 129, 0, 256]),            # long and one-tile units in one share
+    ((2, 1, 64), [40, 1, 7], [1, 5000, 1]),                         # shares that hold only the cost of a unit
+    ((8, 8, 64), [1] * 18 + [200], [1] * 18 + [6000]),              # many one-tile units ahead of a long one
+    ((8, 8, 128), [100] * 9, [6400, 0, 1, 6400, 1, 1, 1, 1, 130])])
+def test_shares_of_units_of_one_tile_and_of_many(dev, heads, qlen, kv, fp8):
+    """K/V ranges shared out by weight: cuts before, in and behind units of one tile."""
+    CrossCase(dev, workloads.F16, *heads, qlen, kv, fp8=fp8, seed=len(kv)).both()
+    for cut in range(1, 4):  # the cuts move with the total
+        CrossCase(dev, workloads.F16, *heads, qlen, [max(0, n - 128 * cut) if n > 1000 else n for n in kv], fp8=fp8,
+                  seed=cut).both()
+
+
 @pytest.mark.parametrize("n", [1, 31, 33, 64, 127, 128, 129, 200])
 def test_batches_taken_longest_first(dev, n):
     """Around the batch size up to which whole units go by length: equal lengths, zeros, one far longer than the rest."""
