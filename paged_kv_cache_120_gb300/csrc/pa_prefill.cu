@@ -1916,8 +1916,8 @@ LaunchPlan plan_launch(int num_seqs, int max_seqlen_q, int num_q_heads, int num_
     lp.heads_per_cta = group < 16 ? group : 16;
     lp.head_tiles = group / lp.heads_per_cta;
     lp.rows_per_head = (kM / lp.heads_per_cta) & ~7;
-    const int q_tiles = (max_seqlen_q + lp.rows_per_head - 1) / lp.rows_per_head;
-    lp.q_pairs = (q_tiles + 1) / 2;
+    const long long q_tiles = ((long long)max_seqlen_q + lp.rows_per_head - 1) / lp.rows_per_head;
+    lp.q_pairs = (int)((q_tiles + 1) / 2);
     lp.units = (long long)lp.q_pairs * num_seqs * num_kv_heads * lp.head_tiles;
     lp.split_grid = 0;
     lp.split_bytes = 0;
@@ -2053,7 +2053,15 @@ int prefill_impl(const char *who, void *out, const void *query, const void *kv_c
     rc = current_sms(who, &dev, &sms);
     if (rc != PA_OK)
         return rc;
-    const LaunchPlan lp = plan_launch(num_seqs, max_seqlen_q, num_q_heads, num_kv_heads, head_size, sms);
+    LaunchPlan lp = plan_launch(num_seqs, max_seqlen_q, num_q_heads, num_kv_heads, head_size, sms);
+    // A bound above total_q says no more than total_q: whole units are planned
+    // for that, so that none is looked at in vain (the split, whose workspace
+    // was sized by the caller's bound, keeps to it: it has few units).
+    if (cross && lp.split_grid == 0 && max_seqlen_q > total_q) {
+        max_seqlen_q = total_q;
+        lp = plan_launch(num_seqs, max_seqlen_q, num_q_heads, num_kv_heads, head_size, sms);
+        lp.split_grid = 0;
+    }
     if (lp.units > 0x7fffffffLL)
         return set_error(PA_ERR_UNSUPPORTED, "%s: too many query tiles", who);
     // Stream-K needs the workspace; without one the launch takes whole units.

@@ -160,6 +160,14 @@ def test_a_few_candidates_each(dev, heads, most, fp8):
     CrossCase(dev, workloads.BF16, *heads, qlen, kv, fp8=fp8, seed=most).both()
 
 
+@pytest.mark.parametrize("most", [700, 10 ** 6, 2 ** 31 - 1])
+def test_a_bound_far_above_all_the_queries(dev, most):
+    """It means no more than total_q: no unit is taken in vain, nothing overflows."""
+    c = CrossCase(dev, workloads.F16, 8, 8, 64, [3, 1, 300, 0, 40, 2], [100, 300, 50, 9, 0, 700])
+    for ws in (binding.cross_attention_workspace(c.q, c.pool, 6, most), None):
+        c.check(c.run(ws, max_q=most))
+
+
 def test_a_larger_bound_than_the_longest_chunk(dev):
     c = CrossCase(dev, workloads.F16, 8, 2, 128, [1, 2, 1], [100, 300, 50])
     for most in (2, 3, 4, 5, 40, 1000):
