@@ -48,6 +48,7 @@
 #include <cudaTypedefs.h>
 
 #include <cmath>
+#include <cfloat>
 #include <cstdint>
 #include <mutex>
 
@@ -662,7 +663,10 @@ __global__ void __launch_bounds__(decode_warps<D, NT, FP8, RAGGED>() * 32, decod
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                m_run[nt][e] = -INFINITY;
+                // The least finite value, not -inf: a tile of nothing but -inf
+                // or NaN scores then weighs its -inf ones 0 (-inf - m is no
+                // NaN), and a piece of such tiles is no empty share.
+                m_run[nt][e] = -FLT_MAX;
                 l_run[nt][e] = 0.f;
             }
 #pragma unroll
@@ -1060,7 +1064,8 @@ struct MergeState {
 // Fold the pieces o = o_first, o_first + ostep, ... <= o_hi into the state.
 // Piece o's record is slot first_slot when o == o_lo, else 2o. PPR pieces
 // are loaded per round (m, l and the O rows together) and folded with the
-// online-softmax rule; a piece with m = -inf (an empty share) weighs 0. The
+// online-softmax rule; m = -inf marks an empty share, which weighs 0 (a piece
+// that saw tiles has m >= -FLT_MAX, whatever its scores). The
 // state holds CN * 8 of a record's NT * 8 columns, from column c0 on.
 template <int D, int NT, int CN>
 __device__ void fold_pieces(const float *recs, int o_first, int ostep, int o_hi, int o_lo,
