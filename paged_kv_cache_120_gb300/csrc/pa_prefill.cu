@@ -1736,10 +1736,10 @@ __global__ void __launch_bounds__(256) paged_prefill_merge_kernel(const PrefillP
         L[k] = 0.f;
         A[k][0] = A[k][1] = A[k][2] = A[k][3] = 0.f;
     }
-    // Fold one state (m, l, o) into (M, L, A): the online rule.
+    // Fold one state (m, l, o) into (M, L, A): the online rule. m = -inf is a
+    // piece without a finite score: l and o are 0 (no visible token, or only
+    // scores of -inf), or they hold Inf or NaN, which stay.
     auto fold = [](float &Mk, float &Lk, float *Ak, float m, float l, float o0, float o1, float o2, float o3) {
-        if (m == -INFINITY)
-            return;  // an empty piece (no visible token): weight 0
         if (m > Mk) {
             const float alpha = ex2(Mk - m);  // 0 while M is -inf
             Lk *= alpha;

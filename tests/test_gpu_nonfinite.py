@@ -185,3 +185,79 @@ def test_decode_a_few_candidates(dev):
         c.q[4, 0, 100] = INF
         c.reference()
         c.check(c.run_cross(True))
+
+
+# --------------------------------------------------------- the chunk kernel
+
+CHUNKS = [((4, 4, 64), [300, 3], "pairs"), ((8, 2, 128), [200, 40], "pairs")]
+
+
+@pytest.mark.parametrize("split", [False, True], ids=["whole", "split"])
+@pytest.mark.parametrize("dtype,fp8", TYPES, ids=IDS)
+@pytest.mark.parametrize("heads,qlen,kind", CHUNKS, ids=lambda x: str(x) if isinstance(x, str) else "x".join(map(str, x)))
+def test_chunk_nan_keys_of_a_whole_share(dev, heads, qlen, kind, dtype, fp8, split):
+    """One NaN state behind a full K/V tile, and whole tiles of them, at many places: they are all that a query tile or a
+    piece of a split range sees."""
+    n = len(qlen)
+    for L, width, starts in ((129, 1, (128,)), (2048, 128, range(0, 2048, 384)), (2049, 1, (0, 1920, 2048)),
+                             (2000, 256, (128, 1792))):
+        if split and L < 2000:
+            continue
+        for start in starts:
+            c = Poisoned(dev, dtype, *heads, qlen, [L] * n, fp8=fp8, seed=start + n, extra_width=60)
+            for w in windows(L, width, [start]):
+                c.put(0, n - 1, w, NAN)
+            c.reference()
+            c.check(c.run_cross(split))
+
+
+@pytest.mark.parametrize("split", [False, True], ids=["whole", "split"])
+@pytest.mark.parametrize("value", [INF, -INF], ids=["+inf", "-inf"])
+@pytest.mark.parametrize("heads,qlen,kind", CHUNKS, ids=lambda x: str(x) if isinstance(x, str) else "x".join(map(str, x)))
+def test_chunk_infinite_keys(dev, heads, qlen, kind, value, split):
+    n = len(qlen)
+    for dtype, sign, scale in ((workloads.F16, 1, None), (workloads.BF16, -1, None), (workloads.F16, 0, None),
+                               (workloads.BF16, 0, -0.1)):
+        for L, width, start in ((129, 1, 128), (2048, 128, 0), (2048, 128, 640), (2049, 1, 2048), (2000, 256, 1792)):
+            if split and L < 2000:
+                continue
+            c = Poisoned(dev, dtype, *heads, qlen, [L] * n, seed=L + start, scale=scale, extra_width=60)
+            if sign:
+                c.sign_of_first(sign)
+            c.put(0, n - 1, windows(L, width, [start])[0], value)
+            c.reference()
+            c.check(c.run_cross(split))
+
+
+@pytest.mark.parametrize("split", [False, True], ids=["whole", "split"])
+@pytest.mark.parametrize("dtype,fp8", TYPES, ids=IDS)
+@pytest.mark.parametrize("heads,qlen,kind", CHUNKS, ids=lambda x: str(x) if isinstance(x, str) else "x".join(map(str, x)))
+def test_chunk_values_that_are_not_finite(dev, heads, qlen, kind, dtype, fp8, split):
+    """Also behind keys so far below the others that their weights are 0 (0 * NaN is NaN)."""
+    n = len(qlen)
+    for L, width, start in ((256, 128, 128), (2048, 128, 640), (2049, 1, 2048)):
+        if split and L < 2000:
+            continue
+        c = Poisoned(dev, dtype, *heads, qlen, [L] * n, fp8=fp8, seed=L, extra_width=60)
+        w = windows(L, width, [start])[0]
+        c.put(1, n - 1, w, NAN, dims=slice(5, 9))
+        if not fp8:
+            c.sign_of_first(1)
+            c.put(0, n - 1, w, -60000.0)  # scores of -60000 * 0.125 * scale and less
+        c.reference()
+        c.check(c.run_cross(split))
+
+
+@pytest.mark.parametrize("split", [False, True], ids=["whole", "split"])
+@pytest.mark.parametrize("dtype,fp8", TYPES, ids=IDS)
+@pytest.mark.parametrize("heads,qlen", [((4, 4, 64), [300, 3]), ((8, 2, 128), [33, 70])], ids=["4x4x64", "8x2x128"])
+def test_causal_keys_that_are_not_finite(dev, heads, qlen, dtype, fp8, split):
+    """pa_prefill: rows before the state are untouched, those behind it follow the definition."""
+    n = len(qlen)
+    for value in (NAN,) if fp8 else (NAN, INF, -INF):
+        for L, width, start in ((2048, 128, 0), (2048, 128, 640), (2049, 1, 2048), (2000, 256, 1664), (2000, 1, 1999 - 40)):
+            c = Poisoned(dev, dtype, *heads, qlen, [L] * n, fp8=fp8, seed=L + start, extra_width=60)
+            c.causal = True
+            c.put(0, n - 1, windows(L, width, [start])[0], value)
+            c.reference()
+            c.check(c.run_prefill(split))
