@@ -1547,7 +1547,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
             float o[32];
             // Solo: B leaves its rows' states for A and waits until A has
             // read its O; A folds them into its own.
-            float fa = 1.f, fb = 0.f;  // weights of A's and B's O
+            float fa = 1.f, fb = 1.f;  // weights of A's and B's O
             if constexpr (SOLO) {
                 if (x == 1) {
                     solo_ml[r] = work ? make_float2(m_run, l_run) : make_float2(-INFINITY, 0.f);
@@ -1561,12 +1561,12 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                 tc_fence_after();
                 if (x == 1)
                     continue;
+                // m = -inf: no finite score, so l and O are 0 or hold Inf or
+                // NaN, which any weight but 0 keeps.
                 const float2 b = solo_ml[r];
                 const float m = fmaxf(m_run, b.x);
-                if (b.x != -INFINITY) {
-                    fa = m_run == -INFINITY ? 0.f : ex2(m_run - m);
-                    fb = ex2(b.x - m);
-                }
+                fa = m_run == -INFINITY ? 1.f : ex2(m_run - m);
+                fb = b.x == -INFINITY ? 1.f : ex2(b.x - m);
                 l_run = l_run * fa + b.y * fb;
                 m_run = m;
             }
@@ -1584,7 +1584,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                     tc_ld32(tO(1) + lane_off + c * 32, ob);
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        o[i] = o[i] * fa + (fb != 0.f ? ob[i] * fb : 0.f);
+                        o[i] = o[i] * fa + ob[i] * fb;  // a weight of 0 too: 0 * NaN is NaN
                 }
             };
             auto store_row = [&](int c, const float *v, float inv) {

@@ -189,7 +189,8 @@ def test_decode_a_few_candidates(dev):
 
 # --------------------------------------------------------- the chunk kernel
 
-CHUNKS = [((4, 4, 64), [300, 3], "pairs"), ((8, 2, 128), [200, 40], "pairs")]
+CHUNKS = [((4, 4, 64), [100], "solo"), ((8, 2, 128), [30, 7, 32], "solo"), ((4, 4, 64), [300, 3], "pairs"),
+          ((8, 2, 128), [200, 40], "pairs")]
 
 
 @pytest.mark.parametrize("split", [False, True], ids=["whole", "split"])
