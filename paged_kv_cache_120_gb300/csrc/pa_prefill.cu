@@ -1599,8 +1599,8 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                 }
             };
             if (whole) {
-                // O / l for the valid rows.
-                const float inv = l_run > 0.f ? p.v_scale / l_run : 0.f;
+                // O / l for the valid rows (l = 0: every score is -inf, 0 / 0).
+                const float inv = p.v_scale / l_run;
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {
                     load_o(c);
@@ -1795,7 +1795,7 @@ __global__ void __launch_bounds__(256) paged_prefill_merge_kernel(const PrefillP
             continue;
         const int r = rb * Geo::kBlockRows + k * kRows + rsub;
         const int g = r / T, t = r - g * T;
-        const float inv = L[k] > 0.f ? p.v_scale / L[k] : 0.f;
+        const float inv = p.v_scale / L[k];
         uint16_t *out = static_cast<uint16_t *>(p.out) +
                         ((long long)(job.y + x * T + t) * p.num_q_heads + job.w + g) * D + tpr * 4;
         *reinterpret_cast<uint2 *>(out) =

@@ -262,3 +262,17 @@ def test_causal_keys_that_are_not_finite(dev, heads, qlen, dtype, fp8, split):
             c.put(0, n - 1, windows(L, width, [start])[0], value)
             c.reference()
             c.check(c.run_prefill(split))
+
+
+@pytest.mark.parametrize("split", [False, True], ids=["whole", "split"])
+@pytest.mark.parametrize("qlen", [[100], [300]])
+def test_rows_whose_every_score_is_minus_infinity(dev, qlen, split):
+    """0 / 0: NaN, as the decode kernels give it."""
+    c = Poisoned(dev, workloads.F16, 4, 4, 64, qlen, [2000], seed=6, extra_width=60).sign_of_first(1)
+    c.put(0, 0, np.arange(2000), -INF)
+    c.reference()
+    assert bool(c.want.isnan().all())
+    c.check(c.run_cross(split))
+    c.causal = True
+    c.reference()
+    c.check(c.run_prefill(split))
