@@ -1475,15 +1475,15 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                 else
                     fill(std::false_type{});
                 if (sc == 0.f && kb + kN - 1 > pos) {
-                    // Scale 0: a masked score would have given 0 x inf = NaN.
-                    // Every visible token weighs 2^-ref, every masked one 0.
-                    const float pv = ex2(-ref);
+                    // Scale 0: a masked score gave 0 x inf = NaN; its weight
+                    // is 0. The visible ones keep theirs, 2^-ref, or NaN
+                    // where the score itself is infinite or NaN.
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         l8[i] = 0.f;
 #pragma unroll
                     for (int c = 0; c < kN / 2; ++c) {
-                        pw[c] = pack2<kMmaBF16>(kb + 2 * c <= pos ? pv : 0.f, kb + 2 * c + 1 <= pos ? pv : 0.f);
+                        pw[c] &= (kb + 2 * c <= pos ? 0xFFFFu : 0u) | (kb + 2 * c + 1 <= pos ? 0xFFFF0000u : 0u);
                         l8[c & 7] = add_pair<kMmaBF16>(l8[c & 7], pw[c]);
                     }
                 }

@@ -276,3 +276,17 @@ def test_rows_whose_every_score_is_minus_infinity(dev, qlen, split):
     c.causal = True
     c.reference()
     c.check(c.run_prefill(split))
+
+
+@pytest.mark.parametrize("qlen", [[1, 1], [100, 3], [300, 3]])
+def test_scale_zero_times_infinity(dev, qlen):
+    """0 * inf and 0 * NaN are NaN, in a sequence's last, partly filled tile as in a full one."""
+    for L in (40, 128, 200):
+        for value in (NAN, INF):
+            c = Poisoned(dev, workloads.F16, 8, 2, 64, qlen, [L, 90], seed=7, scale=0.0)
+            c.put(0, 0, [L - 9], value)
+            c.reference()
+            c.check(c.run(None))
+            ws = c.workspace()
+            if ws is not None:
+                c.check(c.run(ws))
