@@ -1470,7 +1470,10 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                         }
                     }
                 };
-                if (__all_sync(kFull, fabsf(ref) < 0x1p20f))
+                // Cross attention's rows without a query (another sequence's, or
+                // whatever shared memory held) have no say in it: they are never
+                // stored, and a stored row's bits must not depend on them.
+                if (__all_sync(kFull, (CROSS && !valid) || fabsf(ref) < 0x1p20f))
                     fill(std::true_type{});
                 else
                     fill(std::false_type{});
