@@ -13,9 +13,9 @@
 //  * Work units. A unit is two adjacent 128-row query tiles (A and B) of
 //    one (sequence, kv head, head tile); rows are (query head of the group,
 //    query token) pairs, so the heads sharing a kv head, and both tiles,
-//    share every K/V tile. One persistent CTA per SM takes units from a
-//    per-launch counter (warp 11, which also loads each unit's Q) and hands
-//    them to every role through a small ring; TMA rings and barrier phases
+//    share every K/V tile. One persistent CTA per SM takes units from the
+//    launch's grid, a CTA per unit, by cluster launch control (warp 11,
+//    which also loads each unit's Q) and hands them to every role through a small ring; TMA rings and barrier phases
 //    run on across units.
 //  * Few units (a few long sequences with short chunks). With at most four
 //    units per SM and a workspace, the CTAs instead take equal contiguous
@@ -57,7 +57,6 @@
 #include <cmath>
 #include <cstdint>
 #include <algorithm>
-#include <atomic>
 #include <mutex>
 #include <type_traits>
 
@@ -68,12 +67,6 @@
 namespace pa {
 
 __device__ int g_prefill_error;  // PA_DEVERR_* bits of the prefill kernels
-
-// Work-unit counters of in-flight prefill launches: {next unit, CTAs done}
-// per slot; a launch takes slot (launch number % 64), the last CTA to finish
-// puts both back to 0.
-constexpr int kSchedSlots = 64;
-__device__ int g_prefill_sched[kSchedSlots][2];
 
 // Stream-K launches (few work units): at most this many units.
 constexpr int kMaxSplitUnits = 1024;
@@ -406,7 +399,6 @@ struct PrefillParams {
     int max_len;        // max_blocks_per_seq * block_size
     int num_kv_heads;
     int num_units;      // q_pairs * num_seqs * num_kv_heads * head_tiles
-    int sched_slot;     // this launch's row of g_prefill_sched
     float *part_o;      // stream-K: partial O rows [CTA][slot 2][tile 2][128][D] fp32
     float2 *part_ml;    // stream-K: partial (reference maximum, row sum) [CTA][slot 2][tile 2][128]
     int4 *jobs;         // stream-K: per CTA c, the split unit whose first piece c holds (kNoJob: none):
@@ -421,7 +413,7 @@ struct PrefillParams {
 // queries come later, so B sees at least as many tiles as A). With qp =
 // q_pairs - 1 - qr, units are numbered heaviest first, u = ((qr * num_seqs
 // + s) * num_kv_heads + h) * head_tiles + ht, when each CTA takes whole
-// units from a counter; sequence-major, u = ((s * num_kv_heads + h) *
+// units; sequence-major, u = ((s * num_kv_heads + h) *
 // head_tiles + ht) * q_pairs + qr, when CTAs take equal shares of the
 // tiles (stream-K), so that a sequence's units lie side by side. Cross
 // attention always numbers sequence-major: its units of a sequence and head
@@ -599,7 +591,7 @@ struct PrefillBars {
 };
 
 // SPLIT: the stream-K instance (few units, K/V ranges shared out evenly);
-// otherwise whole units from a counter (cross attention: from the grid).
+// otherwise whole units, each a CTA of the grid.
 // KIND: what a query sees, its position's causal prefix or (cross attention)
 // all L cached tokens, and whether the chunks fit one query tile. A template
 // parameter because a runtime flag costs the causal kernel 1 - 8 %.
@@ -620,7 +612,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
     __shared__ PrefillBars bars;
     constexpr bool CROSS = KIND != kCausal, SOLO = KIND == kCrossSolo;
     constexpr bool kEmptyItems = CROSS && !SPLIT;  // items of sequences without tokens
-    __shared__ __align__(16) uint4 claim[1];  // cross, whole units: the answer to a claim
+    __shared__ __align__(16) uint4 claim[1];  // whole units: the answer to a claim
     __shared__ uint64_t claim_bar;
     __shared__ __align__(16) UnitFields fields[CROSS ? kUnitSlots : 1];
     __shared__ uint8_t order[CROSS && !SPLIT ? kOrderedSeqs : 1];  // the sequences, longest first
@@ -629,8 +621,8 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int T = p.rows_per_head, HPC = p.heads_per_cta;
-    // Persistent: the Q warp takes the next unit from the launch's counter or
-    // grid (skipping units without queries) and hands it to every role through
+    // Persistent: the Q warp takes the next unit from the launch's grid
+    // (skipping units without queries) and hands it to every role through
     // a small ring; the TMA rings and barrier phases run on across units.
 
     const uint32_t raw = smem_addr(smem_raw);
@@ -665,7 +657,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
         mbar_init(b_q, 1);
         mbar_init(b_qr, 256);  // the 8 softmax warps
         mbar_init(b_qe, 1);
-        if constexpr (CROSS && !SPLIT)
+        if constexpr (!SPLIT)
             mbar_init(smem_addr(&claim_bar), 1);
         if constexpr (SOLO) {
             mbar_init(smem_addr(&solo_bars[0]), 128);
@@ -760,7 +752,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
         // ------------------------------------------------------------ Q
         // Scheduler and Q: find this CTA's next work item, hand it on, and
         // load its two query tiles once the previous item's last S = Q K^T
-        // has completed. Whole units come from the launch's counter; under
+        // has completed. Whole units come from the launch's grid; under
         // stream-K, CTA c takes tiles [c W / G, (c + 1) W / G) of the W K/V
         // tiles of all units laid end to end (G CTAs), cut at unit ends.
         const int H = p.num_kv_heads * p.head_tiles;  // units of one query pair of a sequence
@@ -844,17 +836,19 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
             __syncwarp();
         }
         if (lane == 0) {
-            int *next = &g_prefill_sched[p.sched_slot][0];
-            // Cross, whole units: the grid has a CTA per unit; this one starts
-            // with its own and then takes over CTAs that have not started, one
-            // at a time, until none is left. Nothing outlives the launch: no
-            // counter to clear, and captured launches share none (40 x up to
-            // 224 queries over 1 .. 1500 states: 76.8 us with a counter cleared
-            // before the launch, 81 us dealt out in turn, 71 us so; 39 x 243
-            // over up to 16941: 557, 632 and 530 us; 8 x 1024 over 6404: 626,
-            // 628 and 645 us).
+            // Whole units: the grid has a CTA per unit; this one starts with
+            // its own and then takes over CTAs that have not started, one at a
+            // time, until none is left. Nothing outlives the launch: there is
+            // no counter to clear, and none that two captured launches, or
+            // launches on two streams, could share. Cross attention, 40 x up
+            // to 224 queries over 1 .. 1500 states: 76.8 us with a counter
+            // cleared before the launch, 81 us dealt out in turn, 71 us so;
+            // 39 x 243 over up to 16941: 557, 632 and 530 us; 8 x 1024 over
+            // 6404: 626, 628 and 645 us. Causal, against a counter in the
+            // library: 8 x 512 queries of 40 heads 150 and 145 us (FP8 181 and
+            // 168), 16 x 512 of 32/8 heads 194 and 181 us (FP8 242 and 215).
             int taken = 0;
-            auto next_cross = [&]() {
+            auto next_unit = [&]() {
                 if (taken++ == 0)
                     return (int)blockIdx.x;
                 fence_proxy_async();  // the last answer has been read
@@ -933,7 +927,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                 } else {
                     int u;
                     do {
-                        u = CROSS ? next_cross() : atomicAdd(next, 1);
+                        u = next_unit();
                     } while (u < p.num_units && !unit_of<false, CROSS>(p, order, u, w, true));
                     if (u < p.num_units) {
                         it.u = u;
@@ -1648,17 +1642,6 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    // Every role has left its loop, so this CTA takes no more units; the
-    // last CTA to get here resets the launch's counters for the next use
-    // (a stream-K launch uses none).
-    if (!SPLIT && !CROSS && tid == 0) {
-        __threadfence();
-        if (atomicAdd(&g_prefill_sched[p.sched_slot][1], 1) == (int)gridDim.x - 1) {
-            g_prefill_sched[p.sched_slot][0] = 0;
-            g_prefill_sched[p.sched_slot][1] = 0;
-            __threadfence();
-        }
-    }
     if (warp == kWarpMMA)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols)
                      : "memory");
@@ -1897,9 +1880,8 @@ using namespace pa;
 
 namespace {
 
-// A launch's work units and scheduling. With enough units, each of
-// min(units, SMs) persistent CTAs takes whole units, heaviest first, from a
-// counter. With few (at most kSplitUnitsPerSm per SM, and a workspace), the
+// A launch's work units and scheduling. With enough units, persistent CTAs
+// take whole units, heaviest first, from the launch's grid. With few (at most kSplitUnitsPerSm per SM, and a workspace), the
 // units' K/V tiles are dealt out in equal contiguous shares (stream-K) to
 // one CTA per SM, however many pieces that cuts a unit into (the merge
 // spreads a unit's pieces over several threads per row).
@@ -2060,7 +2042,7 @@ int prefill_impl(const char *who, void *out, const void *query, const void *kv_c
     // A bound above total_q says no more than total_q: whole units are planned
     // for that, so that none is looked at in vain (the split, whose workspace
     // was sized by the caller's bound, keeps to it: it has few units).
-    if (cross && lp.split_grid == 0 && max_seqlen_q > total_q) {
+    if (lp.split_grid == 0 && max_seqlen_q > total_q) {
         max_seqlen_q = total_q;
         lp = plan_launch(num_seqs, max_seqlen_q, num_q_heads, num_kv_heads, head_size, sms);
         lp.split_grid = 0;
@@ -2102,9 +2084,6 @@ int prefill_impl(const char *who, void *out, const void *query, const void *kv_c
                                                      (size_t)lp.split_grid * 2 * 2 * kM * head_size)
                         : nullptr;
     prm.jobs = split ? reinterpret_cast<int4 *>(prm.part_ml + (size_t)lp.split_grid * 2 * 2 * kM) : nullptr;
-    // Prefill's counters live in the library, a slot per launch in turn.
-    static std::atomic<unsigned> launches{0};
-    prm.sched_slot = cross ? 0 : (int)(launches.fetch_add(1u) % (unsigned)kSchedSlots);
 
     CUtensorMap kv_map, q_map;
     rc = fp8 ? encode_kv_map_fp8(&kv_map, kv_cache, num_blocks, block_size, num_kv_heads, head_size)
@@ -2149,11 +2128,9 @@ int prefill_impl(const char *who, void *out, const void *query, const void *kv_c
             done = dev < 64;
         }
     }
-    // Persistent grid: one CTA per SM (the CTA holds 225 KB of shared
-    // memory), never more CTAs than units; G CTAs under stream-K. Cross
-    // attention's whole units are a CTA each, claimed by those that run.
-    const dim3 grid(split ? (unsigned)lp.split_grid
-                          : (unsigned)std::min<long long>(lp.units, cross ? lp.units : (long long)sms));
+    // One CTA per SM runs at a time (it holds 225 KB of shared memory): G
+    // CTAs under stream-K, else a CTA per unit, claimed by those that run.
+    const dim3 grid(split ? (unsigned)lp.split_grid : (unsigned)lp.units);
     void *args[] = {&kv_map, &q_map, &prm};
     e = cudaLaunchKernel(fn, grid, dim3(threads_for(fp8)), args, kSmemBytes, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess)
