@@ -161,6 +161,14 @@ def _fp8_pool(t, name):
     return _dev(t, name)
 
 
+def _pool_dims(kv_cache):
+    """(blocks, block size, kv heads, head size) of a pool, which holds K and V: libpa finds V behind K's blocks."""
+    shape = kv_cache.shape
+    if len(shape) != 5 or shape[0] != 2:
+        raise PAError(PA_ERR_INVALID_ARG, f"kv_cache must be (2, num_blocks, block_size, num_kv_heads, head_size), not {tuple(shape)}")
+    return shape[1:]
+
+
 def _dev(t, name):
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor")
@@ -207,7 +215,7 @@ def pa_last_error() -> str:
 
 def pa_reshape_and_cache(key, value, kv_cache, slot_mapping, stream=None) -> None:
     """key/value [T, Hkv, D], kv_cache (2, NB, B, Hkv, D), slot_mapping [T] int32."""
-    _, nb, bs, hkv, d = kv_cache.shape
+    nb, bs, hkv, d = _pool_dims(kv_cache)
     _check(lib().pa_reshape_and_cache(
         _dev(key, "key"), _dev(value, "value"), _dev(kv_cache, "kv_cache"),
         _dev(slot_mapping, "slot_mapping"), int(slot_mapping.shape[0]), nb, bs, hkv, d,
@@ -226,7 +234,7 @@ def decode_workspace(query, kv_cache):
     """A correctly sized uint8 workspace tensor for pa_decode on this batch shape."""
     import torch
     s, hq, d = query.shape
-    _, _, bs, hkv, _ = kv_cache.shape
+    _, bs, hkv, _ = _pool_dims(kv_cache)
     n = pa_decode_workspace_size(s, hq, hkv, d, bs, _dtype_code(kv_cache))
     return torch.empty(max(n, 256), dtype=torch.uint8, device=query.device)
 
@@ -237,7 +245,7 @@ def pa_decode(out, query, kv_cache, block_tables, seq_lens, scale, workspace,
     seq_lens [S] int32; workspace: uint8 CUDA tensor (see decode_workspace);
     flags: an OR of PA_DECODE_SHARED_BLOCKS and PA_DECODE_LENS_READY (0 = none)."""
     s, hq, d = query.shape
-    _, nb, bs, hkv, _ = kv_cache.shape
+    nb, bs, hkv, _ = _pool_dims(kv_cache)
     _check(lib().pa_decode(
         _dev(out, "out"), _dev(query, "query"), _dev(kv_cache, "kv_cache"),
         _dev(block_tables, "block_tables"), int(block_tables.shape[1]),
@@ -251,7 +259,7 @@ def pa_decode_static_scratch(out, query, kv_cache, block_tables, seq_lens, scale
     """pa_decode without a workspace: the scratch is the library's static
     device array (for callers that cannot allocate device memory)."""
     s, hq, d = query.shape
-    _, nb, bs, hkv, _ = kv_cache.shape
+    nb, bs, hkv, _ = _pool_dims(kv_cache)
     _check(lib().pa_decode_static_scratch(
         _dev(out, "out"), _dev(query, "query"), _dev(kv_cache, "kv_cache"),
         _dev(block_tables, "block_tables"), int(block_tables.shape[1]),
@@ -263,7 +271,7 @@ def pa_reshape_and_cache_fp8(key, value, kv_cache, slot_mapping, k_scale, v_scal
                              stream=None) -> None:
     """key/value [T, Hkv, D] fp16/bf16; kv_cache (2, NB, B, Hkv, D) of E4M3 codes
     (uint8 or float8_e4m3fn); slot_mapping [T] int32."""
-    _, nb, bs, hkv, d = kv_cache.shape
+    nb, bs, hkv, d = _pool_dims(kv_cache)
     _check(lib().pa_reshape_and_cache_fp8(
         _dev(key, "key"), _dev(value, "value"), _fp8_pool(kv_cache, "kv_cache"),
         _dev(slot_mapping, "slot_mapping"), int(slot_mapping.shape[0]), nb, bs, hkv, d,
@@ -282,7 +290,7 @@ def decode_fp8_workspace(query, kv_cache):
     """A correctly sized uint8 workspace tensor for pa_decode_fp8 on this batch shape."""
     import torch
     s, hq, d = query.shape
-    _, _, bs, hkv, _ = kv_cache.shape
+    _, bs, hkv, _ = _pool_dims(kv_cache)
     n = pa_decode_fp8_workspace_size(s, hq, hkv, d, bs, _dtype_code(query))
     return torch.empty(max(n, 256), dtype=torch.uint8, device=query.device)
 
@@ -291,7 +299,7 @@ def pa_decode_fp8(out, query, kv_cache, block_tables, seq_lens, scale, k_scale, 
                   workspace, flags=0, stream=None) -> None:
     """pa_decode over an E4M3 pool; out/query fp16 or bf16 [S, Hq, D]."""
     s, hq, d = query.shape
-    _, nb, bs, hkv, _ = kv_cache.shape
+    nb, bs, hkv, _ = _pool_dims(kv_cache)
     _check(lib().pa_decode_fp8(
         _dev(out, "out"), _dev(query, "query"), _fp8_pool(kv_cache, "kv_cache"),
         _dev(block_tables, "block_tables"), int(block_tables.shape[1]),
@@ -318,7 +326,7 @@ def prefill_workspace(query, kv_cache, num_seqs, max_seqlen_q):
     the K/V ranges of this shape, or None when they would not split."""
     import torch
     _, hq, d = query.shape
-    hkv = kv_cache.shape[3]
+    _, _, hkv, _ = _pool_dims(kv_cache)
     n = pa_prefill_workspace_size(num_seqs, max_seqlen_q, hq, hkv, d)
     return torch.empty(n, dtype=torch.uint8, device=query.device) if n else None
 
@@ -329,7 +337,7 @@ def pa_prefill(out, query, kv_cache, block_tables, cu_seqlens_q, seq_lens, scale
     cu_seqlens_q [S + 1] int32; seq_lens [S] int32 (chunk included); max_seqlen_q: host int;
     workspace: None (no K/V split) or a uint8 CUDA tensor (see prefill_workspace)."""
     total_q, hq, d = query.shape
-    _, nb, bs, hkv, _ = kv_cache.shape
+    nb, bs, hkv, _ = _pool_dims(kv_cache)
     ws, ws_bytes = _workspace_args(workspace)
     _check(lib().pa_prefill(
         _dev(out, "out"), _dev(query, "query"), _dev(kv_cache, "kv_cache"),
@@ -342,9 +350,9 @@ def pa_prefill(out, query, kv_cache, block_tables, cu_seqlens_q, seq_lens, scale
 def pa_prefill_fp8(out, query, kv_cache, block_tables, cu_seqlens_q, seq_lens, scale, max_seqlen_q,
                    k_scale, v_scale, workspace=None, stream=None) -> None:
     """pa_prefill over an E4M3 byte pool (2, NB, B, Hkv, D) uint8; out/query 16-bit."""
-    _fp8_pool(kv_cache, "kv_cache")
     total_q, hq, d = query.shape
-    _, nb, bs, hkv, _ = kv_cache.shape
+    nb, bs, hkv, _ = _pool_dims(kv_cache)
+    _fp8_pool(kv_cache, "kv_cache")
     ws, ws_bytes = _workspace_args(workspace)
     _check(lib().pa_prefill_fp8(
         _dev(out, "out"), _dev(query, "query"), _dev(kv_cache, "kv_cache"),
@@ -436,7 +444,7 @@ def _rope_args(query_out, query, key, value, kv_cache, slot_mapping, positions, 
     import torch
     shape, dt = query.shape, query.dtype
     tokens, hq, d = shape
-    _, nb, bs, hkv, dc = kv_cache.shape
+    nb, bs, hkv, dc = _pool_dims(kv_cache)
     dev = _device(query, "query")
     if dc != d:
         _bad(f"kv_cache holds heads of {dc}, the queries {d}")
@@ -471,10 +479,9 @@ def pa_rope_and_cache(query_out, query, key, value, kv_cache, slot_mapping, posi
 def pa_rope_and_cache_fp8(query_out, query, key, value, kv_cache, slot_mapping, positions, plan, k_scale, v_scale,
                           adjacent=False, stream=None) -> None:
     """pa_rope_and_cache into a pool of E4M3 codes (uint8 or float8_e4m3fn)."""
+    args = _rope_args(query_out, query, key, value, kv_cache, slot_mapping, positions, plan, adjacent)
     _fp8_pool(kv_cache, "kv_cache")
-    _check(lib().pa_rope_and_cache_fp8(
-        *_rope_args(query_out, query, key, value, kv_cache, slot_mapping, positions, plan, adjacent),
-        _dtype_code(query), float(k_scale), float(v_scale), _stream(stream)))
+    _check(lib().pa_rope_and_cache_fp8(*args, _dtype_code(query), float(k_scale), float(v_scale), _stream(stream)))
 
 
 def pa_cross_attention_workspace_size(num_seqs, max_seqlen_q, num_q_heads, num_kv_heads, head_size, block_size, dtype,
@@ -490,7 +497,7 @@ def cross_attention_workspace(query, kv_cache, num_seqs, max_seqlen_q):
     they would not."""
     import torch
     _, hq, d = query.shape
-    _, _, bs, hkv, _ = kv_cache.shape
+    _, bs, hkv, _ = _pool_dims(kv_cache)
     n = pa_cross_attention_workspace_size(num_seqs, max_seqlen_q, hq, hkv, d, bs, _dtype_code(query), _pool_code(kv_cache))
     return torch.empty(n, dtype=torch.uint8, device=query.device) if n else None
 
@@ -499,7 +506,7 @@ def _cross_args(out, query, kv_cache, block_tables, cu_seqlens_q, kv_lens, scale
     import torch
     i32 = torch.int32
     total_q, hq, d = query.shape
-    _, nb, bs, hkv, dc = kv_cache.shape
+    nb, bs, hkv, dc = _pool_dims(kv_cache)
     s, width = block_tables.shape
     dev = _device(query, "query")
     if dc != d or out.shape != query.shape or out.dtype is not query.dtype:
@@ -527,15 +534,19 @@ def pa_cross_attention(out, query, kv_cache, block_tables, cu_seqlens_q, kv_lens
 def pa_cross_attention_fp8(out, query, kv_cache, block_tables, cu_seqlens_q, kv_lens, scale, max_seqlen_q, k_scale, v_scale,
                            workspace=None, flags=0, stream=None) -> None:
     """pa_cross_attention over a pool of E4M3 codes (uint8 or float8_e4m3fn)."""
-    _fp8_pool(kv_cache, "kv_cache")
     args, ws = _cross_args(out, query, kv_cache, block_tables, cu_seqlens_q, kv_lens, scale, max_seqlen_q, workspace)
+    _fp8_pool(kv_cache, "kv_cache")
     _check(lib().pa_cross_attention_fp8(*args, float(k_scale), float(v_scale), *ws, int(flags), _stream(stream)))
 
 
 def pa_copy_blocks(kv_caches, src_dst_pairs, stream=None) -> None:
     """kv_caches: list of per-layer pools (fp16, bf16, or E4M3 codes as uint8 /
     float8_e4m3fn); src_dst_pairs [N, 2] int32 CUDA tensor."""
-    _, nb, bs, hkv, d = kv_caches[0].shape
+    shape = kv_caches[0].shape
+    nb, bs, hkv, d = _pool_dims(kv_caches[0])
+    for c in kv_caches:
+        if c.shape != shape or c.dtype != kv_caches[0].dtype:
+            raise PAError(PA_ERR_INVALID_ARG, f"kv_caches differ: {tuple(c.shape)} {c.dtype}, {tuple(shape)} {kv_caches[0].dtype}")
     ptrs = (ctypes.c_void_p * len(kv_caches))(*[_dev(c, "kv_cache").value for c in kv_caches])
     _check(lib().pa_copy_blocks(ptrs, len(kv_caches), _dev(src_dst_pairs, "src_dst_pairs"),
                                 int(src_dst_pairs.shape[0]), nb, bs, hkv, d,
