@@ -294,8 +294,12 @@ __global__ void __launch_bounds__(kStepThreads) build_step_kernel(const StepPara
     }
     // 5. Given-back blocks that no row took stay on the free list.
     const uint32_t left = avail - pops;
-    for (uint32_t i = (uint32_t)n_free + me; i < left; i += step)
-        p.free_list[i] = popped(avail - 1u - i);
+    for (uint32_t i = (uint32_t)n_free + me; i < left; i += step) {
+        const int id = popped(avail - 1u - i);
+        if ((unsigned)id >= (unsigned)p.num_blocks)
+            step_raise(PA_DEVERR_BLOCK_ID);
+        p.free_list[i] = id;
+    }
 
     // 6. Lengths, offsets, counts: after every CTA has read the old ones.
     cluster_wait();
