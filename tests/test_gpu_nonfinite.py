@@ -251,6 +251,24 @@ def test_chunk_values_that_are_not_finite(dev, heads, qlen, kind, dtype, fp8, sp
 
 @pytest.mark.parametrize("split", [False, True], ids=["whole", "split"])
 @pytest.mark.parametrize("dtype,fp8", TYPES, ids=IDS)
+@pytest.mark.parametrize("heads,qlen,kind", CHUNKS, ids=lambda x: str(x) if isinstance(x, str) else "x".join(map(str, x)))
+def test_chunk_queries_that_are_not_finite(dev, heads, qlen, kind, dtype, fp8, split):
+    """Only their own rows are lost."""
+    c = Poisoned(dev, dtype, *heads, qlen, [2000] * len(qlen), fp8=fp8, seed=8, extra_width=60)
+    c.q[3, 0, 7] = NAN
+    c.q[5, 1] = NAN
+    c.q[6, 2, 11] = INF
+    c.q[int(c.cu[-1]) - 1, 3, 0] = -INF
+    c.reference()
+    assert not bool(c.want.isfinite().all()) and bool(c.want[4].isfinite().all())
+    c.check(c.run_cross(split))
+    c.causal = True
+    c.reference()
+    c.check(c.run_prefill(split))
+
+
+@pytest.mark.parametrize("split", [False, True], ids=["whole", "split"])
+@pytest.mark.parametrize("dtype,fp8", TYPES, ids=IDS)
 @pytest.mark.parametrize("heads,qlen", [((4, 4, 64), [300, 3]), ((8, 2, 128), [33, 70])], ids=["4x4x64", "8x2x128"])
 def test_causal_keys_that_are_not_finite(dev, heads, qlen, dtype, fp8, split):
     """pa_prefill: rows before the state are untouched, those behind it follow the definition."""
