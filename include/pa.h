@@ -179,8 +179,9 @@ int pa_decode_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads,
  * Result: out[s][hq] = sum_i softmax_i(scale * q.k_i) v_i over the
  * seq_lens[s] logical tokens, computed with fp32 dot products, an fp32
  * online softmax ([book] §4.6), split-K partial states merged with the same
- * (m, s, O) rule, and one rounding to dtype at the end. For a given device
- * and batch shape the result does not depend on where the blocks sit in
+ * (m, s, O) rule, and one rounding to dtype at the end. A NaN or +inf score
+ * makes its row NaN and a score of -inf weighs 0, as in the definition (here
+ * and in every attention call below). For a given device and batch shape the result does not depend on where the blocks sit in
  * the pool (bit-identical under any permutation of physical placement).
  * num_seqs must be <= 4096. Returns PA_OK or a PA_ERR_* code.
  */
@@ -468,8 +469,8 @@ int pa_rope_plan(const double *inv_freq, const int32_t *pair_axes, int num_pairs
  *   adjacent       0: pair i is dimensions (i, i + rot_dim / 2); else (2i, 2i + 1)
  *   head_size      a multiple of 8, <= 1024; num_tokens <= 2^30
  * Result: (x1, x2) becomes (x1 cos a - x2 sin a, x1 sin a + x2 cos a) in fp32,
- * rounded once to dtype (values that pass are bit copies); a is reduced exactly
- * (to 2^-31 turns) at any 32-bit position. Two tokens with the same slot race. Launched
+ * rounded once to dtype (values that pass are bit copies); a is off by at most
+ * about 2^-26 turns (1e-7 radians) at any 32-bit position. Two tokens with the same slot race. Launched
  * with programmatic dependent launch: it waits for the preceding kernel before
  * it reads anything. Returns PA_OK or a PA_ERR_* code.
  */
@@ -508,7 +509,11 @@ int pa_rope_and_cache_fp8(void *query_out, const void *query, const void *key, c
  *   num_seqs, total_q, max_seqlen_q, scale, num_q_heads, num_kv_heads,
  *   head_size, num_blocks, block_size, dtype: as for pa_prefill. Rows of query
  *   and out behind cu_seqlens_q[num_seqs] are not read for a result and not
- *   written. Several sequences may use the same blocks.
+ *   written. Several sequences may use the same blocks. max_seqlen_q and the
+ *   table's width (max_blocks_per_seq), not the lengths on the device, choose
+ *   the kernel and the split: the tightest bounds are the fastest. Single
+ *   queries under a bound for chunks run on 128-row tiles, and short sequences
+ *   in a table for far longer ones may be split where whole ranges are faster.
  *   kv_lens        device, [num_seqs] int32, in [0, max_blocks_per_seq *
  *                  block_size], longer or shorter than the queries
  *   workspace      device, NULL or >= pa_cross_attention_workspace_size(...)

@@ -2007,8 +2007,8 @@ int check_call(const char *who, const void *out, const void *query, const void *
 // Whether a cross batch of few units shares their tiles out or takes them
 // whole. Whole units leave SMs idle in the last round: ceil(u) - 0.75 u units
 // an SM (u: units per SM; 0.75: sequences are rarely all of the longest
-// length), of the longest sequence's tiles and the two that a unit costs
-// itself. Sharing costs about 9 + 5 u tiles (partial results, their merge, the
+// length), of the longest possible sequence's tiles (max_len, the width of the
+// table: the host knows no lengths) and the two that a unit costs itself. Sharing costs about 9 + 5 u tiles (partial results, their merge, the
 // cut units). Measured, 8 heads of 128, FP8 cache, shared against whole: 0.8
 // units an SM over 400 / 1404 / 6404 states 35 / 51 / 117 and 18 / 31 / 118 us
 // (78 and 102 over 1 .. 6404), 0.1 an SM 20 / 23 / 33 and 17 / 29 / 100, 2.1 an

@@ -11,11 +11,12 @@
 // pa_reshape_and_cache.
 //
 // Angles. Only the fraction of a turn matters, so f_i / 2 pi is kept as a
-// 64-bit fraction of a turn (pa_rope_plan) and multiplied by the integer
+// 62-bit fraction of a turn (pa_rope_plan) and multiplied by the integer
 // position modulo 2^64: the wrap-around is exact, and for any 32-bit position
-// the angle is off by at most 2^-32 turns, where an fp32 product would be off
+// the product is off by at most 2^-31 turns, where an fp32 product would be off
 // by a radian at a position of 10^7. The upper 32 bits as a signed number are
-// the angle in [-1, 1) half turns.
+// the angle in [-1, 1) half turns; rounded to fp32 for the sines it is off by
+// up to 2^-26 turns (1e-7 radians), far below a 16-bit rounding of the result.
 //
 // HBM-bound: per token the q row is read and written, the k and v rows read
 // and written once; the sines are computed once per unit, not per head.
