@@ -68,6 +68,8 @@ typedef struct CUstream_st *pa_stream_t;
 /* Element type of an FP8 pool (pa_copy_blocks only; the FP8 calls below take
  * the 16-bit type of their activations as `dtype`). */
 #define PA_FP8_E4M3  2
+/* Element type of rows of probabilities or logits (pa_verify_draft only). */
+#define PA_F32       3
 
 /* pa_decode flags. */
 #define PA_DECODE_SHARED_BLOCKS 1u  /* some physical block appears in more than one
@@ -86,6 +88,11 @@ typedef struct CUstream_st *pa_stream_t;
 #define PA_DEVERR_SEQ_LEN   4   /* a seq_len < 0 or > max_blocks_per_seq * block_size */
 #define PA_DEVERR_PAIR      8   /* a copy pair out of range, or a dst repeated / also a src */
 #define PA_DEVERR_TIMEOUT  16   /* a bounded wait inside a kernel gave up */
+#define PA_DEVERR_TREE     32   /* a drafted tree's parent that is no earlier node, an accepted path that
+                                   does not ascend, a row of probabilities without a positive finite sum */
+
+/* Nodes of one sequence's drafted tree at most. */
+#define PA_MAX_TREE_NODES 1024
 
 /* Library version (major * 10000 + minor * 100 + patch). */
 int pa_version(void);
@@ -560,6 +567,176 @@ int pa_cross_attention_fp8(void *out, const void *query, const void *kv_cache,
 int pa_cross_attention_workspace_size(int num_seqs, int max_seqlen_q, int num_q_heads,
                                       int num_kv_heads, int head_size, int block_size,
                                       int dtype, int cache_dtype, size_t *bytes);
+
+/* ------------------------------------------------------------------ */
+/* The speculative step. A drafter proposes a tree of tokens behind each */
+/* sequence; the model scores all of them in one pass; the tokens that   */
+/* its probabilities accept stay in the cache. The tree of sequence s is */
+/* its nodes cu_seqlens_q[s] .. cu_seqlens_q[s+1] - 1: node 0, the root,  */
+/* is the sequence's last token (sampled, not yet cached), and parents[] */
+/* holds each node's parent as an index within the sequence, smaller than */
+/* the node's own; -1 for the root and for unused nodes (padding), which   */
+/* nothing hangs from. Node i occupies position seq_lens[s] - n + i of the */
+/* cache (n nodes, seq_lens with them: what pa_build_step lays out) until  */
+/* pa_commit_draft has moved it, but its rotary position is the context's  */
+/* length plus its depth. A step: pa_build_step, pa_build_tree, per layer   */
+/* pa_rope_and_cache and pa_tree_attention, then pa_verify_draft and        */
+/* pa_commit_draft; all of it runs from a CUDA graph. The pages name no     */
+/* speculative decoding; this is the reading this library takes.            */
+/* ------------------------------------------------------------------ */
+
+/*
+ * pa_build_tree — the trees' positions and ancestor masks.
+ *
+ *   parents       device, [total_q] int32 (above). A parent that is neither -1
+ *                 nor an earlier node sets PA_DEVERR_TREE and counts as -1.
+ *   cu_seqlens_q  device, [num_seqs + 1] int32, as for pa_prefill
+ *   seq_lens      device, [num_seqs] int32: cached tokens, the nodes included
+ *   positions     device, [total_q] int32 out, or NULL: seq_lens[s] - n + depth
+ *                 (the root's and an unused node's depth is 0)
+ *   tree_masks    device, [total_q][mask_words] int32 out: bit j % 32 of word
+ *                 j / 32 is set when node j is the row's node or an ancestor
+ *   mask_words    1 .. 32; sequences have at most 32 * mask_words nodes
+ * num_seqs <= 4096. Sequences with inconsistent offsets, more nodes or a length
+ * below their nodes set PA_DEVERR_SEQ_LEN and are not written, nor are rows
+ * behind cu_seqlens_q[num_seqs]. One launch. Returns PA_OK or a PA_ERR_* code.
+ */
+int pa_build_tree(const int32_t *parents, const int32_t *cu_seqlens_q, const int32_t *seq_lens,
+                  int num_seqs, int total_q, int32_t *positions, int32_t *tree_masks,
+                  int mask_words, pa_stream_t stream);
+
+/*
+ * pa_tree_attention — attention of a tree's nodes over the paged cache: node i
+ * of sequence s, with n nodes and seq_lens[s] = L cached tokens (the nodes'
+ * K and V written), sees the context, tokens 0 .. L - n - 1, and token L - n + j
+ * for every bit j < n set in its mask. The masks of pa_build_tree give each
+ * node its ancestors and itself; any others may be passed. A row that sees
+ * nothing (no context, no bit) is zeros.
+ *
+ *   tree_masks    device, [total_q][mask_words] int32; max_seqlen_q <= 32 *
+ *                 mask_words
+ *   workspace     NULL or >= pa_tree_attention_workspace_size(...) bytes,
+ *                 256-byte aligned, as for pa_cross_attention
+ *   flags         0 or PA_DECODE_SHARED_BLOCKS (tables share blocks)
+ * Everything else is as for pa_prefill: shapes, limits, head sizes, types,
+ * handling of bad offsets, lengths and block ids. max_seqlen_q <=
+ * PA_MAX_TREE_NODES. What a row does not see does not reach it, whatever its
+ * K and V hold (NaN and infinities included). Few rows (nodes x query heads of a kv head
+ * <= 16, with a workspace) run on the decode kernels, more on tcgen05 tiles of
+ * 128; the bound max_seqlen_q chooses, so the tightest is the fastest.
+ * Deterministic for a given device, shape and workspace choice. Allocates
+ * nothing. Returns PA_OK or a PA_ERR_* code.
+ */
+int pa_tree_attention(void *out, const void *query, const void *kv_cache,
+                      const int32_t *block_tables, int max_blocks_per_seq,
+                      const int32_t *cu_seqlens_q, const int32_t *seq_lens,
+                      const int32_t *tree_masks, int mask_words, int num_seqs,
+                      int total_q, int max_seqlen_q, float scale,
+                      int num_q_heads, int num_kv_heads, int head_size,
+                      int num_blocks, int block_size, int dtype,
+                      void *workspace, size_t workspace_bytes, unsigned flags,
+                      pa_stream_t stream);
+
+/* pa_tree_attention over an FP8 pool, with pa_prefill_fp8's conventions. */
+int pa_tree_attention_fp8(void *out, const void *query, const void *kv_cache,
+                          const int32_t *block_tables, int max_blocks_per_seq,
+                          const int32_t *cu_seqlens_q, const int32_t *seq_lens,
+                          const int32_t *tree_masks, int mask_words, int num_seqs,
+                          int total_q, int max_seqlen_q, float scale,
+                          int num_q_heads, int num_kv_heads, int head_size,
+                          int num_blocks, int block_size, int dtype,
+                          float k_scale, float v_scale,
+                          void *workspace, size_t workspace_bytes, unsigned flags,
+                          pa_stream_t stream);
+
+/* Workspace bytes the tree attention calls want for this shape on the current
+ * device (0: none); arguments as for pa_cross_attention_workspace_size. */
+int pa_tree_attention_workspace_size(int num_seqs, int max_seqlen_q, int num_q_heads,
+                                     int num_kv_heads, int head_size, int block_size,
+                                     int dtype, int cache_dtype, size_t *bytes);
+
+/*
+ * pa_verify_draft — which nodes of each tree the target's rows accept, and the
+ * token that follows, from given random numbers. From the root on, at a node
+ * with the target's row p (the next token's distribution after it):
+ *   greedy  (uniforms NULL): y is p's largest entry (the first of equals; NaN
+ *           is passed over). The first child holding y is accepted, else y is
+ *           the sequence's new token. p may hold logits.
+ *   sample  (uniforms, draft NULL): y is drawn from p with the node's second
+ *           number; then as above. For children that were chosen, not drawn:
+ *           the law of the result is the target's.
+ *   draft   (uniforms and draft): the children were drawn, one after the other
+ *           and independently, from the drafter's row q of this node. With r =
+ *           p, Z = 1 at first, child x is accepted if u q(x) Z < r(x), u the
+ *           child's first number; refused, r becomes max(r - Z q, 0) and Z its
+ *           sum, and the next child is tried. When none is left, the new token is
+ *           drawn from r with the node's second number (from p if r is all
+ *           zero). The law of the result is the target's, whatever q is.
+ * A draw with u takes the first entry whose running sum exceeds u times the
+ * row's sum. Sums are held to about 46 bits.
+ *
+ *   num_accepted  device, [num_seqs] int32 out: nodes accepted, the root among
+ *                 them; 0 for a sequence without nodes
+ *   path          device, [total_q] int32 out: entry cu_seqlens_q[s] + k is the
+ *                 k-th accepted node, -1 behind them
+ *   tokens_out    device, [total_q] int32 out: the sequence's new tokens, as
+ *                 many as accepted nodes (the accepted drafted tokens, then the
+ *                 new one), -1 behind them
+ *   tokens, parents  device, [total_q] int32: each node's token (one outside the
+ *                 vocabulary is never accepted) and parent
+ *   target, draft device, rows of vocab_size entries, one per node, target_stride
+ *                 and draft_stride elements apart (>= vocab_size); row i is the
+ *                 distribution behind node i. Probabilities are taken as given:
+ *                 finite, summing to about 1. Entries not above 0 weigh 0.
+ *   dtype         PA_F16, PA_BF16 or PA_F32, of both
+ *   uniforms      device, [total_q][2] fp32 in [0, 1), or NULL
+ * num_seqs <= 4096, at most PA_MAX_TREE_NODES nodes a sequence. Outputs overlap
+ * no input. A sequence with inconsistent offsets sets PA_DEVERR_SEQ_LEN, and its
+ * count is 0. A row without a positive finite sum sets PA_DEVERR_TREE and gives
+ * token 0; so do bad parents (see pa_build_tree). One launch. Deterministic.
+ * Returns PA_OK or a PA_ERR_* code.
+ */
+int pa_verify_draft(int32_t *num_accepted, int32_t *path, int32_t *tokens_out,
+                    const int32_t *tokens, const int32_t *parents,
+                    const int32_t *cu_seqlens_q, int num_seqs, int total_q,
+                    const void *target, int64_t target_stride, const void *draft,
+                    int64_t draft_stride, int vocab_size, int dtype,
+                    const float *uniforms, pa_stream_t stream);
+
+/*
+ * pa_commit_draft — keep the accepted nodes of each tree: their K and V move, in
+ * every layer's pool, to the places behind the context (node path[k] to place
+ * k), the sequence's length becomes context + accepted nodes, and blocks behind
+ * that go back to the free list, as pa_build_step's finished rows do: row after
+ * row, the last logical block first. Bit copies; nodes already in place are not
+ * touched.
+ *
+ *   kv_caches     HOST array of num_layers device pointers, as for pa_copy_blocks
+ *   block_tables, max_blocks_per_seq, cu_seqlens_q: the step's. No two sequences
+ *                 hold the same block among those of their nodes.
+ *   seq_lens      device, [num_seqs] int32: lengths with the nodes
+ *   num_accepted, path  device, as pa_verify_draft writes them: path ascends.
+ *                 num_accepted may be 0: no node is kept. Not read for a sequence
+ *                 without nodes, whose length stays.
+ *   seq_lens_out  device, [num_seqs] int32; may be seq_lens itself
+ *   free_list     device, [num_blocks] int32, in and out, or NULL: blocks stay
+ *                 with their sequences (num_free and num_free_out are not used)
+ *   num_free, num_free_out  device, [1] int32; may be one
+ * num_seqs <= 4096. A sequence with inconsistent offsets, length or count sets
+ * PA_DEVERR_SEQ_LEN, one whose path does not ascend within its nodes
+ * PA_DEVERR_TREE; nothing of either moves, its length and blocks stay. A block
+ * id outside the pool sets PA_DEVERR_BLOCK_ID, and its token is not moved; so do
+ * a free count outside [0, num_blocks] and blocks returned beyond num_blocks,
+ * which are dropped. Two launches, the second programmatic. Returns PA_OK or a
+ * PA_ERR_* code.
+ */
+int pa_commit_draft(void *const *kv_caches, int num_layers, const int32_t *block_tables,
+                    int max_blocks_per_seq, const int32_t *cu_seqlens_q,
+                    const int32_t *seq_lens, const int32_t *num_accepted,
+                    const int32_t *path, int num_seqs, int total_q, int32_t *seq_lens_out,
+                    int32_t *free_list, const int32_t *num_free, int32_t *num_free_out,
+                    int num_blocks, int block_size, int num_kv_heads, int head_size,
+                    int dtype, pa_stream_t stream);
 
 /*
  * pa_get_device_error — read and clear the current device's error word

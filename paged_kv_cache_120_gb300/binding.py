@@ -26,6 +26,7 @@ PA_ERR_NOT_FOUND = -6
 PA_F16 = 0
 PA_BF16 = 1
 PA_FP8_E4M3 = 2
+PA_F32 = 3
 PA_DECODE_SHARED_BLOCKS = 1
 PA_DECODE_LENS_READY = 2
 PA_PCACHE_NO_CACHE = 1
@@ -34,6 +35,8 @@ PA_DEVERR_SLOT = 2
 PA_DEVERR_SEQ_LEN = 4
 PA_DEVERR_PAIR = 8
 PA_DEVERR_TIMEOUT = 16
+PA_DEVERR_TREE = 32
+PA_MAX_TREE_NODES = 1024
 
 # (name, restype, argtypes) of every exported function, in header order.
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
@@ -67,6 +70,15 @@ SIGNATURES = [
     ("pa_cross_attention_fp8", _i, [_vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _f, _i, _i, _i, _i, _i, _i, _f, _f,
                                     _vp, _sz, _u, _vp]),
     ("pa_cross_attention_workspace_size", _i, [_i, _i, _i, _i, _i, _i, _i, _i, ctypes.POINTER(_sz)]),
+    ("pa_build_tree", _i, [_vp, _vp, _vp, _i, _i, _vp, _vp, _i, _vp]),
+    ("pa_tree_attention", _i, [_vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _i, _i, _i, _i, _f, _i, _i, _i, _i, _i, _i,
+                               _vp, _sz, _u, _vp]),
+    ("pa_tree_attention_fp8", _i, [_vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _i, _i, _i, _i, _f, _i, _i, _i, _i, _i, _i, _f, _f,
+                                   _vp, _sz, _u, _vp]),
+    ("pa_tree_attention_workspace_size", _i, [_i, _i, _i, _i, _i, _i, _i, _i, ctypes.POINTER(_sz)]),
+    ("pa_verify_draft", _i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _vp, _i64, _vp, _i64, _i, _i, _vp, _vp]),
+    ("pa_commit_draft", _i, [ctypes.POINTER(_vp), _i, _vp, _i, _vp, _vp, _vp, _vp, _i, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _i,
+                             _i, _vp]),
     ("pa_copy_blocks", _i, [ctypes.POINTER(_vp), _i, _vp, _i, _i, _i, _i, _i, _i, _vp]),
     ("pa_get_device_error", _i, [_ip]),
     ("pa_alloc_create", _vp, [_i, _i, _i32p]),
@@ -537,6 +549,133 @@ def pa_cross_attention_fp8(out, query, kv_cache, block_tables, cu_seqlens_q, kv_
     args, ws = _cross_args(out, query, kv_cache, block_tables, cu_seqlens_q, kv_lens, scale, max_seqlen_q, workspace)
     _fp8_pool(kv_cache, "kv_cache")
     _check(lib().pa_cross_attention_fp8(*args, float(k_scale), float(v_scale), *ws, int(flags), _stream(stream)))
+
+
+def _masks(tree_masks, total_q, index):
+    """(address, words of a row) of the nodes' mask rows, int32 [total_q, words]."""
+    import torch
+    if tree_masks.dim() != 2:
+        _bad(f"tree_masks must be [total_q, mask_words], not {tuple(tree_masks.shape)}")
+    words = tree_masks.shape[1]
+    return _ints(tree_masks, "tree_masks", total_q * words, index, torch.int32), words
+
+
+def pa_build_tree(parents, cu_seqlens_q, seq_lens, positions, tree_masks, stream=None) -> None:
+    """int32 CUDA tensors: parents [total_q] (index within the sequence, -1 for the root and unused nodes), cu_seqlens_q
+    [S + 1], seq_lens [S] (the nodes included); out: positions [total_q] or None, tree_masks [total_q, mask_words] (bit
+    j % 32 of word j / 32: node j is the row's node or an ancestor)."""
+    import torch
+    i32 = torch.int32
+    total, s = parents.numel(), seq_lens.numel()
+    dev = _device(parents, "parents")
+    masks, words = _masks(tree_masks, total, dev)
+    _check(lib().pa_build_tree(
+        _ints(parents, "parents", total, dev, i32), _ints(cu_seqlens_q, "cu_seqlens_q", s + 1, dev, i32),
+        _ints(seq_lens, "seq_lens", s, dev, i32), s, total,
+        None if positions is None else _ints(positions, "positions", total, dev, i32), masks, words, _stream(stream)))
+
+
+def pa_tree_attention_workspace_size(num_seqs, max_seqlen_q, num_q_heads, num_kv_heads, head_size, block_size, dtype,
+                                     cache_dtype) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().pa_tree_attention_workspace_size(int(num_seqs), int(max_seqlen_q), num_q_heads, num_kv_heads, head_size,
+                                                  block_size, dtype, cache_dtype, ctypes.byref(out)))
+    return out.value
+
+
+def tree_attention_workspace(query, kv_cache, num_seqs, max_seqlen_q):
+    """A uint8 workspace tensor for the tree attention calls of this shape, or None when they want none."""
+    import torch
+    _, hq, d = query.shape
+    _, bs, hkv, _ = _pool_dims(kv_cache)
+    n = pa_tree_attention_workspace_size(num_seqs, max_seqlen_q, hq, hkv, d, bs, _dtype_code(query), _pool_code(kv_cache))
+    return torch.empty(n, dtype=torch.uint8, device=query.device) if n else None
+
+
+def _tree_args(out, query, kv_cache, block_tables, cu_seqlens_q, seq_lens, tree_masks, scale, max_seqlen_q, workspace):
+    args, ws = _cross_args(out, query, kv_cache, block_tables, cu_seqlens_q, seq_lens, scale, max_seqlen_q, workspace)
+    return args[:7] + _masks(tree_masks, query.shape[0], query.get_device()) + args[7:], ws
+
+
+def pa_tree_attention(out, query, kv_cache, block_tables, cu_seqlens_q, seq_lens, tree_masks, scale, max_seqlen_q,
+                      workspace=None, flags=0, stream=None) -> None:
+    """out/query [total_q, Hq, D], a row per node; kv_cache (2, NB, B, Hkv, D) with the nodes' K and V behind the context;
+    block_tables [S, maxblk], cu_seqlens_q [S + 1], seq_lens [S] (the nodes included), tree_masks [total_q, mask_words]
+    int32 (see pa_build_tree); max_seqlen_q: host int, most nodes of a sequence; workspace: None or a uint8 CUDA tensor (see
+    tree_attention_workspace); flags: 0 or PA_DECODE_SHARED_BLOCKS."""
+    if kv_cache.dtype != query.dtype:
+        _bad(f"kv_cache is {kv_cache.dtype}, the queries {query.dtype}")
+    args, ws = _tree_args(out, query, kv_cache, block_tables, cu_seqlens_q, seq_lens, tree_masks, scale, max_seqlen_q, workspace)
+    _check(lib().pa_tree_attention(*args, *ws, int(flags), _stream(stream)))
+
+
+def pa_tree_attention_fp8(out, query, kv_cache, block_tables, cu_seqlens_q, seq_lens, tree_masks, scale, max_seqlen_q,
+                          k_scale, v_scale, workspace=None, flags=0, stream=None) -> None:
+    """pa_tree_attention over a pool of E4M3 codes (uint8 or float8_e4m3fn)."""
+    args, ws = _tree_args(out, query, kv_cache, block_tables, cu_seqlens_q, seq_lens, tree_masks, scale, max_seqlen_q, workspace)
+    _fp8_pool(kv_cache, "kv_cache")
+    _check(lib().pa_tree_attention_fp8(*args, float(k_scale), float(v_scale), *ws, int(flags), _stream(stream)))
+
+
+def _prob_rows(t, name, total, vocab, index, dtype):
+    """(address, row stride) of a row of `vocab` entries per node; rows may be strided."""
+    st = t.stride()
+    if t.dtype is not dtype or tuple(t.shape) != (total, vocab) or t.get_device() != index or (vocab > 1 and st[1] != 1):
+        _bad(f"{name} must be {dtype} ({total}, {vocab}) with dense rows on cuda:{index}, not {t.dtype} {tuple(t.shape)} strides "
+             f"{st} on {t.device}")
+    return t.data_ptr(), st[0] if total > 1 else vocab
+
+
+def pa_verify_draft(num_accepted, path, tokens_out, tokens, parents, cu_seqlens_q, target, draft=None, uniforms=None,
+                    stream=None) -> None:
+    """int32 CUDA tensors: num_accepted [S], path and tokens_out [total_q] out; tokens, parents [total_q], cu_seqlens_q [S + 1].
+    target (and draft, the drafter's rows that children were drawn from, or None): [total_q, vocab] fp32, fp16 or bf16, rows
+    may be strided; uniforms [total_q, 2] fp32, or None: greedy, target may then hold logits."""
+    import torch
+    i32 = torch.int32
+    total, s = tokens.numel(), num_accepted.numel()
+    dev = _device(tokens, "tokens")
+    if target.dim() != 2:
+        _bad(f"target must be [total_q, vocab], not {tuple(target.shape)}")
+    vocab = target.shape[1]
+    code = PA_F32 if target.dtype is torch.float32 else _dtype_code(target)
+    t, ts = _prob_rows(target, "target", total, vocab, dev, target.dtype)
+    d, ds = (None, 0) if draft is None else _prob_rows(draft, "draft", total, vocab, dev, target.dtype)
+    _check(lib().pa_verify_draft(
+        _ints(num_accepted, "num_accepted", s, dev, i32), _ints(path, "path", total, dev, i32),
+        _ints(tokens_out, "tokens_out", total, dev, i32), _ints(tokens, "tokens", total, dev, i32),
+        _ints(parents, "parents", total, dev, i32), _ints(cu_seqlens_q, "cu_seqlens_q", s + 1, dev, i32), s, total, t, ts, d, ds,
+        vocab, code, None if uniforms is None else _ints(uniforms, "uniforms", 2 * total, dev, torch.float32), _stream(stream)))
+
+
+def pa_commit_draft(kv_caches, block_tables, cu_seqlens_q, seq_lens, num_accepted, path, seq_lens_out, free_list=None,
+                    num_free=None, num_free_out=None, stream=None) -> None:
+    """kv_caches: list of per-layer pools (fp16, bf16, or E4M3 codes as uint8 / float8_e4m3fn); int32 CUDA tensors:
+    block_tables [S, maxblk], cu_seqlens_q [S + 1], seq_lens [S] (the nodes included), num_accepted [S] and path [total_q]
+    (see pa_verify_draft); seq_lens_out [S] (may be seq_lens); free_list [num_blocks] (a stack, in place) with num_free and
+    num_free_out [1] (may be one), or None: no block is returned."""
+    import torch
+    i32 = torch.int32
+    first = kv_caches[0]
+    nb, bs, hkv, d = _pool_dims(first)
+    s, width = block_tables.shape
+    total = path.numel()
+    dev = _device(block_tables, "block_tables")
+    for c in kv_caches:
+        if c.shape != first.shape or c.dtype != first.dtype:
+            _bad(f"kv_caches differ: {tuple(c.shape)} {c.dtype}, {tuple(first.shape)} {first.dtype}")
+    ptrs = (ctypes.c_void_p * len(kv_caches))(*[_pool(c, "kv_cache", dev) for c in kv_caches])
+    free = (None, None, None)
+    if free_list is not None:
+        if num_free is None or num_free_out is None:
+            _bad("free_list without num_free and num_free_out")
+        free = (_ints(free_list, "free_list", nb, dev, i32), _ints(num_free, "num_free", 1, dev, i32),
+                _ints(num_free_out, "num_free_out", 1, dev, i32))
+    _check(lib().pa_commit_draft(
+        ptrs, len(kv_caches), _ints(block_tables, "block_tables", s * width, dev, i32), width,
+        _ints(cu_seqlens_q, "cu_seqlens_q", s + 1, dev, i32), _ints(seq_lens, "seq_lens", s, dev, i32),
+        _ints(num_accepted, "num_accepted", s, dev, i32), _ints(path, "path", total, dev, i32), s, total,
+        _ints(seq_lens_out, "seq_lens_out", s, dev, i32), *free, nb, bs, hkv, d, _pool_code(first), _stream(stream)))
 
 
 def pa_copy_blocks(kv_caches, src_dst_pairs, stream=None) -> None:

@@ -28,6 +28,8 @@ CXX_FLAGS = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-Wextra"]
 UNITS = [
     ("pa_kernels.cu", "nvcc"),
     ("pa_prefill.cu", "nvcc"),
+    ("pa_tree_attention.cu", "nvcc"),
+    ("pa_tree.cu", "nvcc"),
     ("pa_static_scratch.cu", "nvcc"),
     ("pa_step.cu", "nvcc"),
     ("pa_rope.cu", "nvcc"),
@@ -39,7 +41,8 @@ UNITS = [
 
 def _sources():
     files = [os.path.join(CSRC, f) for f, _ in UNITS]
-    files += [os.path.join(CSRC, "pa_internal.h"), os.path.join(CSRC, "pa_device.cuh"), HEADER,
+    files += [os.path.join(CSRC, "pa_internal.h"), os.path.join(CSRC, "pa_device.cuh"),
+              os.path.join(CSRC, "pa_prefill_kernel.cuh"), HEADER,
               os.path.abspath(__file__)]
     return files
 

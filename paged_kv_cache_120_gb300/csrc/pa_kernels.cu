@@ -27,7 +27,8 @@
 //    permutation of block placement.
 //  * Cross attention of a few rows (pa_cross_attention) is the same kernel
 //    with ragged queries: a tile's columns are the (query, head) pairs of a
-//    sequence's one or few queries, up to 16.
+//    sequence's one or few queries, up to 16. So is tree attention of a few
+//    (pa_tree_attention), whose masks count in a sequence's last tiles only.
 //  * reshape_and_cache and copy_blocks are bit copies with 16-byte accesses.
 //  * FP8 cache (OCP E4M3 codes with one scale for K and one for V; a reading
 //    of the book's "lower-precision KV cache", §4.8): the same pipeline moves
@@ -281,7 +282,16 @@ struct DecodeParams {
     int tile_heads;
     int max_q;
     int total_q;
+    // Tree attention: the queries are the sequence's last tokens, and of those
+    // each sees what its row of mask_words words names.
+    const uint32_t *tree_masks;
+    int mask_words;
+    const void *kv_cache;  // V once more, where it is not finite
 };
+
+// What a launch's queries are: one per sequence, a ragged few that see every
+// cached token (cross attention), or a tree's few nodes.
+enum : int { kOneQuery = 0, kFewQueries = 1, kFewNodes = 2 };
 
 template <int D, int NT>
 constexpr int record_floats()
@@ -355,13 +365,14 @@ __device__ __forceinline__ int owner_of(long long u, long long N, long long K)
 }
 
 // Main decode kernel. Template: head size D, N-tiles of 8 query heads NT,
-// element type of Q and the output, FP8 cache or not, one query per sequence
-// or a ragged few. One CTA = decode_warps<NT>() independent warp pipelines.
-template <int D, int NT, bool BF16, bool FP8, bool RAGGED>
-__global__ void __launch_bounds__(decode_warps<D, NT, FP8, RAGGED>() * 32, decode_min_ctas<D, NT>())
+// element type of Q and the output, FP8 cache or not, what the queries are.
+// One CTA = decode_warps<NT>() independent warp pipelines.
+template <int D, int NT, bool BF16, bool FP8, int FORM>
+__global__ void __launch_bounds__(decode_warps<D, NT, FP8, FORM != kOneQuery>() * 32, decode_min_ctas<D, NT>())
     paged_decode_kernel(const __grid_constant__ CUtensorMap kv_map, const DecodeParams p)
 {
     using Geo = TileGeo<D, FP8>;
+    constexpr bool RAGGED = FORM != kOneQuery, TREE = FORM == kFewNodes;
     constexpr int kWarps = decode_warps<D, NT, FP8, RAGGED>();
     constexpr int kStages = decode_stages<D, NT, FP8, RAGGED>();
     constexpr int KS = D / 16;  // k-steps of QK^T and m-tiles of V^T P^T
@@ -413,7 +424,7 @@ __global__ void __launch_bounds__(decode_warps<D, NT, FP8, RAGGED>() * 32, decod
             if constexpr (RAGGED) {
                 const int q0 = p.cu_q[s];
                 const long long n = (long long)p.cu_q[s + 1] - q0;
-                const bool ok = n >= 0 && n <= p.max_q && q0 >= 0 && q0 <= p.total_q - n && L >= 0 && L <= max_len;
+                const bool ok = n >= 0 && n <= p.max_q && q0 >= 0 && q0 <= p.total_q - n && L >= (TREE ? n : 0) && L <= max_len;
                 if (!ok)
                     raise_error(PA_DEVERR_SEQ_LEN);
                 rows[s] = ok ? make_int2(q0, (int)n) : make_int2(0, 0);
@@ -580,6 +591,10 @@ __global__ void __launch_bounds__(decode_warps<D, NT, FP8, RAGGED>() * 32, decod
     uint32_t qf[NT][KS][2];
     float xscale[NT][2];  // per-column score scale (bf16 queries on an FP8 cache)
     int cur_seg = -1;
+    // Tree: the segment's first unit, the first one that holds a node, and
+    // whether some V element of its nodes was not finite.
+    [[maybe_unused]] long long seg_at = 0, nodes_at = 0;
+    [[maybe_unused]] bool poisoned = false;
 
     auto seg_coords = [&](int seg, int &s, int &segl, int &hq0) {
         s = seg / segs_per_seq;
@@ -601,9 +616,20 @@ __global__ void __launch_bounds__(decode_warps<D, NT, FP8, RAGGED>() * 32, decod
         }
     };
 
+    // Tree: the mask of column col's query; null if it is none of s's.
+    [[maybe_unused]] auto mask_of = [&](int s, int col) -> const uint32_t * {
+        const int q = col / p.tile_heads;
+        return q < rows[s].y ? p.tree_masks + (long long)(rows[s].x + q) * p.mask_words : nullptr;
+    };
+
     auto begin_segment = [&](int seg) {
         int s, segl, hq0;
         seg_coords(seg, s, segl, hq0);
+        if constexpr (TREE) {
+            seg_at = prefix[s] + (long long)segl * ((lens[s] + kTile - 1) / kTile);
+            nodes_at = seg_at + (lens[s] - rows[s].y) / kTile;
+            poisoned = false;
+        }
         const uint16_t *qbase = p.query + ((long long)(RAGGED ? rows[s].x : s) * p.num_q_heads + hq0) * D;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -694,6 +720,58 @@ __global__ void __launch_bounds__(decode_warps<D, NT, FP8, RAGGED>() * 32, decod
         const int ntiles = (lens[s] + kTile - 1) / kTile;
         const long long seg_start = prefix[s] + (long long)segl * ntiles;
         const long long seg_end = seg_start + ntiles;
+        if constexpr (TREE) {
+            const int n = rows[s].y, context = lens[s] - n;
+            if (context == 0) {
+                // A column that sees nothing: O is 0, and so is 0 / 1.
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t *mask = mask_of(s, nt * 8 + 2 * tig + e);
+                        uint32_t any = mask ? 0u : 1u;
+                        for (int k = 0; mask && 32 * k < n; ++k)
+                            any |= n - 32 * k >= 32 ? mask[k] : mask[k] & ((1u << (n - 32 * k)) - 1u);
+                        if (any == 0u)
+                            lsum[nt][e] = 1.f;
+                    }
+            }
+            if (poisoned) {
+                // The elements of V zeroed below, to the columns that see them.
+                const int lo = (int)(max(max(seg_start, r0), nodes_at) - seg_start) * kTile;
+                const int hi = min(lens[s], (int)(min(seg_end, r1) - seg_start) * kTile);
+                for (int tok = max(lo, context); tok < hi; ++tok) {
+                    const int node = tok - context;
+                    const int phys = p.block_tables[(long long)s * p.max_blocks_per_seq + tok / p.block_size];
+                    if ((unsigned)phys >= (unsigned)p.num_blocks)
+                        continue;
+                    const long long slot = (long long)phys * p.block_size + tok % p.block_size;
+                    const long long at =
+                        (((long long)p.num_blocks * p.block_size + slot) * p.num_kv_heads + segl / p.qtiles) * D;
+                    auto extra = [&](int d) {
+                        if constexpr (FP8) {
+                            return (static_cast<const uint8_t *>(p.kv_cache)[at + d] & 0x7F) == 0x7F ? NAN : 0.f;
+                        } else {
+                            const float v = unpack2<BF16>(static_cast<const uint16_t *>(p.kv_cache)[at + d]).x;
+                            return isfinite(v) ? 0.f : v;
+                        }
+                    };
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const uint32_t *mask = mask_of(s, nt * 8 + 2 * tig + e);
+                            if (mask && (mask[node >> 5] >> (node & 31) & 1u)) {
+#pragma unroll
+                                for (int mt = 0; mt < KS; ++mt) {
+                                    acc[mt][nt][e] += extra(FP8 ? VB * g + 2 * mt : 16 * mt + g);
+                                    acc[mt][nt][2 + e] += extra(FP8 ? VB * g + 2 * mt + 1 : 16 * mt + g + 8);
+                                }
+                            }
+                        }
+                }
+            }
+        }
         if (seg_start >= r0 && seg_end <= r1) {
             // Whole segment in this warp's share: normalise and store.
             uint16_t *out =
@@ -813,6 +891,57 @@ __global__ void __launch_bounds__(decode_warps<D, NT, FP8, RAGGED>() * 32, decod
             }
             fence_proxy_async();
             __syncwarp();
+        }
+
+        // Tree, a tile that holds nodes: bit 4 nt + 2 h + e of `seen` is whether
+        // column 2 tig + e of nt sees token g + 8 h; and V elements of nodes that
+        // are not finite are zeroed, since 0 x NaN would reach the columns that do
+        // not see them (finish_segment adds them to those that do).
+        [[maybe_unused]] uint32_t seen = ~0u;
+        if constexpr (TREE) {
+            if (i >= nodes_at) {
+                const int s = sg / segs_per_seq, n = rows[s].y;
+                const int first = (int)(i - seg_at) * kTile - (lens[s] - n);  // node of the tile's first token
+                seen = 0u;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t *mask = mask_of(s, nt * 8 + 2 * tig + e);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int node = first + g + 8 * h;
+                            if (node < 0 || (node < n && (!mask || (__ldg(mask + (node >> 5)) >> (node & 31) & 1u))))
+                                seen |= 1u << (4 * nt + 2 * h + e);
+                        }
+                    }
+                constexpr int CPR = Geo::kRowBytes / 16;
+                bool found = false;
+                for (int z = lane; z < kTile * CPR * Geo::kBoxes; z += 32) {
+                    const int bx = z / (kTile * CPR), rem = z - bx * (kTile * CPR), r = rem / CPR;
+                    if (first + r < 0 || first + r >= n)
+                        continue;
+                    const uint32_t at = sbuf + bx * Geo::kBoxBytes + Geo::kVOffset + r * Geo::kRowBytes + (rem % CPR) * 16;
+                    const uint4 v = lds128(at);
+                    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+                    uint32_t y[4], any = 0u;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        constexpr uint32_t e = FP8 ? 0x7F7F7F7Fu : BF16 ? 0x7F807F80u : 0x7C007C00u;
+                        const uint32_t bad = FP8 ? __vcmpeq4(x[k] & e, e) : __vcmpeq2(x[k] & e, e);
+                        y[k] = x[k] & ~bad;
+                        any |= bad;
+                    }
+                    if (any) {
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(y[0]), "r"(y[1]), "r"(y[2]),
+                                     "r"(y[3])
+                                     : "memory");
+                        found = true;
+                    }
+                }
+                poisoned |= __any_sync(kFull, found);
+                __syncwarp();
+            }
         }
 
         // S^T[16 tokens][8*NT queries] = K Q^T. All K fragments are loaded
@@ -948,8 +1077,10 @@ __global__ void __launch_bounds__(decode_warps<D, NT, FP8, RAGGED>() * 32, decod
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const float xs = (FP8 && BF16) ? xscale[nt][e] : p.scale_log2;
-                const float x0 = tok0 ? (sc[nt][e] + sc2[nt][e]) * xs : -INFINITY;
-                const float x1 = tok1 ? (sc[nt][2 + e] + sc2[nt][2 + e]) * xs : -INFINITY;
+                const bool see0 = tok0 && (!TREE || (seen >> (4 * nt + e) & 1u));
+                const bool see1 = tok1 && (!TREE || (seen >> (4 * nt + 2 + e) & 1u));
+                const float x0 = see0 ? (sc[nt][e] + sc2[nt][e]) * xs : -INFINITY;
+                const float x1 = see1 ? (sc[nt][2 + e] + sc2[nt][2 + e]) * xs : -INFINITY;
                 float mx = fmaxf(x0, x1);
                 mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 4));
                 mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 8));
@@ -1551,10 +1682,11 @@ struct DecodePlan {
     size_t total() const { return prefix_bytes + task_bytes + warp_record_bytes; }
 };
 
-template <int D, int NT, bool BF16, bool FP8, bool RAGGED>
+template <int D, int NT, bool BF16, bool FP8, int FORM>
 void pick_kernels(DecodePlan &pl, int num_seqs)
 {
-    pl.main_fn = reinterpret_cast<const void *>(&paged_decode_kernel<D, NT, BF16, FP8, RAGGED>);
+    constexpr bool RAGGED = FORM != kOneQuery;
+    pl.main_fn = reinterpret_cast<const void *>(&paged_decode_kernel<D, NT, BF16, FP8, FORM>);
     pl.warps = decode_warps<D, NT, FP8, RAGGED>();
     pl.reduce_fn = reinterpret_cast<const void *>(&paged_decode_reduce_kernel<D, NT, BF16, RAGGED, kMergeWarps>);
     pl.reduce_smem = reduce_smem_bytes<D, NT, RAGGED, kMergeWarps>();
@@ -1567,23 +1699,23 @@ void pick_kernels(DecodePlan &pl, int num_seqs)
     pl.smem = decode_smem_bytes<D, NT, FP8, RAGGED>(num_seqs);
 }
 
-template <int D, int NT, bool RAGGED>
+template <int D, int NT, int FORM>
 void pick_kernels(DecodePlan &pl, int num_seqs, bool bf, bool fp8)
 {
     if (fp8)
-        bf ? pick_kernels<D, NT, true, true, RAGGED>(pl, num_seqs) : pick_kernels<D, NT, false, true, RAGGED>(pl, num_seqs);
+        bf ? pick_kernels<D, NT, true, true, FORM>(pl, num_seqs) : pick_kernels<D, NT, false, true, FORM>(pl, num_seqs);
     else
-        bf ? pick_kernels<D, NT, true, false, RAGGED>(pl, num_seqs)
-           : pick_kernels<D, NT, false, false, RAGGED>(pl, num_seqs);
+        bf ? pick_kernels<D, NT, true, false, FORM>(pl, num_seqs)
+           : pick_kernels<D, NT, false, false, FORM>(pl, num_seqs);
 }
 
-template <bool RAGGED>
+template <int FORM>
 void pick_kernels(DecodePlan &pl, int head_size, int num_seqs, bool bf, bool fp8)
 {
     if (head_size == 64)
-        pl.nt == 1 ? pick_kernels<64, 1, RAGGED>(pl, num_seqs, bf, fp8) : pick_kernels<64, 2, RAGGED>(pl, num_seqs, bf, fp8);
+        pl.nt == 1 ? pick_kernels<64, 1, FORM>(pl, num_seqs, bf, fp8) : pick_kernels<64, 2, FORM>(pl, num_seqs, bf, fp8);
     else
-        pl.nt == 1 ? pick_kernels<128, 1, RAGGED>(pl, num_seqs, bf, fp8) : pick_kernels<128, 2, RAGGED>(pl, num_seqs, bf, fp8);
+        pl.nt == 1 ? pick_kernels<128, 1, FORM>(pl, num_seqs, bf, fp8) : pick_kernels<128, 2, FORM>(pl, num_seqs, bf, fp8);
 }
 
 int validate_decode_shape(int num_seqs, int num_q_heads, int num_kv_heads, int head_size,
@@ -1653,9 +1785,9 @@ cudaError_t kernel_setup(const void *fn, int dev, size_t smem, int threads, int 
 }
 
 // max_q: 0 for one query per sequence (pa_decode), else the most queries of a
-// ragged sequence.
+// ragged sequence; tree: those see what their masks name.
 int make_plan(DecodePlan &pl, int num_seqs, int num_q_heads, int num_kv_heads, int head_size,
-              int dtype, bool fp8, int max_q = 0)
+              int dtype, bool fp8, int max_q = 0, bool tree = false)
 {
     const int group = num_q_heads / num_kv_heads;
     pl.tile_heads = group <= 16 ? group : 16;
@@ -1663,7 +1795,12 @@ int make_plan(DecodePlan &pl, int num_seqs, int num_q_heads, int num_kv_heads, i
     pl.qtiles = group <= 16 ? 1 : group / 16;
     pl.nt = pl.tile_q <= 8 ? 1 : 2;
     const bool bf = dtype == PA_BF16;
-    max_q > 0 ? pick_kernels<true>(pl, head_size, num_seqs, bf, fp8) : pick_kernels<false>(pl, head_size, num_seqs, bf, fp8);
+    if (max_q == 0)
+        pick_kernels<kOneQuery>(pl, head_size, num_seqs, bf, fp8);
+    else if (tree)
+        pick_kernels<kFewNodes>(pl, head_size, num_seqs, bf, fp8);
+    else
+        pick_kernels<kFewQueries>(pl, head_size, num_seqs, bf, fp8);
     int dev = 0, sms = 0, occ = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
@@ -1725,10 +1862,10 @@ int launch_decode(const char *fn, void *out, const void *query, const void *kv_c
                   int max_blocks_per_seq, const int32_t *seq_lens, int num_seqs, float scale, int num_q_heads,
                   int num_kv_heads, int head_size, int num_blocks, int block_size, int dtype, bool fp8, float k_scale,
                   float v_scale, void *workspace, size_t workspace_bytes, unsigned flags, const int32_t *cu_q, int max_q,
-                  int total_q, pa_stream_t stream)
+                  int total_q, const int32_t *tree_masks, int mask_words, pa_stream_t stream)
 {
     DecodePlan pl;
-    int rc = make_plan(pl, num_seqs, num_q_heads, num_kv_heads, head_size, dtype, fp8, cu_q ? max_q : 0);
+    int rc = make_plan(pl, num_seqs, num_q_heads, num_kv_heads, head_size, dtype, fp8, cu_q ? max_q : 0, tree_masks != nullptr);
     if (rc != PA_OK)
         return rc;
     if (workspace_bytes < pl.total())
@@ -1769,6 +1906,9 @@ int launch_decode(const char *fn, void *out, const void *query, const void *kv_c
     prm.tile_heads = pl.tile_heads;
     prm.max_q = max_q;
     prm.total_q = total_q;
+    prm.tree_masks = reinterpret_cast<const uint32_t *>(tree_masks);
+    prm.mask_words = mask_words;
+    prm.kv_cache = kv_cache;
 
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     void *args[] = {&map, &prm};
@@ -1811,7 +1951,7 @@ int decode_impl(const char *fn, void *out, const void *query, const void *kv_cac
         return set_error(PA_ERR_INVALID_ARG, "%s: misaligned pointer (pool/query/out 16 B, workspace 256 B)", fn);
     return launch_decode(fn, out, query, kv_cache, block_tables, max_blocks_per_seq, seq_lens, num_seqs, scale, num_q_heads,
                          num_kv_heads, head_size, num_blocks, block_size, dtype, fp8, k_scale, v_scale, workspace,
-                         workspace_bytes, flags, nullptr, 0, 0, stream);
+                         workspace_bytes, flags, nullptr, 0, 0, nullptr, 0, stream);
 }
 
 // Checks shared by both write paths; *row_vecs = 8-element groups per row.
@@ -1850,10 +1990,10 @@ bool cross_rows_fit(int num_seqs, int max_seqlen_q, int num_q_heads, int num_kv_
 }
 
 int cross_rows_workspace(int num_seqs, int max_seqlen_q, int num_q_heads, int num_kv_heads, int head_size, int dtype, bool fp8,
-                         size_t *bytes)
+                         bool tree, size_t *bytes)
 {
     DecodePlan pl;
-    int rc = make_plan(pl, num_seqs, num_q_heads, num_kv_heads, head_size, dtype, fp8, max_seqlen_q);
+    int rc = make_plan(pl, num_seqs, num_q_heads, num_kv_heads, head_size, dtype, fp8, max_seqlen_q, tree);
     if (rc == PA_OK)
         *bytes = pl.total();
     return rc;
@@ -1862,12 +2002,12 @@ int cross_rows_workspace(int num_seqs, int max_seqlen_q, int num_q_heads, int nu
 int cross_rows(const char *who, void *out, const void *query, const void *kv_cache, const int32_t *block_tables,
                int max_blocks_per_seq, const int32_t *cu_seqlens_q, const int32_t *kv_lens, int num_seqs, int total_q,
                int max_seqlen_q, float scale, int num_q_heads, int num_kv_heads, int head_size, int num_blocks,
-               int block_size, int dtype, bool fp8, float k_scale, float v_scale, void *workspace, size_t workspace_bytes,
-               unsigned flags, pa_stream_t stream)
+               int block_size, int dtype, bool fp8, float k_scale, float v_scale, const int32_t *tree_masks, int mask_words,
+               void *workspace, size_t workspace_bytes, unsigned flags, pa_stream_t stream)
 {
     return launch_decode(who, out, query, kv_cache, block_tables, max_blocks_per_seq, kv_lens, num_seqs, scale, num_q_heads,
                          num_kv_heads, head_size, num_blocks, block_size, dtype, fp8, k_scale, v_scale, workspace,
-                         workspace_bytes, flags, cu_seqlens_q, max_seqlen_q, total_q, stream);
+                         workspace_bytes, flags, cu_seqlens_q, max_seqlen_q, total_q, tree_masks, mask_words, stream);
 }
 
 }  // namespace pa
@@ -2036,6 +2176,14 @@ extern "C" int pa_get_device_error(int *bits)
     e = static_cast<cudaError_t>(rope_take_device_error(&w));
     if (e != cudaSuccess)
         return cuda_fail(e, "pa_get_device_error: rotary word");
+    v |= w;
+    e = static_cast<cudaError_t>(tree_attention_take_device_error(&w));
+    if (e != cudaSuccess)
+        return cuda_fail(e, "pa_get_device_error: tree attention word");
+    v |= w;
+    e = static_cast<cudaError_t>(tree_take_device_error(&w));
+    if (e != cudaSuccess)
+        return cuda_fail(e, "pa_get_device_error: tree word");
     *bits = v | w;
     return PA_OK;
 }
