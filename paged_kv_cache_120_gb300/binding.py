@@ -8,6 +8,7 @@ not built this module raises on first use.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 
@@ -77,7 +78,7 @@ SIGNATURES = [
                                    _vp, _sz, _u, _vp]),
     ("pa_tree_attention_workspace_size", _i, [_i, _i, _i, _i, _i, _i, _i, _i, ctypes.POINTER(_sz)]),
     ("pa_verify_draft", _i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _vp, _i64, _vp, _i64, _i, _i, _vp, _vp]),
-    ("pa_commit_draft", _i, [ctypes.POINTER(_vp), _i, _vp, _i, _vp, _vp, _vp, _vp, _i, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _i,
+    ("pa_commit_draft", _i, [_vp, _i, _vp, _i, _vp, _vp, _vp, _vp, _i, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _i,
                              _i, _vp]),
     ("pa_copy_blocks", _i, [ctypes.POINTER(_vp), _i, _vp, _i, _i, _i, _i, _i, _i, _vp]),
     ("pa_get_device_error", _i, [_ip]),
@@ -661,10 +662,13 @@ def pa_commit_draft(kv_caches, block_tables, cu_seqlens_q, seq_lens, num_accepte
     s, width = block_tables.shape
     total = path.numel()
     dev = _device(block_tables, "block_tables")
-    for c in kv_caches:
-        if c.shape != first.shape or c.dtype != first.dtype:
-            _bad(f"kv_caches differ: {tuple(c.shape)} {c.dtype}, {tuple(first.shape)} {first.dtype}")
-    ptrs = (ctypes.c_void_p * len(kv_caches))(*[_pool(c, "kv_cache", dev) for c in kv_caches])
+    shape, dtype = first.shape, first.dtype
+    at = []
+    for c in kv_caches:  # a model's worth of layers at every step: checked without a call each
+        if c.shape != shape or c.dtype is not dtype or c.get_device() != dev or not c.is_contiguous():
+            _bad(f"kv_caches differ, or are not contiguous on cuda:{dev}: {tuple(c.shape)} {c.dtype} on {c.device}, {tuple(shape)} {dtype}")
+        at.append(c.data_ptr())
+    ptrs = array.array("Q", at)
     free = (None, None, None)
     if free_list is not None:
         if num_free is None or num_free_out is None:
@@ -672,7 +676,7 @@ def pa_commit_draft(kv_caches, block_tables, cu_seqlens_q, seq_lens, num_accepte
         free = (_ints(free_list, "free_list", nb, dev, i32), _ints(num_free, "num_free", 1, dev, i32),
                 _ints(num_free_out, "num_free_out", 1, dev, i32))
     _check(lib().pa_commit_draft(
-        ptrs, len(kv_caches), _ints(block_tables, "block_tables", s * width, dev, i32), width,
+        ptrs.buffer_info()[0], len(at), _ints(block_tables, "block_tables", s * width, dev, i32), width,
         _ints(cu_seqlens_q, "cu_seqlens_q", s + 1, dev, i32), _ints(seq_lens, "seq_lens", s, dev, i32),
         _ints(num_accepted, "num_accepted", s, dev, i32), _ints(path, "path", total, dev, i32), s, total,
         _ints(seq_lens_out, "seq_lens_out", s, dev, i32), *free, nb, bs, hkv, d, _pool_code(first), _stream(stream)))

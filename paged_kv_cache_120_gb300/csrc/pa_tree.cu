@@ -27,73 +27,84 @@ __device__ __forceinline__ void tree_raise(int bit) { atomicOr(&g_tree_error, bi
 
 // ------------------------------------------------------------- pa_build_tree
 
-// One CTA per sequence. With up(i) a node's parent and M(i) the set {i}, each
-// round does M(i) |= M(up(i)) and up(i) = up(up(i)): after r rounds M(i) holds
-// the first 2^r nodes on i's way up, so that a single file of n nodes takes
-// log2 n rounds instead of n steps. The sets are updated in place: a row that
-// another thread has already widened holds ancestors of i all the same. Depths
-// add up along the same jumps. A launch and some rounds in shared memory bound
-// it, not bandwidth.
-__global__ void __launch_bounds__(1024)
+// A CTA takes kGroupWords words of a sequence's masks, blocks of 32 nodes in
+// turn. Within a block a warp finds each node's topmost ancestor there, the ones
+// on the way and their number, by jumping (5 rounds of shuffles); that ancestor's
+// parent lies in an earlier block, so that a node's row is that parent's row and
+// the block's own word. Block after block, the rows before them complete: n / 32
+// steps of one shared load a word, whatever the depth. A launch bounds the small
+// cases, the steps the large ones. 16 sequences of up to 1000 nodes in single
+// file: 60.9 us jumping over the whole tree (log2 n rounds over all words), 15.9
+// with all words in one CTA, 7.2 so.
+constexpr int kGroupWords = 8;
+__global__ void __launch_bounds__(32 * kGroupWords)
     build_tree_kernel(const int32_t *__restrict__ parents, const int32_t *__restrict__ cu_q, const int32_t *__restrict__ seq_lens,
-                      int total_q, int words, int32_t *__restrict__ positions, uint32_t *__restrict__ masks)
+                      int total_q, int words, int lane_words, int32_t *__restrict__ positions, uint32_t *__restrict__ masks)
 {
-    extern __shared__ uint32_t tree_smem[];
-    __shared__ int up[2][kMaxNodes], depth[2][kMaxNodes];
-    const int s = blockIdx.x, tid = threadIdx.x, threads = blockDim.x;
+    extern __shared__ uint32_t tree_smem[];  // [n][lane_words]
+    __shared__ int s_above[kMaxNodes], s_depth[kMaxNodes];
+    __shared__ uint32_t s_own[kMaxNodes];
+    const int s = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const bool first = blockIdx.y == 0;  // the group that flags and writes positions
     const int q0 = cu_q[s], L = seq_lens[s];
     const long long n64 = (long long)cu_q[s + 1] - q0;
     if (n64 < 0 || n64 > min(kMaxNodes, 32 * words) || q0 < 0 || q0 > total_q - n64 || L < n64) {
-        if (tid == 0)
+        if (first && tid == 0)
             tree_raise(PA_DEVERR_SEQ_LEN);
         return;
     }
-    const int n = (int)n64;
-    for (int i = tid; i < n; i += threads) {
-        const int a = parents[q0 + i];
-        const bool has = a >= 0 && a < i;
-        if (!has && a != -1)
-            tree_raise(PA_DEVERR_TREE);
-        up[0][i] = has ? a : -1;
-        depth[0][i] = has ? 1 : 0;
-    }
-    uint32_t *set = tree_smem;  // [n][words]
-    for (int k = tid; k < n * words; k += threads) {
-        const int i = k / words, w = k - i * words;
-        set[k] = w == i >> 5 ? 1u << (i & 31) : 0u;
+    const int n = (int)n64, blocks = (n + 31) / 32;
+    for (int b = warp; b < blocks; b += blockDim.x / 32) {
+        const int i = 32 * b + lane;
+        int a = i < n ? parents[q0 + i] : -1;
+        if (a < -1 || a >= i) {
+            if (first && i < n)
+                tree_raise(PA_DEVERR_TREE);
+            a = -1;
+        }
+        int top = a >= 32 * b ? a - 32 * b : lane;  // of the block; itself: no ancestor there
+        int steps = a >= 32 * b ? 1 : 0;
+        uint32_t own = 1u << lane;
+#pragma unroll
+        for (int r = 0; r < 5; ++r) {
+            own |= __shfl_sync(kFull, own, top);
+            steps += __shfl_sync(kFull, steps, top);
+            top = __shfl_sync(kFull, top, top);
+        }
+        s_above[i] = __shfl_sync(kFull, a, top);
+        s_depth[i] = steps;
+        s_own[i] = own;
     }
     __syncthreads();
-    int cur = 0;
-    for (int reach = 1; reach < n; reach *= 2) {
-        int more = 0;
-        for (int k = tid; k < n * words; k += threads) {
-            const int i = k / words, w = k - i * words, a = up[cur][i];
-            if (a >= 0 && w <= a >> 5)  // ancestors come before their descendants
-                set[k] |= set[a * words + w];
+    // Thread: word w of one node of the block; neighbours share a row.
+    const int w0 = blockIdx.y * kGroupWords, w = w0 + (tid & (lane_words - 1));
+    for (int b = w0; b < blocks; ++b) {
+        const int i = 32 * b + tid / lane_words;
+        if (i < n) {
+            const int above = s_above[i];
+            // A row has no bits in words behind its own block's.
+            uint32_t set = w == b ? s_own[i] : 0u;
+            if (w < b && above >> 5 >= w)
+                set = tree_smem[above * lane_words + w - w0];
+            tree_smem[i * lane_words + w - w0] = set;
+            if (w == 0 && above >= 0)
+                s_depth[i] += s_depth[above] + 1;
         }
-        for (int i = tid; i < n; i += threads) {
-            const int a = up[cur][i];
-            const int b = a >= 0 ? up[cur][a] : -1;
-            up[cur ^ 1][i] = b;
-            depth[cur ^ 1][i] = depth[cur][i] + (a >= 0 ? depth[cur][a] : 0);
-            more |= b >= 0;
-        }
-        cur ^= 1;
-        if (!__syncthreads_or(more))
-            break;
+        __syncthreads();
     }
-    for (int k = tid; k < n * words; k += threads)
-        masks[(long long)q0 * words + k] = set[k];
-    if (positions)
-        for (int i = tid; i < n; i += threads)
-            positions[q0 + i] = L - n + depth[cur][i];
+    if (w < words)
+        for (int i = tid / lane_words; i < n; i += 32)
+            masks[(long long)(q0 + i) * words + w] = i >> 5 >= w0 ? tree_smem[i * lane_words + w - w0] : 0u;
+    if (first && positions)
+        for (int i = tid; i < n; i += blockDim.x)
+            positions[q0 + i] = L - n + s_depth[i];
 }
 
 // ----------------------------------------------------------- pa_verify_draft
 
 // A sum held as an unevaluated pair hi + lo of fp32 numbers (about 46 bits):
-// where a draw falls next to a border, 24 bits are too few, and fp64 adds are
-// a thirtieth of the fp32 rate here.
+// where a draw falls next to a border, 24 bits are too few, and fp64 runs at a
+// sixty-fourth of the fp32 rate here (16 adds by every thread took 1 us).
 struct Sum {
     float hi, lo;
 };
@@ -106,19 +117,66 @@ __device__ __forceinline__ void add(Sum &s, float x, float e)
     s.hi = t;
 }
 
-__device__ __forceinline__ double value(const Sum &s) { return (double)s.hi + (double)s.lo; }
+__device__ __forceinline__ bool above(const Sum &a, const Sum &b) { return (a.hi - b.hi) + (a.lo - b.lo) > 0.f; }
 
-// max(p - a q, 0) as a pair, a = ah + al >= 0: the product's and the
-// difference's rounding errors are kept. Anything not above 0 (NaN too) is 0.
-__device__ __forceinline__ Sum weight(float p, float q, float ah, float al)
+// x (y.hi + y.lo)
+__device__ __forceinline__ Sum times(float x, const Sum &y)
 {
-    const float m = __fmul_rn(ah, q), me = fmaf(ah, q, -m);  // kept apart: no fused p - ah q
-    const float d = p - m, b = d - p;
-    const float e = ((p - (d - b)) + (-m - b)) - (me + al * q);
-    const float hi = d + e;
-    if (!(hi > 0.f))
-        return Sum{0.f, 0.f};
-    return Sum{hi, isinf(hi) ? 0.f : e - (hi - d)};
+    const float h = __fmul_rn(x, y.hi);
+    return Sum{h, fmaf(x, y.lo, fmaf(x, y.hi, -h))};
+}
+
+__device__ __forceinline__ Sum shfl(const Sum &s, int from)
+{
+    return Sum{__shfl_sync(kFull, s.hi, from), __shfl_sync(kFull, s.lo, from)};
+}
+
+// Inclusive sums over the lanes, STEP apart: lane i gets those of i, i - STEP, ...
+template <int STEP>
+__device__ __forceinline__ Sum running(Sum s)
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = STEP; o < 32; o <<= 1) {
+        const float h = __shfl_up_sync(kFull, s.hi, o), l = __shfl_up_sync(kFull, s.lo, o);
+        if (lane >= o)
+            add(s, h, l);
+    }
+    return s;
+}
+
+// max(p - a q, 0) as a pair, a >= 0: the product's and the difference's
+// rounding errors are kept ((p - d) - m is the latter's where p >= m, and only
+// there it counts). Anything not above 0 (NaN too) is 0.
+__device__ __forceinline__ Sum weight(float p, float q, const Sum &a)
+{
+    const float m = __fmul_rn(a.hi, q), me = fmaf(a.hi, q, -m);  // kept apart: no fused p - a q
+    const float d = p - m, e = ((p - d) - m) - fmaf(a.lo, q, me);
+    return d + e > 0.f ? Sum{d, e} : Sum{0.f, 0.f};
+}
+
+// Two sums side by side, and the same of two entries each (packed fp32, an
+// instruction for two: by single ones the arithmetic took as long as the rows).
+struct Sum2 {
+    uint64_t hi, lo;
+};
+
+__device__ __forceinline__ void add(Sum2 &s, const Sum2 &w)
+{
+    const uint64_t t = add2(s.hi, w.hi), b = sub2(t, s.hi);
+    s.lo = add2(s.lo, add2(add2(sub2(s.hi, sub2(t, b)), sub2(w.hi, b)), w.lo));
+    s.hi = t;
+}
+
+__device__ __forceinline__ Sum2 weight(uint64_t p, uint64_t q, const Sum2 &a, uint64_t minus_a)
+{
+    const uint64_t nm = mul2(minus_a, q);
+    const uint64_t d = add2(p, nm), e = sub2(add2(sub2(p, d), nm), fma2(a.lo, q, fma2(a.hi, q, nm)));
+    float d0, d1, e0, e1;
+    unpk2(d, d0, d1);
+    unpk2(e, e0, e1);
+    const bool in0 = d0 + e0 > 0.f, in1 = d1 + e1 > 0.f;
+    return Sum2{pk2(in0 ? d0 : 0.f, in1 ? d1 : 0.f), pk2(in0 ? e0 : 0.f, in1 ? e1 : 0.f)};
 }
 
 template <typename T>
@@ -163,14 +221,34 @@ __device__ __forceinline__ uint32_t cluster_rank()
     return r;
 }
 
-// A 64-bit word of shared memory of CTA `rank` of this cluster, at the address that `p` has here.
-__device__ __forceinline__ unsigned long long load_from(const void *p, uint32_t rank)
+// The address that `p` of this CTA's shared memory has in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t address_in(const void *p, uint32_t rank)
 {
     uint32_t a;
-    unsigned long long v;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
+    return a;
+}
+
+__device__ __forceinline__ unsigned long long load_from(const void *p, uint32_t rank)
+{
+    unsigned long long v;
+    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(address_in(p, rank)) : "memory");
     return v;
+}
+
+__device__ __forceinline__ void store_to(void *p, uint32_t rank, int v)
+{
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(address_in(p, rank)), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ unsigned long long bits_of(const Sum &s)
+{
+    return (unsigned long long)__float_as_uint(s.hi) << 32 | __float_as_uint(s.lo);
+}
+
+__device__ __forceinline__ Sum sum_of(unsigned long long b)
+{
+    return Sum{__uint_as_float((uint32_t)(b >> 32)), __uint_as_float((uint32_t)b)};
 }
 
 struct VerifyParams {
@@ -183,7 +261,11 @@ struct VerifyParams {
 };
 
 enum : int { kGreedy = 0, kSample = 1, kDraft = 2 };
-constexpr int kVerifyThreads = 256, kVerifyWarps = kVerifyThreads / 32, kMaxCluster = 16;
+constexpr int kVerifyThreads = 256, kVerifyWarps = kVerifyThreads / 32, kMaxCluster = 8;
+constexpr int kEntries = 64;
+constexpr int kTiles = 8, kStep = 32 / kTiles;  // 512-byte tiles of a row that a warp loads at once; lanes that hold one's sum
+// CTAs an SM: the drafter's rows beside the target's take 128 registers a thread.
+__host__ __device__ constexpr int verify_ctas(int mode) { return mode == kDraft ? 2 : 3; }
 
 // A cluster of CTAs takes a sequence down its tree; a row of the target (and
 // of the drafter) is read by all of them, a contiguous part per warp, so that
@@ -198,25 +280,27 @@ constexpr int kVerifyThreads = 256, kVerifyWarps = kVerifyThreads / 32, kMaxClus
 //           terms of the row itself r = max(p - A q, 0), A the sum of the Z so
 //           far, so that a refusal costs one pass and no row is ever stored.
 //           The last refusal is followed by a draw from r.
-//   a draw: the first entry whose running sum passes u times the row's sum:
-//           sums per warp, exchanged over the cluster, name the warp that
-//           holds it, which goes through its part again.
+//   a draw: the first entry whose running sum passes u times the row's sum.
+//           The warps' sums, exchanged over the cluster, name the warp that
+//           holds it; its tiles' sums (kept in registers where a part is one
+//           chunk of kTiles) the tile, then the lane, which looks again at its
+//           16 bytes.
 //
 // The chain from row to row bounds it (one row has to be read before the next
-// is known), then the rows' bytes. Every sum is taken in one order, whatever
-// the timing.
+// is known: load, exchange, load again, exchange), then the rows' bytes. Every
+// sum is taken in one order, whatever the timing.
 template <typename T, int MODE>
-__global__ void __launch_bounds__(kVerifyThreads) verify_draft_kernel(const VerifyParams p, int cluster)
+__global__ void __launch_bounds__(kVerifyThreads, verify_ctas(MODE)) verify_draft_kernel(const VerifyParams p, int cluster)
 {
     constexpr int VEC = 16 / sizeof(T);
+    constexpr bool DRAFT = MODE == kDraft;
     __shared__ int s_parent[kMaxNodes], s_token[kMaxNodes];
-    __shared__ float s_p[MODE == kDraft ? kMaxNodes : 1], s_q[MODE == kDraft ? kMaxNodes : 1];
-    // Exchanged with the other CTAs; two turns, so that a slot is written
-    // again only after a barrier behind its last read.
-    __shared__ unsigned long long s_out[2], s_token_out[2];
-    __shared__ double s_warp[2][kVerifyWarps];
-    __shared__ unsigned long long s_best[kVerifyWarps];
-    __shared__ double s_cta[2][kMaxCluster];
+    __shared__ float s_p[DRAFT ? kMaxNodes : 1], s_q[DRAFT ? kMaxNodes : 1], s_u[DRAFT ? kMaxNodes : 1];
+    // The warps' words, and the CTA's, exchanged with the others; two turns, so
+    // that a slot is written again only after a barrier behind its last read.
+    __shared__ unsigned long long s_warp[2][kVerifyWarps], s_cta[2];
+    __shared__ int s_drawn[2];
+    __shared__ float2 s_tile[kVerifyWarps][kEntries];  // the sums of a warp's tiles, or of groups of them
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int s = blockIdx.x / cluster, rank = (int)cluster_rank();
@@ -240,11 +324,12 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_draft_kernel(const Veri
             tree_raise(PA_DEVERR_TREE);
         s_parent[i] = has ? a : -1;
         s_token[i] = x;
-        if constexpr (MODE == kDraft) {
-            // The two numbers that decide on this node as a first child.
+        if constexpr (DRAFT) {
+            // The numbers that decide on this node.
             const bool in = has && (unsigned)x < (unsigned)V;
             s_p[i] = in ? to_float(target[(q0 + a) * p.target_stride + x]) : 0.f;
             s_q[i] = in ? to_float(draft[(q0 + a) * p.draft_stride + x]) : 0.f;
+            s_u[i] = p.uniforms[2 * (q0 + i)];
         }
         if (rank == 0) {
             p.path[q0 + i] = -1;
@@ -275,181 +360,284 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_draft_kernel(const Veri
     auto row_at = [&](int node) {
         Row r;
         r.p = target + (q0 + node) * p.target_stride;
-        r.q = MODE == kDraft ? draft + (q0 + node) * p.draft_stride : nullptr;
+        r.q = DRAFT ? draft + (q0 + node) * p.draft_stride : nullptr;
         r.mis = (int)((reinterpret_cast<uintptr_t>(r.p) & 15) / sizeof(T));
-        r.q_vec = MODE == kDraft && ((reinterpret_cast<uintptr_t>(r.p) ^ reinterpret_cast<uintptr_t>(r.q)) & 15) == 0;
+        r.q_vec = DRAFT && ((reinterpret_cast<uintptr_t>(r.p) ^ reinterpret_cast<uintptr_t>(r.q)) & 15) == 0;
         const long long vecs = ((long long)V + r.mis + VEC - 1) / VEC;
         r.v0 = (int)(vecs * part / parts);
         r.v1 = (int)(vecs * (part + 1) / parts);
         return r;
     };
-    // The VEC elements of vector v of a row, 0 outside it.
-    auto load = [&](const T *row, int mis, int v, bool vec, float *x) {
+    // Vector v of a row, zeros outside it.
+    auto load = [&](const T *row, int mis, int v, bool vec) {
         const int i0 = v * VEC - mis;
-        if (vec && i0 >= 0 && i0 + VEC <= V) {
-            widen<T>(__ldg(reinterpret_cast<const uint4 *>(row + i0)), x);
-        } else {
+        if (vec && i0 >= 0 && i0 + VEC <= V)
+            return __ldg(reinterpret_cast<const uint4 *>(row + i0));
+        uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-            for (int k = 0; k < VEC; ++k)
-                x[k] = i0 + k >= 0 && i0 + k < V ? to_float(row[i0 + k]) : 0.f;
-        }
+        for (int k = 0; k < VEC; ++k)
+            if (i0 + k >= 0 && i0 + k < V) {
+                if constexpr (sizeof(T) == 4)
+                    w[k] = __float_as_uint(row[i0 + k]);
+                else
+                    w[k / 2] |= (uint32_t)reinterpret_cast<const uint16_t *>(row)[i0 + k] << (16 * (k & 1));
+            }
+        return make_uint4(w[0], w[1], w[2], w[3]);
     };
-    // Vector v's weights.
-    auto weights = [&](const Row &r, int v, float ah, float al, Sum *w) {
+    auto weights = [&](const uint4 &vp, const uint4 &vq, const Sum &a, Sum *w) {
         float x[VEC], y[VEC];
-        load(r.p, r.mis, v, true, x);
-        if (MODE == kDraft && ah != 0.f) {
-            load(r.q, r.mis, v, r.q_vec, y);
+        widen<T>(vp, x);
+        if (DRAFT && a.hi != 0.f) {
+            widen<T>(vq, y);
 #pragma unroll
             for (int k = 0; k < VEC; ++k)
-                w[k] = weight(x[k], y[k], ah, al);
+                w[k] = weight(x[k], y[k], a);
         } else {
 #pragma unroll
             for (int k = 0; k < VEC; ++k)
                 w[k] = Sum{x[k] > 0.f ? x[k] : 0.f, 0.f};
         }
     };
-    auto warp_sum = [&](Sum t) {
+    const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+    // Tile lane / kStep's sum over the lanes, of the kTiles tiles from vector v on.
+    auto chunk = [&](const Row &r, int v, const Sum &a) {
+        Sum tile[kTiles];  // this lane's sums of its vectors
+        uint4 x[kTiles], y[DRAFT ? kTiles : 1];
+        const bool with_q = DRAFT && a.hi != 0.f;
+        // Inside the row, as most chunks are, nothing has to be looked at.
+        if (v + 32 * kTiles <= r.v1 && v > 0 && (v + 32 * kTiles) * VEC - r.mis <= V && (!with_q || r.q_vec)) {
+            const uint4 *xp = reinterpret_cast<const uint4 *>(r.p - r.mis) + v + lane;
+            const uint4 *yp = DRAFT ? reinterpret_cast<const uint4 *>(r.q - r.mis) + v + lane : nullptr;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            add(t, __shfl_xor_sync(kFull, t.hi, o), __shfl_xor_sync(kFull, t.lo, o));
-        return value(Sum{__shfl_sync(kFull, t.hi, 0), __shfl_sync(kFull, t.lo, 0)});
+            for (int t = 0; t < kTiles; ++t)
+                x[t] = __ldg(xp + 32 * t);
+            if constexpr (DRAFT) {
+                if (with_q) {
+#pragma unroll
+                    for (int t = 0; t < kTiles; ++t)
+                        y[t] = __ldg(yp + 32 * t);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) {
+                const int at = v + 32 * t + lane;
+                x[t] = at < r.v1 ? load(r.p, r.mis, at, true) : none;
+                if constexpr (DRAFT)
+                    y[t] = at < r.v1 && with_q ? load(r.q, r.mis, at, r.q_vec) : none;
+            }
+        }
+        // Tiles t and t + kTiles / 2 side by side.
+        const Sum2 a2 = {pk2(a.hi, a.hi), pk2(a.lo, a.lo)};
+        const uint64_t minus = pk2(-a.hi, -a.hi);
+#pragma unroll
+        for (int t = 0; t < kTiles / 2; ++t) {
+            float x0[VEC], x1[VEC], y0[VEC], y1[VEC];
+            widen<T>(x[t], x0);
+            widen<T>(x[t + kTiles / 2], x1);
+            if (with_q) {
+                widen<T>(y[DRAFT ? t : 0], y0);
+                widen<T>(y[DRAFT ? t + kTiles / 2 : 0], y1);
+            }
+            Sum2 both;
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) {
+                Sum2 w;
+                if (with_q)
+                    w = weight(pk2(x0[k], x1[k]), pk2(y0[k], y1[k]), a2, minus);
+                else
+                    w = Sum2{pk2(fmaxf(x0[k], 0.f), fmaxf(x1[k], 0.f)), 0ull};
+                if (k == 0)
+                    both = w;
+                else
+                    add(both, w);
+            }
+            unpk2(both.hi, tile[t].hi, tile[t + kTiles / 2].hi);
+            unpk2(both.lo, tile[t].lo, tile[t + kTiles / 2].lo);
+        }
+        // Halving: a lane keeps half of its tiles and gives the others away, until it has one.
+#pragma unroll
+        for (int m = kTiles / 2, bit = 16; m > 0; m /= 2, bit /= 2)
+#pragma unroll
+            for (int k = 0; k < m; ++k) {
+                const bool up = lane & bit;
+                const Sum give = up ? tile[k] : tile[m + k];
+                tile[k] = up ? tile[m + k] : tile[k];
+                add(tile[k], __shfl_xor_sync(kFull, give.hi, bit), __shfl_xor_sync(kFull, give.lo, bit));
+            }
+        Sum one = tile[0];
+#pragma unroll
+        for (int o = kStep / 2; o > 0; o >>= 1) {
+            const float h = __shfl_xor_sync(kFull, one.hi, o), l = __shfl_xor_sync(kFull, one.lo, o);
+            add(one, h, l);
+        }
+        return one;
     };
     int turn = 0;
-    // Every CTA's word, gathered: s_cta[turn][c] and the sum of all, in the
-    // order of the parts. Leaves the warps' own sums in s_warp[turn].
-    auto total_of = [&](const Row &r, double a) {
-        const float ah = (float)a, al = (float)(a - (double)ah);
-        Sum t = {0.f, 0.f};
-#pragma unroll 4
-        for (int v = r.v0 + lane; v < r.v1; v += 32) {
-            Sum w[VEC];
-            weights(r, v, ah, al, w);
-#pragma unroll
-            for (int k = 0; k < VEC; ++k)
-                add(t, w[k].hi, w[k].lo);
+    // With one CTA a sequence there is nobody to wait for beyond it.
+    auto barrier = [&] {
+        if (cluster > 1)
+            cluster_barrier();
+        else
+            __syncthreads();
+    };
+    // Every CTA's word: lane c gets that of CTA c.
+    auto exchange = [&](unsigned long long mine) {
+        if (cluster == 1)
+            return mine;
+        if (tid == 0)
+            s_cta[turn] = mine;
+        cluster_barrier();
+        return lane < cluster ? load_from(&s_cta[turn], lane) : 0ull;
+    };
+    // The sum of max(p - a q, 0) over the row. Leaves what draw needs: lane w's
+    // sum of this CTA's warp w and those up to it, lane c's of CTA c, and the
+    // sums of this warp's tiles in s_tile (of groups of whole chunks where they
+    // are more than kEntries).
+    Sum warp_share, warp_upto, cta_share, cta_upto;
+    auto tiles_per_entry = [&](const Row &r) {
+        const int tiles = (r.v1 - r.v0 + 31) / 32;
+        return tiles <= kEntries ? 1 : (tiles + kEntries * kTiles - 1) / (kEntries * kTiles) * kTiles;
+    };
+    auto total_of = [&](const Row &r, const Sum &a) {
+        const int group = tiles_per_entry(r);
+        Sum mine = {0.f, 0.f}, entry = {0.f, 0.f};
+        __syncwarp();
+        for (int v = r.v0, t = 0; v < r.v1; v += 32 * kTiles, t += kTiles) {
+            const Sum one = chunk(r, v, a);
+            const Sum all = shfl(running<kStep>(one), 31);
+            add(mine, all.hi, all.lo);
+            if (group == 1) {
+                if (lane % kStep == 0 && t + lane / kStep < kEntries)
+                    s_tile[warp][t + lane / kStep] = make_float2(one.hi, one.lo);
+            } else {
+                if (t % group == 0)
+                    entry = Sum{0.f, 0.f};
+                add(entry, all.hi, all.lo);
+                if (lane == 0)
+                    s_tile[warp][t / group] = make_float2(entry.hi, entry.lo);
+            }
         }
-        const double mine = warp_sum(t);
         turn ^= 1;
         if (lane == 0)
-            s_warp[turn][warp] = mine;
+            s_warp[turn][warp] = bits_of(mine);
         __syncthreads();
-        if (tid == 0) {
-            double c = 0.0;
-            for (int w = 0; w < kVerifyWarps; ++w)
-                c += s_warp[turn][w];
-            s_out[turn] = (unsigned long long)__double_as_longlong(c);
-        }
-        cluster_barrier();
-        if (tid < cluster)
-            s_cta[turn][tid] = __longlong_as_double((long long)load_from(&s_out[turn], tid));
-        __syncthreads();
-        double z = 0.0;
-        for (int c = 0; c < cluster; ++c)
-            z += s_cta[turn][c];
-        return z;
+        warp_share = lane < kVerifyWarps ? sum_of(s_warp[turn][lane]) : Sum{0.f, 0.f};
+        warp_upto = running<1>(warp_share);
+        cta_share = sum_of(exchange(bits_of(shfl(warp_upto, 31))));
+        if (cluster == 1 && lane > 0)
+            cta_share = Sum{0.f, 0.f};
+        cta_upto = running<1>(cta_share);
+        return shfl(cta_upto, 31);
     };
-    // A token drawn from max(p - a q, 0), whose sum z total_of has just left
-    // behind. Every CTA gets it.
-    auto draw = [&](const Row &r, double a, double z, float u) {
-        const double t = (double)u * z;
-        // The last CTA and warp with a positive sum takes what rounding leaves over.
-        double before = 0.0;
-        int owner = -1, last = -1;
-        for (int c = 0; c < cluster; ++c) {
-            const double x = s_cta[turn][c];
-            if (x > 0.0) {
-                last = c;
-                if (owner < 0 && before + x > t)
-                    owner = c;
-            }
-            if (owner < 0)
-                before += x;
-        }
-        const bool over = owner < 0;
-        if (over)
-            owner = last;
-        if (owner == rank) {
-            if (over)
-                before = -DBL_MAX;
-            int w_owner = -1, w_last = -1;
-            double w_before = before;
-            for (int w = 0; w < kVerifyWarps; ++w) {
-                const double x = s_warp[turn][w];
-                if (x > 0.0) {
-                    w_last = w;
-                    if (w_owner < 0 && w_before + x > t)
-                        w_owner = w;
+    // Of the lanes' shares the first whose running sum, on top of `run`, passes t;
+    // run becomes the sum before it. Where rounding leaves none, the last share
+    // above 0, and `sure` is false.
+    auto holder = [&](const Sum &share, const Sum &upto, const Sum &t, Sum &run, bool &sure) {
+        Sum here = run;
+        add(here, upto.hi, upto.lo);
+        const unsigned some = __ballot_sync(kFull, share.hi > 0.f);
+        const unsigned over = __ballot_sync(kFull, share.hi > 0.f && above(here, t));
+        sure = over != 0u;
+        const int at = over ? __ffs(over) - 1 : some ? 31 - __clz(some) : 0;
+        const Sum before = shfl(upto, at ? at - 1 : 0);
+        if (at)
+            add(run, before.hi, before.lo);
+        return at;
+    };
+    // A token drawn from max(p - a q, 0), whose sum z total_of has just given.
+    auto draw = [&](const Row &r, const Sum &a, const Sum &z, float u) {
+        const Sum t = times(u, z);
+        Sum run = {0.f, 0.f};
+        bool sure = true;
+        const int owner = holder(cta_share, cta_upto, t, run, sure);
+        if (rank == owner && warp == holder(warp_share, warp_upto, t, run, sure)) {
+            const bool with_q = DRAFT && a.hi != 0.f;
+            const int group = tiles_per_entry(r), entries = ((r.v1 - r.v0 + 31) / 32 + group - 1) / group;
+            int found = -1, at = -1;
+            for (int e0 = 0; sure && e0 < entries; e0 += 32) {
+                const float2 e = e0 + lane < entries ? s_tile[warp][e0 + lane] : make_float2(0.f, 0.f);
+                const Sum share = {e.x, e.y}, upto = running<1>(share);
+                Sum before = run;
+                bool here;
+                const int k = holder(share, upto, t, before, here);
+                if (here) {
+                    run = before;
+                    at = e0 + k;
+                    break;
                 }
-                if (w_owner < 0)
-                    w_before += x;
+                const Sum all = shfl(upto, 31);
+                add(run, all.hi, all.lo);
             }
-            if (w_owner < 0) {  // rounding: the last part's last positive entry
-                w_owner = w_last;
-                w_before = -DBL_MAX;
-            }
-            if (warp == w_owner) {
-                const float ah = (float)a, al = (float)(a - (double)ah);
-                double run = w_before;
-                int found = -1, positive = -1;
-                for (int v0 = r.v0; v0 < r.v1 && found < 0; v0 += 32) {
-                    const int v = v0 + lane;
-                    Sum w[VEC], mine = {0.f, 0.f};
-                    if (v < r.v1)
-                        weights(r, v, ah, al, w);
+            for (int k = 0; at >= 0 && k < group && found < 0; ++k) {
+                const int v = r.v0 + 32 * (at * group + k) + lane;
+                Sum e[VEC], w = {0.f, 0.f};
+                if (v < r.v1)
+                    weights(load(r.p, r.mis, v, true), with_q ? load(r.q, r.mis, v, r.q_vec) : none, a, e);
 #pragma unroll
-                    for (int k = 0; k < VEC; ++k) {
-                        if (v >= r.v1)
-                            w[k] = Sum{0.f, 0.f};
-                        add(mine, w[k].hi, w[k].lo);
-                    }
-                    Sum incl = mine;
+                for (int j = 0; j < VEC; ++j) {
+                    if (v >= r.v1)
+                        e[j] = Sum{0.f, 0.f};
+                    add(w, e[j].hi, e[j].lo);
+                }
+                const Sum upto = running<1>(w);
+                Sum before = run;
+                bool here;
+                const int l = holder(w, upto, t, before, here);
+                const unsigned some = __ballot_sync(kFull, w.hi > 0.f);
+                if (here || (group == 1 && some)) {  // this lane's entries, one after the other
+                    int mine = -1;
+                    bool done = false;
 #pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const float h = __shfl_up_sync(kFull, incl.hi, o), l = __shfl_up_sync(kFull, incl.lo, o);
-                        if (lane >= o)
-                            add(incl, h, l);
-                    }
-                    const float eh = __shfl_up_sync(kFull, incl.hi, 1), el = __shfl_up_sync(kFull, incl.lo, 1);
-                    Sum at = lane ? Sum{eh, el} : Sum{0.f, 0.f};
-                    int here = -1;
-#pragma unroll
-                    for (int k = 0; k < VEC; ++k) {
-                        if (w[k].hi > 0.f) {
-                            add(at, w[k].hi, w[k].lo);
-                            positive = v * VEC + k - r.mis;
-                            if (here < 0 && run + value(at) > t)
-                                here = positive;
+                    for (int j = 0; j < VEC; ++j)
+                        if (e[j].hi > 0.f && !done) {
+                            add(before, e[j].hi, e[j].lo);
+                            mine = v * VEC + j - r.mis;
+                            done = above(before, t);
                         }
-                    }
-                    const unsigned hit = __ballot_sync(kFull, here >= 0);
-                    if (hit)
-                        found = __shfl_sync(kFull, here, __ffs(hit) - 1);
-                    run += value(Sum{__shfl_sync(kFull, incl.hi, 31), __shfl_sync(kFull, incl.lo, 31)});
+                    found = __shfl_sync(kFull, mine, l);
                 }
-                positive = __reduce_max_sync(kFull, positive);
-                if (lane == 0)
-                    s_token_out[turn] = (unsigned long long)(found >= 0 ? found : max(positive, 0));
+                const Sum all = shfl(upto, 31);
+                add(run, all.hi, all.lo);
             }
+            if (found < 0) {  // rounding: the part's last positive entry
+                for (int v = r.v0 + lane; v < r.v1; v += 32) {
+                    Sum e[VEC];
+                    weights(load(r.p, r.mis, v, true), with_q ? load(r.q, r.mis, v, r.q_vec) : none, a, e);
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j)
+                        if (e[j].hi > 0.f)
+                            found = v * VEC + j - r.mis;
+                }
+                found = max(0, __reduce_max_sync(kFull, found));
+            }
+            if (lane < cluster)
+                store_to(&s_drawn[turn], lane, found);
         }
-        cluster_barrier();
-        return (int)load_from(&s_token_out[turn], owner < 0 ? 0 : owner);
+        barrier();
+        return *const_cast<volatile int *>(&s_drawn[turn]);
     };
     // The row's first largest entry, NaN passed over.
     auto largest = [&](const Row &r) {
         float best = -INFINITY;
         int at = 0x7fffffff;
-#pragma unroll 4
-        for (int v = r.v0 + lane; v < r.v1; v += 32) {
-            float x[VEC];
-            load(r.p, r.mis, v, true, x);
-            const int i0 = v * VEC - r.mis;
+        for (int v = r.v0; v < r.v1; v += 32 * kTiles) {
+            uint4 raw[kTiles];
 #pragma unroll
-            for (int k = 0; k < VEC; ++k)
-                if (i0 + k >= 0 && i0 + k < V && x[k] > best) {
-                    best = x[k];
-                    at = i0 + k;
-                }
+            for (int t = 0; t < kTiles; ++t)
+                raw[t] = v + 32 * t + lane < r.v1 ? load(r.p, r.mis, v + 32 * t + lane, true) : none;
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) {
+                float x[VEC];
+                widen<T>(raw[t], x);
+                const int i0 = (v + 32 * t + lane) * VEC - r.mis;
+#pragma unroll
+                for (int k = 0; k < VEC; ++k)
+                    if (v + 32 * t + lane < r.v1 && i0 + k >= 0 && i0 + k < V && x[k] > best) {
+                        best = x[k];
+                        at = i0 + k;
+                    }
+            }
         }
         // Ordered as whole numbers: the larger value first, then the lower index.
         const uint32_t b = __float_as_uint(best + 0.f);
@@ -460,17 +648,19 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_draft_kernel(const Veri
             key = max(key, __shfl_xor_sync(kFull, key, o));
         turn ^= 1;
         if (lane == 0)
-            s_best[warp] = key;
+            s_warp[turn][warp] = key;
         __syncthreads();
-        if (tid == 0) {
-            for (int w = 0; w < kVerifyWarps; ++w)
-                key = max(key, s_best[w]);
-            s_out[turn] = key;
+        auto most = [&] {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                key = max(key, __shfl_xor_sync(kFull, key, o));
+        };
+        key = lane < kVerifyWarps ? s_warp[turn][lane] : 0ull;
+        most();
+        if (cluster > 1) {
+            key = exchange(key);
+            most();
         }
-        cluster_barrier();
-        key = 0ull;
-        for (int c = 0; c < cluster; ++c)
-            key = max(key, load_from(&s_out[turn], c));
         const int i = (int)(0x7fffffffu - (uint32_t)key);
         return i < V ? i : 0;
     };
@@ -478,43 +668,49 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_draft_kernel(const Veri
     int node = 0;
     for (int k = 0; k < n; ++k) {  // each step goes to a later node
         int next = n, token = 0;
-        double a = 0.0, z = 1.0;  // draft: see above
         const Row r = row_at(node);
-        if constexpr (MODE == kDraft) {
-            for (int kid = child_of(node, node); kid < n;) {
-                double rx = s_p[kid];
-                const double qx = s_q[kid];
-                if (a > 0.0)
-                    rx = fmax(rx - a * qx, 0.0);
-                if ((double)p.uniforms[2 * (q0 + kid)] * qx * z < rx) {
-                    next = kid;
+        if constexpr (MODE == kGreedy) {
+            token = largest(r);
+        } else {
+            Sum a = {0.f, 0.f}, z = {1.f, 0.f};  // draft: see above
+            int kid = DRAFT ? child_of(node, node) : n;
+            for (;;) {
+                if constexpr (DRAFT) {
+                    if (kid < n) {
+                        const Sum rx = a.hi > 0.f ? weight(s_p[kid], s_q[kid], a) : Sum{s_p[kid], 0.f};
+                        // u q, a pair, times Z
+                        const float h = __fmul_rn(s_u[kid], s_q[kid]);
+                        Sum bar = times(h, z);
+                        bar.lo += fmaf(s_u[kid], s_q[kid], -h) * z.hi;
+                        if (above(rx, bar)) {
+                            next = kid;
+                            break;
+                        }
+                        add(a, z.hi, z.lo);
+                        const float lead = a.hi + a.lo;
+                        a = Sum{lead, a.lo - (lead - a.hi)};
+                        kid = child_of(node, kid);
+                    }
+                }
+                z = total_of(r, a);
+                if (DRAFT && kid < n)
+                    continue;
+                if (z.hi > 0.f && z.hi <= FLT_MAX) {
+                    token = draw(r, a, z, p.uniforms[2 * (q0 + node) + 1]);
                     break;
                 }
-                a += z;
-                kid = child_of(node, kid);
-                if (kid < n)
-                    z = total_of(r, a);
+                if (a.hi == 0.f) {
+                    if (rank == 0 && tid == 0)
+                        tree_raise(PA_DEVERR_TREE);
+                    break;
+                }
+                a = Sum{0.f, 0.f};  // nothing is left of the row: the target's own
             }
         }
-        if (next == n) {
-            if constexpr (MODE == kGreedy) {
-                token = largest(r);
-            } else {
-                z = total_of(r, a);
-                if (!(z > 0.0 && z <= DBL_MAX) && a > 0.0) {
-                    a = 0.0;  // nothing is left of the row: the target's own
-                    z = total_of(r, a);
-                }
-                if (z > 0.0 && z <= DBL_MAX)
-                    token = draw(r, a, z, p.uniforms[2 * (q0 + node) + 1]);
-                else if (rank == 0 && tid == 0)
-                    tree_raise(PA_DEVERR_TREE);
-            }
-            if constexpr (MODE != kDraft) {
-                next = child_of(node, node);
-                while (next < n && s_token[next] != token)
-                    next = child_of(node, next);
-            }
+        if constexpr (!DRAFT) {
+            next = child_of(node, node);
+            while (next < n && s_token[next] != token)
+                next = child_of(node, next);
         }
         if (rank == 0 && tid == 0) {
             p.path[q0 + k] = node;
@@ -526,7 +722,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_draft_kernel(const Veri
             break;
         node = next;
     }
-    cluster_barrier();  // nobody leaves while its shared memory may be read
+    barrier();  // nobody leaves while its shared memory may be read
 }
 
 // ----------------------------------------------------------- pa_commit_draft
@@ -558,13 +754,17 @@ __device__ __forceinline__ bool commit_row(const CommitParams &p, int s, int &q0
            L <= (long long)p.max_blocks_per_seq * p.block_size && (n == 0 || (k >= 0 && k <= n));
 }
 
-constexpr int kMoveThreads = 256, kMoveBatch = 8;
+constexpr int kMoveThreads = 256, kMoveBatch = 8, kMoveCtas = 16;
 
-// Moves: a thread takes one 16-byte column of one layer's K or V rows and all
-// of a sequence's accepted tokens, in ascending order, kMoveBatch of them read
-// before the first is written. Token path[j] >= j goes to place j, so a write
-// never reaches a row that a later batch still reads, and no other thread
-// touches the column: no copy in between, no barrier. HBM bounds it.
+// Moves: a thread takes one 16-byte column of one layer's K or V rows (then
+// another) and all of a sequence's accepted tokens, in ascending order,
+// kMoveBatch of them read before the first is written. Token path[j] >= j goes
+// to place j, so a write never reaches a row that a later batch still reads, and
+// no other thread touches the column: no copy in between, no barrier. HBM bounds
+// it: 64 sequences, 192 moved tokens, 40 layers of 40 heads of 128 fp16 (315 MB
+// read and written) 57 us, 5.5 TB/s; 69 us with a CTA for every 256 columns,
+// whose look-ups of the slots (count, path, table, one after the other) then
+// took as long as its copies.
 __global__ void __launch_bounds__(kMoveThreads) commit_move_kernel(const __grid_constant__ CommitLayers layers, const CommitParams p)
 {
     __shared__ long long s_from[kMaxNodes], s_to[kMaxNodes];
@@ -603,22 +803,21 @@ __global__ void __launch_bounds__(kMoveThreads) commit_move_kernel(const __grid_
             tree_raise(PA_DEVERR_TREE);
         return;
     }
-    const long long columns = 2LL * p.num_layers * p.row_vecs;
-    const long long c = (long long)blockIdx.x * kMoveThreads + tid;
-    if (c >= columns)
-        return;
-    const int lk = (int)(c / p.row_vecs), v = (int)(c - (long long)lk * p.row_vecs);
-    uint4 *col = layers.p[lk >> 1] + (lk & 1) * p.half_vecs + v;
-    for (int j0 = 0; j0 < k; j0 += kMoveBatch) {
-        uint4 x[kMoveBatch];
+    const int columns = 2 * p.num_layers * p.row_vecs;
+    for (int c = blockIdx.x * kMoveThreads + tid; c < columns; c += gridDim.x * kMoveThreads) {
+        const int lk = c / p.row_vecs, v = c - lk * p.row_vecs;
+        uint4 *col = layers.p[lk >> 1] + (lk & 1) * p.half_vecs + v;
+        for (int j0 = 0; j0 < k; j0 += kMoveBatch) {
+            uint4 x[kMoveBatch];
 #pragma unroll
-        for (int b = 0; b < kMoveBatch; ++b)
-            if (j0 + b < k && s_to[j0 + b] >= 0)
-                x[b] = col[s_from[j0 + b]];
+            for (int b = 0; b < kMoveBatch; ++b)
+                if (j0 + b < k && s_to[j0 + b] >= 0)
+                    x[b] = col[s_from[j0 + b]];
 #pragma unroll
-        for (int b = 0; b < kMoveBatch; ++b)
-            if (j0 + b < k && s_to[j0 + b] >= 0)
-                col[s_to[j0 + b]] = x[b];
+            for (int b = 0; b < kMoveBatch; ++b)
+                if (j0 + b < k && s_to[j0 + b] >= 0)
+                    col[s_to[j0 + b]] = x[b];
+        }
     }
 }
 
@@ -751,12 +950,6 @@ int tree_setup(const char *who, int *sms_out)
     sms = dev < 64 ? sm_count[dev] : 0;
     if (sms == 0) {
         e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-        for (int dtype : {PA_F16, PA_BF16, PA_F32})
-            for (int mode = kGreedy; mode <= kDraft && e == cudaSuccess; ++mode)
-                e = cudaFuncSetAttribute(verify_kernel(dtype, mode), cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(reinterpret_cast<const void *>(&build_tree_kernel),
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxNodes / 32 * kMaxNodes * 4);
         if (e != cudaSuccess)
             return set_error(PA_ERR_CUDA, "%s: kernel attributes: %s", who, cudaGetErrorString(e));
         if (dev < 64)
@@ -782,14 +975,13 @@ extern "C" int pa_build_tree(const int32_t *parents, const int32_t *cu_seqlens_q
         return set_error(PA_ERR_INVALID_ARG, "%s: null pointer argument", who);
     if (!aligned(parents, 4) || !aligned(cu_seqlens_q, 4) || !aligned(seq_lens, 4) || !aligned(positions, 4) || !aligned(tree_masks, 4))
         return set_error(PA_ERR_INVALID_ARG, "%s: misaligned pointer (4 B)", who);
-    int sms = 0;
-    const int rc = tree_setup(who, &sms);
-    if (rc != PA_OK)
-        return rc;
-    // A thread per word of the largest tree's masks, up to a full CTA.
-    const int threads = std::max(64, std::min(1024, 32 * mask_words * mask_words));
-    build_tree_kernel<<<num_seqs, threads, (size_t)32 * mask_words * mask_words * 4, reinterpret_cast<cudaStream_t>(stream)>>>(
-        parents, cu_seqlens_q, seq_lens, total_q, mask_words, positions, reinterpret_cast<uint32_t *>(tree_masks));
+    // A thread per word of 32 nodes' masks.
+    int lane_words = 1;
+    while (lane_words < std::min(mask_words, kGroupWords))
+        lane_words *= 2;
+    const dim3 grid(num_seqs, (mask_words + kGroupWords - 1) / kGroupWords);
+    build_tree_kernel<<<grid, 32 * lane_words, (size_t)32 * mask_words * lane_words * 4, reinterpret_cast<cudaStream_t>(stream)>>>(
+        parents, cu_seqlens_q, seq_lens, total_q, mask_words, lane_words, positions, reinterpret_cast<uint32_t *>(tree_masks));
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess)
         return set_error(PA_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
@@ -822,9 +1014,15 @@ extern "C" int pa_verify_draft(int32_t *num_accepted, int32_t *path, int32_t *to
     const int rc = tree_setup(who, &sms);
     if (rc != PA_OK)
         return rc;
-    // CTAs a sequence: as many as about two an SM allow, of 2048 entries at least.
+    // CTAs a sequence: as many as run at once, up to those that leave a warp one
+    // chunk of a row. Measured with 1 / 2 / 4 / 8 of them: 256 sequences, drafter's
+    // rows, 32000 entries 19.9 / 28.6 / 42.9 / 77.0 us; 48 sequences, drawn, 100003
+    // entries 62 / 38 / 28.8 / 24.3; one, greedy, 131072 entries 30.6 / 19.4 / 12.8 /
+    // 9.4 (clusters of 16, or CTAs of 512 threads, are slower in each).
+    const int mode = !uniforms ? kGreedy : draft ? kDraft : kSample;
+    const long long chunk = kVerifyWarps * kTiles * 512 / (int)elem, room = (long long)sms * verify_ctas(mode);
     int cluster = 1;
-    while (cluster < kMaxCluster && (long long)num_seqs * cluster * 2 <= 2 * sms && vocab_size >= 2048 * cluster * 2)
+    while (cluster < kMaxCluster && cluster * chunk < vocab_size && 2LL * num_seqs * cluster <= room)
         cluster *= 2;
     VerifyParams prm{num_accepted, path, tokens_out, tokens, parents, cu_seqlens_q, target, draft,
                      uniforms, target_stride, draft_stride, total_q, vocab_size};
@@ -840,7 +1038,7 @@ extern "C" int pa_verify_draft(int32_t *num_accepted, int32_t *path, int32_t *to
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     void *args[] = {&prm, &cluster};
-    const cudaError_t e = cudaLaunchKernelExC(&cfg, verify_kernel(dtype, !uniforms ? kGreedy : draft ? kDraft : kSample), args);
+    const cudaError_t e = cudaLaunchKernelExC(&cfg, verify_kernel(dtype, mode), args);
     if (e != cudaSuccess)
         return set_error(PA_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
     return PA_OK;
@@ -899,7 +1097,16 @@ extern "C" int pa_commit_draft(void *const *kv_caches, int num_layers, const int
     prm.row_vecs = (int)(row_bytes / 16);
     prm.half_vecs = (long long)num_blocks * block_size * prm.row_vecs;
     const long long columns = 2LL * num_layers * prm.row_vecs;
-    const dim3 grid((unsigned)((columns + kMoveThreads - 1) / kMoveThreads), num_seqs);
+    if (columns > 0x3fffffffLL)
+        return set_error(PA_ERR_UNSUPPORTED, "%s: %d layers of rows of %lld bytes are too many columns", who, num_layers, row_bytes);
+    int sms = 0;
+    const int rc = tree_setup(who, &sms);
+    if (rc != PA_OK)
+        return rc;
+    // A CTA looks its sequence's slots up once and then takes several columns a
+    // thread: about kMoveCtas CTAs an SM in all.
+    const long long most = (columns + kMoveThreads - 1) / kMoveThreads;
+    const dim3 grid((unsigned)std::min(most, std::max(1LL, (long long)sms * kMoveCtas / num_seqs)), num_seqs);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     commit_move_kernel<<<grid, kMoveThreads, 0, st>>>(layers, prm);
     cudaError_t e = cudaGetLastError();
