@@ -49,7 +49,8 @@ int encode_kv_map(CUtensorMap *m, const void *kv, int num_blocks, int block_size
 // An FP8 pool as rank 5 (head_size bytes, kv_heads, block slots, blocks,
 // K|V), box of the d codes of one head x 16 slots: 128-byte rows with the
 // 128-byte swizzle at d = 128 (2 KB), plain 64-byte rows at d = 64 (1 KB).
-int encode_kv_map_fp8(CUtensorMap *m, const void *kv, int num_blocks, int block_size, int num_kv_heads, int d)
+// Tree attention's MMAs read the codes as they lie: 64-byte rows are swizzled there.
+int encode_kv_map_fp8(CUtensorMap *m, const void *kv, int num_blocks, int block_size, int num_kv_heads, int d, bool swizzle64)
 {
     const cuuint64_t hd = (cuuint64_t)d;
     cuuint64_t dims[5] = {hd, (cuuint64_t)num_kv_heads, (cuuint64_t)block_size, (cuuint64_t)num_blocks, 2};
@@ -59,7 +60,7 @@ int encode_kv_map_fp8(CUtensorMap *m, const void *kv, int num_blocks, int block_
     cuuint32_t estr[5] = {1, 1, 1, 1, 1};
     CUresult r = encoder()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void *>(kv), dims, strides, box, estr,
                            CU_TENSOR_MAP_INTERLEAVE_NONE,
-                           d == kD ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                           d == kD ? CU_TENSOR_MAP_SWIZZLE_128B : swizzle64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE,
                            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? PA_OK : set_error(PA_ERR_CUDA, "pa_prefill_fp8: K/V tensor map (%d)", (int)r);
 }
@@ -291,7 +292,10 @@ int prefill_impl(const char *who, void *out, const void *query, const void *kv_c
     prm.group = group;
     prm.heads_per_cta = lp.heads_per_cta;
     prm.head_tiles = lp.head_tiles;
-    prm.rows_per_head = lp.rows_per_head;
+    const bool solo = max_seqlen_q <= lp.rows_per_head;
+    // A tree's one query tile holds no more rows of a head than it needs, so
+    // that whole warps are without one.
+    prm.rows_per_head = sees == Sees::kTree && solo ? (max_seqlen_q + 7) & ~7 : lp.rows_per_head;
     prm.q_pairs = lp.q_pairs;
     prm.max_q = max_seqlen_q;
     prm.num_blocks = num_blocks;
@@ -303,6 +307,7 @@ int prefill_impl(const char *who, void *out, const void *query, const void *kv_c
     prm.tree_masks = reinterpret_cast<const uint32_t *>(tree_masks);
     prm.mask_words = mask_words;
     prm.kv_cache = kv_cache;
+    prm.query = query;
     prm.num_kv_heads = num_kv_heads;
     prm.num_units = (int)lp.units;
     prm.part_o = split ? static_cast<float *>(workspace) : nullptr;
@@ -312,7 +317,7 @@ int prefill_impl(const char *who, void *out, const void *query, const void *kv_c
     prm.jobs = split ? reinterpret_cast<int4 *>(prm.part_ml + (size_t)lp.split_grid * 2 * 2 * kM) : nullptr;
 
     CUtensorMap kv_map, q_map;
-    rc = fp8 ? encode_kv_map_fp8(&kv_map, kv_cache, num_blocks, block_size, num_kv_heads, head_size)
+    rc = fp8 ? encode_kv_map_fp8(&kv_map, kv_cache, num_blocks, block_size, num_kv_heads, head_size, sees == Sees::kTree)
                  : encode_kv_map(&kv_map, kv_cache, num_blocks, block_size, num_kv_heads, head_size);
     if (rc != PA_OK)
         return rc;
@@ -335,7 +340,6 @@ int prefill_impl(const char *who, void *out, const void *query, const void *kv_c
                                             PA_PREFILL_INSTANCES(false, kCross), PA_PREFILL_INSTANCES(true, kCross),
                                             PA_PREFILL_INSTANCES(false, kCrossSolo), PA_PREFILL_INSTANCES(true, kCrossSolo)};
 #undef PA_PREFILL_INSTANCES
-    const bool solo = max_seqlen_q <= lp.rows_per_head;
     const int kind = sees == Sees::kCausal ? kCausal : sees == Sees::kAll ? (solo ? kCrossSolo : kCross) : solo ? kTreeSolo : kTree;
     const int type = (split ? 8 : 0) + (fp8 ? 4 : 0) + (d64 ? 2 : 0) + (bf ? 1 : 0);
     const int variant = kind * 16 + type;

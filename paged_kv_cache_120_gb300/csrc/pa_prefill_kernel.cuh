@@ -128,6 +128,34 @@ __device__ __forceinline__ void tc_mma(uint32_t d_tmem, uint64_t a, uint64_t b, 
         : "memory");
 }
 
+// The same for 8-bit operands (kind::f8f6f4, fp32 accumulator, both K-major): A
+// is E4M3 or E5M2, B E4M3.
+__device__ __forceinline__ uint32_t instr_desc8(int m, int n, bool a_e5m2)
+{
+    return 1u << 4 | (a_e5m2 ? 1u : 0u) << 7 | (uint32_t)(n >> 3) << 17 | (uint32_t)(m >> 4) << 24;
+}
+
+// Descriptor of a K-major operand of 8-bit rows: 128 of them (128-byte swizzle) or 64 (64-byte swizzle).
+template <int D>
+__device__ __forceinline__ uint64_t smem_desc8(uint32_t addr)
+{
+    uint64_t d = (uint64_t)((addr >> 4) & 0x3FFF);
+    d |= (uint64_t)1 << 16;
+    d |= (uint64_t)((8 * D) >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)(D == 128 ? 2 : 4) << 61;
+    return d;
+}
+
+__device__ __forceinline__ void tc_mma8(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 // Arrive once on `bar` when every MMA this thread issued so far has completed.
 __device__ __forceinline__ void tc_commit(uint32_t bar)
 {
@@ -185,6 +213,38 @@ __device__ __forceinline__ void tc_st32(uint32_t taddr, const float *v)
         : "memory");
 }
 
+// The same for 16 columns, and their store: short code for what rarely runs.
+__device__ __forceinline__ void tc_ld16(uint32_t taddr, float *v)
+{
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ void tc_st16(uint32_t taddr, const float *v)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]), "f"(v[10]),
+        "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+        : "memory");
+}
+
+__device__ __forceinline__ void tc_st8u(uint32_t taddr, const uint32_t *v)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 // O += A B with A read from TMEM (32-bit columns holding two 16-bit
 // elements, the lower-indexed one in the low half) and B from shared memory.
 __device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
@@ -194,6 +254,46 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
         "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// The same issued by one lane of a converged warp: with one query tile a tree's MMA
+// warp runs its loop as a whole (64 x 16 nodes over an FP8 cache of 4096 tokens,
+// 32 / 8 heads: 222 us by a thread of its own, 205 us so; with two tiles it is 3 %
+// slower).
+__device__ __forceinline__ void tc_mma_elected(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\telect.sync _|q, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void tc_mma8_elected(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\telect.sync _|q, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void tc_mma_ts_elected(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+                                                  uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\telect.sync _|q, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void tc_commit_elected(uint32_t bar)
+{
+    asm volatile(
+        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
         : "memory");
 }
 
@@ -210,6 +310,21 @@ __device__ __forceinline__ uint32_t e4m3_pair_hi(uint32_t x)
 {
     uint32_t d;
     asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(d) : "r"(x));
+    return d;
+}
+
+// Two floats to E4M3 (or E5M2) codes, nearest, saturating; `lo` to the low byte.
+__device__ __forceinline__ uint32_t to_e4m3_pair(float lo, float hi)
+{
+    uint32_t d;
+    asm("{\n\t.reg .b16 r;\n\tcvt.rn.satfinite.e4m3x2.f32 r, %1, %2;\n\tcvt.u32.u16 %0, r;\n\t}" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t to_e5m2_pair(float lo, float hi)
+{
+    uint32_t d;
+    asm("{\n\t.reg .b16 r;\n\tcvt.rn.satfinite.e5m2x2.f32 r, %1, %2;\n\tcvt.u32.u16 %0, r;\n\t}" : "=r"(d) : "f"(hi), "f"(lo));
     return d;
 }
 
@@ -354,7 +469,19 @@ constexpr int kPolyEvery = PA_PREFILL_POLY_EVERY;
 constexpr int kUnitSlots = 4;              // ring of unit indices handed from the scheduler to every role
 // Unit consumers (one arrival each): K, V and MMA warps and the 8 softmax
 // warps; with an FP8 cache the 4 widening warps instead of K and V.
-__host__ __device__ constexpr int unit_consumers(bool fp8) { return fp8 ? 13 : 11; }
+__host__ __device__ constexpr int unit_consumers(bool fp8, bool native) { return native ? 14 : fp8 ? 13 : 11; }
+// Tree attention over an FP8 cache ("native"): the scores' MMAs take K's codes
+// as they are, and the queries as a sum of 8-bit terms, each the nearest code to
+// what the ones before leave: two E4M3 terms hold a bf16 element (8 bits, 4 and 4
+// with the second's sign), a third, E5M2, an fp16 one; what lies 2^-18 below a
+// row's largest element is lost (2^-25 with the third term). Only V is widened,
+// by four warps a quarter tile each, from staging buffers two or three deep.
+// K and V both widened by two warps each from one buffer, as pa_prefill_fp8 does
+// it, take 2.2 us a tile, three times what the tile takes to arrive.
+constexpr int native_terms(bool bf16) { return bf16 ? 2 : 3; }
+constexpr int native_k_stages(bool bf16, bool solo) { return solo ? 4 : bf16 ? 3 : 2; }
+constexpr int native_staging(bool solo) { return solo ? 3 : 2; }
+constexpr int kNativeKMax = 4, kNativeStagingMax = 3;
 // Registers per thread at launch (65536 / threads, one CTA per SM) and the
 // per-warpgroup split; the sum stays within the launch's total.
 constexpr int kRegsSoftmax16 = 192, kRegsIO16 = 120;  // 384 threads, 168 each at launch
@@ -398,6 +525,7 @@ struct TreeParams : PrefillParams {
     const uint32_t *tree_masks;  // a row of mask_words words per query
     int mask_words;
     const void *kv_cache;        // V once more, where it is not finite
+    const void *query;           // over an FP8 cache the softmax threads read their rows themselves
 };
 template <int KIND>
 using KindParams = std::conditional_t<(KIND >= kTree), TreeParams, PrefillParams>;
@@ -674,7 +802,16 @@ struct PrefillBars {
 // SPLIT: the stream-K instance (few units, K/V ranges shared out evenly);
 // otherwise whole units, each a CTA of the grid.
 //
-// kCrossSolo, kTreeSolo: chunks of at most one query tile, so that no
+// kTreeSolo: trees of at most one query tile. Both softmax warpgroups work on
+// every K/V tile, a row's columns halved between a thread of each (the maximum
+// goes through shared memory), so that a tile's softmax takes half as long; the
+// one O leaves room in tensor memory for P beside S, so that the next tile's
+// scores are there before this one's softmax ends, and the next item's before
+// this one's epilogue does. Measured (FP8 cache, 64 sequences x 16 nodes
+// of 32 / 8 heads over 4096 tokens): 247 us with two query tiles' turn-taking as
+// below, 193 us so; 16-bit caches are bound by HBM either way (208 and 204).
+//
+// kCrossSolo: chunks of at most one query tile, so that no
 // unit has a tile B. B then takes A's queries as well, A the even and B the
 // odd K/V tiles of the item, so that one's matrix work still overlaps the
 // other's softmax, and A folds B's state into its own at the end (disjoint
@@ -689,7 +826,8 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
     __shared__ PrefillBars bars;
     // CROSS: every query tile reads all of the sequence's K/V tiles. TREE: and
     // what of the last tokens a row sees is in its mask.
-    constexpr bool CROSS = KIND != kCausal, TREE = KIND >= kTree, SOLO = KIND == kCrossSolo || KIND == kTreeSolo;
+    // COOP (kTreeSolo): one query tile, its columns shared by both warpgroups.
+    constexpr bool CROSS = KIND != kCausal, TREE = KIND >= kTree, SOLO = KIND == kCrossSolo, COOP = KIND == kTreeSolo;
     constexpr bool kEmptyItems = CROSS && !TREE && !SPLIT;  // items of sequences without tokens
     __shared__ __align__(16) uint4 claim[1];  // whole units: the answer to a claim
     __shared__ uint64_t claim_bar;
@@ -701,6 +839,14 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
     // is not finite (whoever brings V runs at most kUnitSlots items ahead).
     constexpr int kPoisonSlots = 2 * kUnitSlots;
     __shared__ int poison[TREE ? kPoisonSlots : 1];
+    constexpr bool kNative = FP8 && TREE;
+    constexpr int kTerms = native_terms(BF16), kNativeStg = native_staging(COOP);
+    __shared__ uint64_t native_k[kNative ? 2 * kNativeKMax : 1];                 // K stages full, then empty
+    __shared__ uint64_t native_stg[kNative ? 4 * kNativeStagingMax : 1];         // a widening warp's buffer has landed
+    __shared__ uint64_t coop_q[COOP ? 4 : 1];       // Q of an even / odd item has landed, is no longer read
+    __shared__ uint64_t coop_pair[COOP ? 4 : 1];    // the two warps of a quarter of the rows meet
+    __shared__ float coop_row[COOP ? 2 * kM : 1];   // a row's extremum or sum, of either half
+    __shared__ uint8_t coop_grow[COOP ? 16 : 1];    // a warp's rows want another reference (two turns)
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int T = p.rows_per_head, HPC = p.heads_per_cta;
@@ -717,17 +863,23 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
     // the codes widen to fp16 in one instruction per pair and bf16 queries
     // are moved to fp16 (kQToF16) by the softmax threads, row by row.
     constexpr bool kMmaBF16 = BF16 && !FP8;
-    constexpr bool kQToF16 = BF16 && FP8;
-    constexpr int kKStages = FP8 ? kKStages8 : kKStages16;
+    constexpr bool kQToF16 = BF16 && FP8 && !kNative;
+    constexpr int kKStages = kNative ? native_k_stages(BF16, COOP) : FP8 ? kKStages8 : kKStages16;
     constexpr int kVStages = FP8 ? kVStages8 : kVStages16;
-    constexpr int kOffV = kOffK + kKStages * kTileBytes;
+    // Native: Q's terms, then the K ring, both of 8-bit rows.
+    constexpr int kBytes8 = kM * D;
+    constexpr int kOffRingK = kNative ? (COOP ? 1 : 2) * kTerms * kBytes8 : kOffK;
+    constexpr int kStageK = kNative ? kBytes8 : kTileBytes;
+    constexpr int kOffV = kOffRingK + kKStages * kStageK;
     constexpr int kOffStage = kOffV + kVStages * kTileBytes;  // FP8: K then V staging tile
-    auto sK = [&](int st) { return base + kOffK + st * kTileBytes; };
+    static_assert(!kNative || kOffStage + kNativeStg * kBytes8 + 1024 <= kSmemBytes, "shared memory plan");
+    auto sK = [&](int st) { return base + kOffRingK + st * kStageK; };
+    [[maybe_unused]] auto sTerm = [&](int x, int term) { return base + ((COOP ? 0 : x) * kTerms + term) * kBytes8; };
     auto sV = [&](int st) { return base + kOffV + st * kTileBytes; };
     const uint32_t b_q = smem_addr(&bars.q_full), b_qe = smem_addr(&bars.q_empty);
     const uint32_t b_qr = smem_addr(&bars.q_ready);
-    auto b_kf = [&](int st) { return smem_addr(&bars.k_full[st]); };
-    auto b_ke = [&](int st) { return smem_addr(&bars.k_empty[st]); };
+    auto b_kf = [&](int st) { return smem_addr(kNative ? &native_k[st] : &bars.k_full[st]); };
+    auto b_ke = [&](int st) { return smem_addr(kNative ? &native_k[kNativeKMax + st] : &bars.k_empty[st]); };
     auto b_vf = [&](int st) { return smem_addr(&bars.v_full[st]); };
     auto b_ve = [&](int st) { return smem_addr(&bars.v_empty[st]); };
     auto b_s = [&](int x) { return smem_addr(&bars.s_full[x]); };
@@ -747,28 +899,38 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
             mbar_init(smem_addr(&solo_bars[1]), 128);
         }
         for (int st = 0; st < kKStages; ++st) {
-            mbar_init(b_kf(st), FP8 ? 2 : 1);  // FP8: the two widening warps of the tile
+            mbar_init(b_kf(st), FP8 && !kNative ? 2 : 1);  // FP8: the two widening warps of the tile
             mbar_init(b_ke(st), 1);
         }
         for (int st = 0; st < kVStages; ++st) {
-            mbar_init(b_vf(st), FP8 ? 2 : 1);
+            mbar_init(b_vf(st), kNative ? 4 : FP8 ? 2 : 1);
             mbar_init(b_ve(st), 1);
         }
         for (int x = 0; x < 2; ++x) {
             mbar_init(b_s(x), 1);
-            mbar_init(b_p(x), 128);
+            mbar_init(b_p(x), COOP ? 256 : 128);
             mbar_init(b_pv(x), 1);
         }
         for (int i = 0; i < 4; ++i)
             mbar_init(smem_addr(&bars.stg_full[i >> 1][i & 1]), 1);
         for (int i = 0; i < kUnitSlots; ++i) {
             mbar_init(b_uf(i), 1);
-            mbar_init(b_ue(i), unit_consumers(FP8));
+            mbar_init(b_ue(i), unit_consumers(FP8, kNative));
         }
         bars.fail = 0;
         if constexpr (TREE) {
             for (int i = 0; i < kPoisonSlots; ++i)
                 poison[i] = 0;
+        }
+        if constexpr (COOP) {
+            for (int i = 0; i < 4; ++i) {
+                mbar_init(smem_addr(&coop_q[i]), 1);
+                mbar_init(smem_addr(&coop_pair[i]), 2);
+            }
+        }
+        if constexpr (kNative) {
+            for (int i = 0; i < 4 * kNativeStg; ++i)
+                mbar_init(smem_addr(&native_stg[i]), 1);
         }
         fence_barrier_init();
     }
@@ -1038,6 +1200,20 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                     break;
                 if (kEmptyItems && w.L == 0)
                     continue;  // no queries to bring
+                if (kNative)
+                    continue;  // the softmax threads bring them
+                if constexpr (COOP) {
+                    // Two tiles' room for one: an item's queries come while the last one runs.
+                    const uint32_t full = smem_addr(&coop_q[i & 1]);
+                    if (i > 1 && !wait_or_fail(smem_addr(&coop_q[2 + (i & 1)]), ((i >> 1) - 1) & 1))
+                        break;
+                    mbar_expect_tx(full, (uint32_t)(kChunks * HPC * T * 128));
+                    for (int c = 0; c < kChunks; ++c)
+                        for (int g = 0; g < HPC; ++g)
+                            tma_load_3d(sQ(i & 1) + c * kChunkBytes + g * T * 128, &q_map, full, c * 64,
+                                        w.h * p.group + w.ht * HPC + g, w.q0 + w.t0[0]);
+                    continue;
+                }
                 const int qi = kEmptyItems ? loaded++ : i;  // items whose queries were brought before
                 if (qi > 0 && !wait_or_fail(b_qe, (qi - 1) & 1))
                     break;
@@ -1048,13 +1224,13 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                     for (int c = 0; c < kChunks; ++c)
                         for (int g = 0; g < HPC; ++g)
                             tma_load_3d(sQ(x) + c * kChunkBytes + g * T * 128, &q_map, b_q, c * 64, head0 + g,
-                                        w.q0 + w.t0[SOLO ? 0 : x]);
+                                        w.q0 + w.t0[SOLO || COOP ? 0 : x]);
             }
         }
     } else if (warp == kWarpK || warp == kWarpV) {
         // ---------------------------------------------------------- K, V
         const bool is_k = warp == kWarpK;
-        if constexpr (!FP8) {
+        if (!FP8 || (kNative && is_k)) {
             // Warp 8 produces the K tiles, warp 10 the V tiles, each at its own
             // pace through its ring; lane i < 8 moves the 16-token box i of each
             // tile. The block-table entry of the next tile is loaded while the
@@ -1096,8 +1272,12 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                             phys = p.num_blocks;  // past the sequence end: outside the map, zeros
                         const uint32_t full = is_k ? b_kf(st) : b_vf(st);
                         if (lane == leader)
-                            mbar_expect_tx(full, kChunks * kChunkBytes);
+                            mbar_expect_tx(full, kNative ? kBytes8 : kChunks * kChunkBytes);
                         __syncwarp(group_mask);
+                        if constexpr (kNative) {
+                            tma_load_5d(sK(st) + box * (kBoxTokens * D), &kv_map, full, 0, w.h, tib, phys, 0);
+                            continue;
+                        }
                         const uint32_t dst = (is_k ? sK(st) : sV(st)) + box * (kBoxTokens * 128);
                         for (int c = 0; c < kChunks; ++c)
                             tma_load_5d(dst + c * kChunkBytes, &kv_map, full, c * 64, w.h, tib, phys, is_k ? 0 : 1);
@@ -1115,6 +1295,98 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
         // stage in the MMA's layout (rows past the sequence end as zeros),
         // arrives on the stage's full barrier (two arrivals make it full)
         // and requests its half of the next tile.
+        if constexpr (kNative) {
+            // Native: each warp a quarter of every V tile, 32 rows, a row a lane,
+            // from kNativeStg buffers that lanes 0 and 1 fill again once read.
+            const int cw = warp - 12;
+            auto stg = [&](int b) { return base + kOffStage + (uint32_t)((b * 4 + cw) * (32 * D)); };
+            auto b_stg = [&](int b) { return smem_addr(&native_stg[cw * kNativeStg + b]); };
+            const int step_blk = kN / p.block_size, step_off = kN - step_blk * p.block_size;
+            int gc = 0, gi = 0;  // tiles widened, and asked for, by this warp so far
+            bool go = true;
+            for (int i = 0; go; ++i) {
+                Item it;
+                Unit w;
+                if (!take_unit(i, kFull, lane == 0, it, w) || it.u < 0)
+                    break;
+                const int n = SPLIT ? min(max(w.n[0], w.n[1]), it.j1) : max(w.n[0], w.n[1]);
+                const int32_t *table = p.block_tables + (long long)w.s * p.max_blocks_per_seq;
+                // Lanes 0 and 1: the block and the place in it of their 16 tokens,
+                // tile after tile (no division), and its entry of the table, looked
+                // up a tile ahead of its issue, so that nothing waits for it.
+                int kt = it.j0 * kN + cw * 32 + kBoxTokens * lane;
+                int blk = kt / p.block_size, off = kt - blk * p.block_size;
+                auto lookup = [&](int2 &at) {  // {physical block or -1, place}
+                    at = make_int2(lane < 2 && kt < min(w.L, n * kN) ? __ldg(table + blk) : -1, off);
+                    kt += kN;
+                    blk += step_blk;
+                    off += step_off;
+                    if (off >= p.block_size) {
+                        off -= p.block_size;
+                        ++blk;
+                    }
+                };
+                auto issue = [&](int j, int2 at) {
+                    const int b = gi % kNativeStg;
+                    if (lane < 2) {
+                        int phys = at.x;
+                        if (phys >= p.num_blocks || (phys < 0 && j * kN + cw * 32 + kBoxTokens * lane < w.L)) {
+                            prefill_raise(PA_DEVERR_BLOCK_ID);
+                            phys = p.num_blocks;
+                        }
+                        if (phys < 0)
+                            phys = p.num_blocks;  // past the sequence end: outside the map, zeros
+                        if (lane == 0)
+                            mbar_expect_tx(b_stg(b), 32 * D);
+                        __syncwarp(0x3u);
+                        tma_load_5d(stg(b) + lane * (kBoxTokens * D), &kv_map, b_stg(b), 0, w.h, at.y, phys, 1);
+                    }
+                    ++gi;
+                };
+                int2 next;
+                lookup(next);
+#pragma unroll
+                for (int k = 0; k < kNativeStg; ++k)
+                    if (it.j0 + k < n) {
+                        issue(it.j0 + k, next);
+                        lookup(next);
+                    }
+                for (int j = it.j0; j < n; ++j, ++gc) {
+                    const int b = gc % kNativeStg, st = gc % kVStages;
+                    if (!__all_sync(kFull, wait_or_fail(b_stg(b), (gc / kNativeStg) & 1)) ||
+                        (gc >= kVStages && !__all_sync(kFull, wait_or_fail(b_ve(st), ((gc - kVStages) / kVStages) & 1)))) {
+                        go = false;
+                        break;
+                    }
+                    const int r = cw * 32 + lane, tok = j * kN + r;  // row of the tile, token
+                    const bool pad = tok >= w.L, node = tok >= w.L - w.q_len;
+                    const uint32_t from = stg(b) + lane * D, to = sV(st) + r * 128;
+                    bool nan = false;
+#pragma unroll 2
+                    for (int q = 0; q < D / 16; ++q) {
+                        uint4 c = pad ? make_uint4(0u, 0u, 0u, 0u)
+                                      : lds128(from + ((q ^ (D == 128 ? lane & 7 : (lane >> 1) & 3)) << 4));
+                        if (node)
+                            nan |= drop_nan_codes(c);
+                        const uint32_t h[8] = {e4m3_pair_lo(c.x), e4m3_pair_hi(c.x), e4m3_pair_lo(c.y), e4m3_pair_hi(c.y),
+                                               e4m3_pair_lo(c.z), e4m3_pair_hi(c.z), e4m3_pair_lo(c.w), e4m3_pair_hi(c.w)};
+                        const uint32_t row = to + (q >> 2) * kChunkBytes;
+                        const int u0 = 2 * (q & 3);
+                        sts128(row + ((u0 ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
+                        sts128(row + (((u0 + 1) ^ (r & 7)) << 4), h[4], h[5], h[6], h[7]);
+                    }
+                    if (nan)
+                        *const_cast<volatile int *>(&poison[i % kPoisonSlots]) = i + 1;
+                    fence_proxy_async();  // widened rows for the MMA; staging reads before its reuse
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(b_vf(st));
+                    if (j + kNativeStg < n)
+                        issue(j + kNativeStg, next);
+                    lookup(next);
+                }
+            }
+        } else {
         const int cw = warp - 12, part = cw & 1;
         const bool is_k = cw < 2;
         const uint32_t stg = base + kOffStage + cw * (kStageBytes8 / 2);
@@ -1158,14 +1430,6 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                     break;
                 }
                 const uint32_t dst = is_k ? sK(st) : sV(st);
-                // Tree: codes of a node's V that are NaN become 0.
-                auto finite_codes = [&](uint4 c, int r) {
-                    if constexpr (TREE) {
-                        if (!is_k && j * kN + r >= w.L - w.q_len && drop_nan_codes(c))
-                            *const_cast<volatile int *>(&poison[i % kPoisonSlots]) = i + 1;
-                    }
-                    return c;
-                };
 #pragma unroll
                 for (int rr = 0; rr < 2; ++rr) {
                     const int rh = lane + 32 * rr;          // row within the half
@@ -1183,7 +1447,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                         // conflict within a quarter warp.
                         const int q = D == 128 ? qi : qi ^ ((0x78 >> (2 * ((rh >> 1) & 3))) & 3);
                         const uint32_t src = D == 128 ? stg + rh * 128 + ((q ^ (rh & 7)) << 4) : stg + rh * 64 + (q << 4);
-                        const uint4 c = pad ? make_uint4(0u, 0u, 0u, 0u) : finite_codes(lds128(src), r);
+                        const uint4 c = pad ? make_uint4(0u, 0u, 0u, 0u) : lds128(src);
                         // fp16 whatever the query type: the MMAs of the FP8
                         // path run in fp16 (bf16 queries are moved to fp16).
                         const uint32_t h[8] = {e4m3_pair_lo(c.x), e4m3_pair_hi(c.x), e4m3_pair_lo(c.y),
@@ -1204,6 +1468,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                     issue(j + 1);
             }
         }
+        }
     } else if (warp == kWarpMMA) {
         // ---------------------------------------------------------- MMA
         // Per K/V tile j: S_A(0), S_B(0) up front, then for each tile x in
@@ -1211,21 +1476,61 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
         // scores of one tile are computed while the other tile's softmax
         // runs. S_x(j + 1) overwrites P_x(j) in TMEM: MMAs complete in issue
         // order, so the P V that reads it is done first.
-        if (lane == 0) {
+        // COOP: the whole warp, its MMAs and commits by an elected lane.
+        if (COOP || lane == 0) {
+            auto all_ok = [&](bool v) { return COOP ? (bool)__all_sync(kFull, v) : v; };
+            auto mma = [&](uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+                if constexpr (COOP)
+                    tc_mma_elected(d, a, b, id, acc);
+                else
+                    tc_mma(d, a, b, id, acc);
+            };
+            auto mma_ts = [&](uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+                if constexpr (COOP)
+                    tc_mma_ts_elected(d, a, b, id, acc);
+                else
+                    tc_mma_ts(d, a, b, id, acc);
+            };
+            [[maybe_unused]] auto mma8 = [&](uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+                if constexpr (COOP)
+                    tc_mma8_elected(d, a, b, id, acc);
+                else
+                    tc_mma8(d, a, b, id, acc);
+            };
+            auto commit = [&](uint32_t bar) {
+                if constexpr (COOP)
+                    tc_commit_elected(bar);
+                else
+                    tc_commit(bar);
+            };
             const uint32_t id_s = instr_desc(kM, kN, kMmaBF16, false);
             const uint32_t id_o = instr_desc(kM, D, kMmaBF16, true);
             // Descriptors are built once per operand tile; each k step adds
             // its byte offset / 16 to the start-address field (bits 0-13,
             // which cannot carry: shared memory ends below 256 KB).
-            auto issue_s = [&](int x, int ks) {
-                const uint64_t dq = smem_desc(sQ(x), 16, 1024), dk = smem_desc(sK(ks), 16, 1024);
+            // x: the scores' place, and (COOP: qt instead) the query tile.
+            auto issue_s = [&](int x, int ks, int qt = 0) {
+                if constexpr (kNative) {
+                    const uint64_t dk = smem_desc8<D>(sK(ks));
+#pragma unroll
+                    for (int term = 0; term < kTerms; ++term) {
+                        const uint64_t dq = smem_desc8<D>(sTerm(x, term));
+                        const uint32_t id = instr_desc8(kM, kN, term == 2);
+#pragma unroll
+                        for (int k = 0; k < D / 32; ++k)
+                            mma8(tS(x), dq + 2 * k, dk + 2 * k, id, term > 0 || k > 0 ? 1u : 0u);
+                    }
+                    commit(b_s(x));
+                    return;
+                }
+                const uint64_t dq = smem_desc(sQ(COOP ? qt : x), 16, 1024), dk = smem_desc(sK(ks), 16, 1024);
                 const uint32_t ts = tS(x);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     const uint64_t off = (uint64_t)(((k >> 2) * kChunkBytes + (k & 3) * 32) >> 4);
-                    tc_mma(ts, dq + off, dk + off, id_s, k > 0 ? 1u : 0u);
+                    mma(ts, dq + off, dk + off, id_s, k > 0 ? 1u : 0u);
                 }
-                tc_commit(b_s(x));
+                commit(b_s(x));
             };
             int kc = 0, vc = 0, ui = 0;  // K tiles, V tiles and units consumed so far
             int gx[2] = {0, 0};          // P V of tile x issued so far
@@ -1233,7 +1538,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
             for (int i = 0; go; ++i) {
                 Item it;
                 Unit w;
-                if (!take_unit(i, 1u, true, it, w) || it.u < 0)
+                if (!take_unit(i, COOP ? kFull : 1u, lane == 0, it, w) || it.u < 0)
                     break;
                 if (kEmptyItems && w.L == 0)
                     continue;
@@ -1242,30 +1547,71 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                 const int j1 = SPLIT ? min(max(w.n[0], w.n[1]), it.j1) : max(w.n[0], w.n[1]);
                 const int ne_piece[2] = {min(w.n[0], j1), min(w.n[1], j1)};
                 const int *ne = SPLIT ? ne_piece : w.n;
-                if (!wait_or_fail(kQToF16 ? b_qr : b_q, ui & 1))
+                if constexpr (COOP) {
+                    if (!all_ok(kNative ? wait_or_fail(b_qr, ui & 1)
+                                        : wait_or_fail(smem_addr(&coop_q[ui & 1]), (ui >> 1) & 1)))
+                        break;
+                } else if (!all_ok(wait_or_fail(kQToF16 || kNative ? b_qr : b_q, ui & 1)))
                     break;
                 ++ui;
                 tc_fence_after();
+                if constexpr (COOP) {
+                    // Scores run two tiles ahead, into the place whose last ones
+                    // the softmax has read (its P has arrived).
+                    const int qt = (ui - 1) & 1;
+                    auto scores = [&](int j) {
+                        const int ks = kc % kKStages;
+                        if (!all_ok(wait_or_fail(b_kf(ks), (kc / kKStages) & 1)))
+                            return false;
+                        tc_fence_after();
+                        issue_s(kc & 1, ks, qt);
+                        commit(b_ke(ks));
+                        ++kc;
+                        if (!kNative && j + 1 == j1)
+                            commit(smem_addr(&coop_q[2 + qt]));  // Q free once the item's last scores are done
+                        return true;
+                    };
+                    go = scores(j0) && (j0 + 1 >= j1 || scores(j0 + 1));
+                    for (int j = j0; go && j < j1; ++j) {
+                        const int b = vc & 1, vs = vc % kVStages;
+                        if (!all_ok(wait_or_fail(b_vf(vs), (vc / kVStages) & 1)) || !all_ok(wait_or_fail(b_p(b), (vc >> 1) & 1))) {
+                            go = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint64_t dv = smem_desc(sV(vs), kChunkBytes, 1024);
+#pragma unroll
+                        for (int k = 0; k < kN / 16; ++k)
+                            mma_ts(tmem + 384u, tmem + 256u + 64u * b + k * 8, dv + (uint64_t)(k * (2048 >> 4)), id_o,
+                                      (j > j0 || k > 0) ? 1u : 0u);
+                        commit(b_pv(0));
+                        commit(b_ve(vs));
+                        ++vc;
+                        if (j + 2 < j1)
+                            go = scores(j + 2);
+                    }
+                    continue;
+                }
                 if constexpr (SOLO) {
                     // K/V tile j belongs to query tile (j - j0) & 1. Scores
                     // run two tiles ahead; a K stage is free after one S, a V
                     // stage after one P V.
                     auto scores = [&](int j) {
                         const int ks = kc % kKStages;
-                        if (!wait_or_fail(b_kf(ks), (kc / kKStages) & 1))
+                        if (!all_ok(wait_or_fail(b_kf(ks), (kc / kKStages) & 1)))
                             return false;
                         tc_fence_after();
                         issue_s((j - j0) & 1, ks);
-                        tc_commit(b_ke(ks));
+                        commit(b_ke(ks));
                         ++kc;
                         if (j + 1 == j1)
-                            tc_commit(b_qe);  // Q free once the item's last scores are done
+                            commit(b_qe);  // Q free once the item's last scores are done
                         return true;
                     };
                     go = scores(j0) && (j0 + 1 >= j1 || scores(j0 + 1));
                     for (int j = j0; go && j < j1; ++j) {
                         const int x = (j - j0) & 1, vs = vc % kVStages;
-                        if (!wait_or_fail(b_vf(vs), (vc / kVStages) & 1) || !wait_or_fail(b_p(x), gx[x] & 1)) {
+                        if (!all_ok(wait_or_fail(b_vf(vs), (vc / kVStages) & 1)) || !all_ok(wait_or_fail(b_p(x), gx[x] & 1))) {
                             go = false;
                             break;
                         }
@@ -1274,10 +1620,10 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                         const uint32_t to = tO(x), ts = tS(x);
 #pragma unroll
                         for (int k = 0; k < kN / 16; ++k)
-                            tc_mma_ts(to, ts + k * 8, dv + (uint64_t)(k * (2048 >> 4)), id_o,
+                            mma_ts(to, ts + k * 8, dv + (uint64_t)(k * (2048 >> 4)), id_o,
                                       (j > j0 + 1 || k > 0) ? 1u : 0u);
-                        tc_commit(b_pv(x));
-                        tc_commit(b_ve(vs));
+                        commit(b_pv(x));
+                        commit(b_ve(vs));
                         ++gx[x];
                         ++vc;
                         if (j + 2 < j1)
@@ -1287,20 +1633,20 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                 }
                 {
                     const int ks = kc % kKStages;
-                    if (!wait_or_fail(b_kf(ks), (kc / kKStages) & 1))
+                    if (!all_ok(wait_or_fail(b_kf(ks), (kc / kKStages) & 1)))
                         break;
                     tc_fence_after();
                     for (int x = 0; x < 2; ++x)
                         if (ne[x] > j0)
                             issue_s(x, ks);
-                    tc_commit(b_ke(ks));
+                    commit(b_ke(ks));
                     ++kc;
                     if (j1 - j0 == 1)
-                        tc_commit(b_qe);  // Q free once the item's last scores are done
+                        commit(b_qe);  // Q free once the item's last scores are done
                 }
                 for (int j = j0; go && j < j1; ++j) {
                     const int vs = vc % kVStages;
-                    if (!wait_or_fail(b_vf(vs), (vc / kVStages) & 1)) {
+                    if (!all_ok(wait_or_fail(b_vf(vs), (vc / kVStages) & 1))) {
                         go = false;
                         break;
                     }
@@ -1308,7 +1654,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                     for (int x = 0; x < 2; ++x) {
                         if (j >= ne[x])
                             continue;
-                        if (!wait_or_fail(b_p(x), gx[x] & 1)) {
+                        if (!all_ok(wait_or_fail(b_p(x), gx[x] & 1))) {
                             go = false;
                             break;
                         }
@@ -1320,19 +1666,19 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                         const uint32_t to = tO(x), ts = tS(x);
 #pragma unroll
                         for (int k = 0; k < kN / 16; ++k)
-                            tc_mma_ts(to, ts + k * 8, dv + (uint64_t)(k * (2048 >> 4)), id_o,
+                            mma_ts(to, ts + k * 8, dv + (uint64_t)(k * (2048 >> 4)), id_o,
                                       (j > j0 || k > 0) ? 1u : 0u);
-                        tc_commit(b_pv(x));
+                        commit(b_pv(x));
                         ++gx[x];
                         // The tile's last O += P V is issued: V's stage is
                         // free once it completes (tile B, if it reads V_j,
                         // comes after tile A).
                         if (x == 1 || j >= ne[1])
-                            tc_commit(b_ve(vs));
+                            commit(b_ve(vs));
                         if (j + 1 < ne[x]) {
                             if (ks_next < 0) {
                                 ks_next = kc % kKStages;
-                                if (!wait_or_fail(b_kf(ks_next), (kc / kKStages) & 1)) {
+                                if (!all_ok(wait_or_fail(b_kf(ks_next), (kc / kKStages) & 1))) {
                                     go = false;
                                     break;
                                 }
@@ -1344,10 +1690,10 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                     if (!go)
                         break;
                     if (ks_next >= 0) {
-                        tc_commit(b_ke(ks_next));
+                        commit(b_ke(ks_next));
                         ++kc;
                         if (j + 2 == j1)
-                            tc_commit(b_qe);
+                            commit(b_qe);
                     }
                     ++vc;
                 }
@@ -1377,6 +1723,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
             zero_rows<D>(p, tid);
         float sc = p.scale_log2;  // this row's score factor (base 2)
         const bool sc_pos = sc >= 0.f;
+        [[maybe_unused]] int met = 0;  // times the two warps of a quarter have met
         int gx = 0, vbase = 0;  // tiles of this query tile, and V tiles of the CTA, so far
         bool alive = true;
         int empty = 0;  // items without tiles so far
@@ -1409,14 +1756,14 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
             constexpr int kStep = SOLO ? 2 : 1;  // and from one to the next
             const bool zeroes = !FP8 && jp >= j0 && jp < nx &&
                                 (SOLO ? ((jp - j0) & 1) == x : x == 0 || jp >= (SPLIT ? min(w.n[0], j1) : w.n[0]));
-            const bool valid = g < HPC && w.t0[SOLO ? 0 : x] + t < w.q_len;
+            const bool valid = g < HPC && w.t0[SOLO || COOP ? 0 : x] + t < w.q_len;
             // Tree: this row's mask, and whether it sees nothing at all.
             [[maybe_unused]] const int context = w.L - w.q_len, item = i;
             [[maybe_unused]] const uint32_t *mask_row = nullptr;
             [[maybe_unused]] bool blank = false;
             if constexpr (TREE) {
                 if (valid) {
-                    mask_row = p.tree_masks + (long long)(w.q0 + w.t0[SOLO ? 0 : x] + t) * p.mask_words;
+                    mask_row = p.tree_masks + (long long)(w.q0 + w.t0[SOLO || COOP ? 0 : x] + t) * p.mask_words;
                     if (context == 0) {
                         uint32_t any = 0u;
                         for (int k = 0; 32 * k < w.q_len; ++k)
@@ -1427,6 +1774,67 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
             }
             // Last token this row sees (cross: rows without a query run on, unread).
             const int pos = CROSS ? w.L - 1 : valid ? w.L - w.q_len + w.t0[x] + t : -1;
+            if constexpr (kNative) {
+                // This row's query as 8-bit terms, scaled by 2^-e so that its
+                // largest magnitude lies in [2^7, 2^8); 2^e joins the score factor.
+                // A row that is not finite is NaN (its every score is NaN or
+                // infinite, which makes the output NaN).
+                const int first = w.t0[SOLO || COOP ? 0 : x];
+                const uint4 *qrow = reinterpret_cast<const uint4 *>(
+                    static_cast<const uint16_t *>(p.query) +
+                    ((long long)(w.q0 + first + t) * p.num_q_heads + w.h * p.group + w.ht * HPC + g) * D);
+                uint4 qv[kChunks * 8];
+                uint32_t mag = 0;  // largest |q| as 16 bits, per half
+#pragma unroll
+                for (int k = 0; k < kChunks * 8; ++k)
+                    qv[k] = valid ? __ldg(qrow + k) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                for (int k = 0; k < kChunks * 8; ++k) {
+                    mag = __vmaxu2(mag, __vmaxu2(qv[k].x & 0x7FFF7FFFu, qv[k].y & 0x7FFF7FFFu));
+                    mag = __vmaxu2(mag, __vmaxu2(qv[k].z & 0x7FFF7FFFu, qv[k].w & 0x7FFF7FFFu));
+                }
+                mag = max(mag & 0xFFFFu, mag >> 16);
+                const float top = unpack2<BF16>(mag).x;
+                const int field = (int)(__float_as_uint(top) >> 23);  // biased exponent
+                const int e = field == 255 ? 0 : field == 0 ? (mag ? -120 : 0) : max(field - 134, -120);
+                const float down = __int_as_float((127 - e) << 23);  // 2^-e
+                sc = p.scale_log2 * __int_as_float((127 + e) << 23);
+                {
+                    const uint32_t row = (uint32_t)(r * D);
+                    // COOP: a half of the row each (the loop is unrolled).
+#pragma unroll
+                    for (int u = 0; u < D / 16; ++u) {
+                        if (COOP && (u & 1) != x)
+                            continue;
+                        uint32_t code[kTerms][4];
+                        const uint4 v[2] = {qv[2 * u], qv[2 * u + 1]};
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            const uint4 &half = v[c >> 2];
+                            const uint32_t pair = (c & 3) == 0 ? half.x : (c & 3) == 1 ? half.y : (c & 3) == 2 ? half.z : half.w;
+                            float2 f = unpack2<BF16>(pair);
+                            f.x = field == 255 ? NAN : f.x * down;
+                            f.y = field == 255 ? NAN : f.y * down;
+#pragma unroll
+                            for (int term = 0; term < kTerms; ++term) {
+                                const uint32_t two = term < 2 ? to_e4m3_pair(f.x, f.y) : to_e5m2_pair(f.x, f.y);
+                                code[term][c >> 1] = c & 1 ? code[term][c >> 1] | two << 16 : two;
+                                if (term + 1 < kTerms) {
+                                    const float2 held = unpack2<false>(e4m3_pair_lo(two));
+                                    f.x -= held.x;
+                                    f.y -= held.y;
+                                }
+                            }
+                        }
+#pragma unroll
+                        for (int term = 0; term < kTerms; ++term)
+                            sts128(sTerm(x, term) + row + ((u ^ (D == 128 ? r & 7 : (r >> 1) & 3)) << 4), code[term][0],
+                                   code[term][1], code[term][2], code[term][3]);
+                    }
+                    fence_proxy_async();  // the terms, for the score MMAs
+                    mbar_arrive(b_qr);
+                }
+            }
             if constexpr (kQToF16) {
                 // Move Q row r of this tile to fp16 in place, scaled by 2^-e
                 // so that the row's largest magnitude lies in [2^14, 2^15):
@@ -1466,6 +1874,267 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                 }
                 fence_proxy_async();  // the fp16 rows, for the score MMAs
                 mbar_arrive(b_qr);
+            }
+            if constexpr (COOP) {
+                // Columns 64 x .. 64 x + 63 of every K/V tile, dimensions x D / 2 .. of O.
+                constexpr int kHalf = kN / 2, kOut = D / 2;
+                const uint32_t tO1 = tmem + 384u + lane_off + x * kOut;
+                // Meet the other half's warp: bounded, as every wait, and shared
+                // memory written before is visible after it.
+                auto pair_sync = [&] {
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(smem_addr(&coop_pair[quarter]));
+                    return __all_sync(kFull, wait_or_fail(smem_addr(&coop_pair[quarter]), met++ & 1));
+                };
+                const bool active = __any_sync(kFull, valid);  // a warp without rows only keeps in step: its P may be anything
+                const float none = sc_pos ? -INFINITY : INFINITY;
+                float r_ref = none, l_run = 0.f;  // reference: a raw score (none yet: of no finite one)
+                if (valid)
+                    asm volatile("prefetch.global.L1 [%0];" ::"l"(mask_row));
+                // One K/V tile. Two instances: tiles of context alone, whose loop
+                // is short (its instructions' way from memory is what bounds a
+                // softmax thread), and those that hold nodes.
+                auto step = [&](int j, auto nodes) {
+                    constexpr bool NODES = decltype(nodes)::value;
+                    // Native at head size 128: 16 columns at a time, read twice, so
+                    // that the loop's code is a quarter as long (238 us by 64, 208
+                    // by 32, 195 by 16 at 64 x 16 nodes over 4096 tokens, 32 / 8
+                    // heads; at head size 64 it costs 10 %).
+                    constexpr bool kPieces = kNative && D == 128 && !NODES;
+                    const int b = gx & 1;
+                    if (!__all_sync(kFull, wait_or_fail(b_s(b), (gx >> 1) & 1)))
+                        return false;
+                    tc_fence_after();
+                    if (active) {
+                        [[maybe_unused]] float sv[kPieces ? 1 : kHalf];
+                        const uint32_t ta = tmem + 128u * b + lane_off + x * kHalf;
+                        if constexpr (!kPieces) {
+                            uint32_t *rv = reinterpret_cast<uint32_t *>(sv);
+                            tc_ld32_async(ta, rv);
+                            tc_ld32_async(ta + 32, rv + 32);
+                            tc_wait_ld();
+                        }
+                        [[maybe_unused]] uint32_t vis[kN / 32];
+                        if constexpr (NODES) {
+                            // Masked scores: neutral for the extremum, weight 0.
+                            tree_bits(mask_row, w.q_len, j * kN + x * kHalf - context, vis);
+#pragma unroll
+                            for (int c = 0; c < kHalf; ++c)
+                                sv[c] = vis[c >> 5] >> (c & 31) & 1u ? sv[c] : none;
+                        }
+                        float e8[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            e8[k] = none;
+                        auto extrema = [&](const float *v, auto count) {
+                            constexpr int n = decltype(count)::value;
+                            if (sc_pos) {
+#pragma unroll
+                                for (int c = 0; c < n; c += 2)
+                                    e8[(c >> 1) & 7] = max3(e8[(c >> 1) & 7], v[c], v[c + 1]);
+                            } else {
+#pragma unroll
+                                for (int c = 0; c < n; c += 2)
+                                    e8[(c >> 1) & 7] = min3(e8[(c >> 1) & 7], v[c], v[c + 1]);
+                            }
+                        };
+                        if constexpr (kPieces) {
+#pragma unroll 1
+                            for (int q = 0; q < kHalf / 16; ++q) {
+                                float v[16];
+                                tc_ld16(ta + 16 * q, v);
+                                extrema(v, std::integral_constant<int, 16>{});
+                            }
+                        } else {
+                            extrema(sv, std::integral_constant<int, kHalf>{});
+                        }
+                        float e = sc_pos ? max3(max3(e8[0], e8[1], e8[2]), max3(e8[3], e8[4], e8[5]), fmaxf(e8[6], e8[7]))
+                                         : min3(min3(e8[0], e8[1], e8[2]), min3(e8[3], e8[4], e8[5]), fminf(e8[6], e8[7]));
+                        // The reference moves when a score of either half exceeds it
+                        // by more than kRescaleLog2, which is rare: the two warps tell
+                        // each other whether, and only then the extrema. (An infinite
+                        // extremum is no reference: the row's sum is NaN then.)
+                        auto exceeds = [&](float raw) {
+                            return fabsf(raw) != INFINITY && (r_ref == none || __fmul_rn(raw - r_ref, sc) > kRescaleLog2);
+                        };
+                        const bool mine = __any_sync(kFull, exceeds(e));
+                        if (lane == 0)
+                            *const_cast<volatile uint8_t *>(&coop_grow[8 * b + warp]) = mine;
+                        if (!pair_sync())
+                            return false;
+                        if (mine || *const_cast<volatile uint8_t *>(&coop_grow[8 * b + (warp ^ 4)])) {
+                            coop_row[x * kM + r] = e;
+                            if (!pair_sync())
+                                return false;
+                            const float other = coop_row[(x ^ 1) * kM + r];
+                            e = sc_pos ? fmaxf(e, other) : fminf(e, other);
+                            float alpha = 1.f;
+                            if (exceeds(e)) {
+                                alpha = r_ref == none ? 0.f : ex2(__fmul_rn(r_ref - e, sc));
+                                r_ref = e;
+                            }
+                            l_run *= alpha;
+                            if (j > j0) {
+                                // O, once the last tile's O += P V is done (it was issued
+                                // before this tile's scores).
+#pragma unroll 1
+                                for (int c = 0; c < kOut / 16; ++c) {
+                                    float o[16];
+                                    tc_ld16(tO1 + c * 16, o);
+#pragma unroll
+                                    for (int k = 0; k < 16; ++k)
+                                        o[k] *= alpha;
+                                    tc_st16(tO1 + c * 16, o);
+                                }
+                            }
+                            if (!pair_sync())  // read, before anything else goes there
+                                return false;
+                        }
+                        // P = 2^((s - reference) scale), rounded to the element type, in
+                        // pairs; the row sum adds the rounded values. The difference comes
+                        // first, so that the largest score's argument is small however
+                        // large the scores.
+                        const float ref = r_ref == none ? 0.f : r_ref;
+                        const uint64_t sc2 = pk2(sc, sc), nref2 = pk2(-ref, -ref);
+                        float l8[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            l8[k] = 0.f;
+                        auto fill = [&](const float *v, uint32_t *pw, auto count) {
+#pragma unroll
+                            for (int c = 0; c < decltype(count)::value / 2; ++c) {
+                                float x0, x1;
+                                unpk2(mul2(add2(pk2(v[2 * c], v[2 * c + 1]), nref2), sc2), x0, x1);
+                                pw[c] = pack2<kMmaBF16>(ex2(x0), ex2(x1));
+                                l8[c & 7] = add_pair<kMmaBF16>(l8[c & 7], pw[c]);
+                            }
+                        };
+                        // P's place was read by the tile before last, whose O += P V
+                        // came before this tile's scores.
+                        const uint32_t tp = tmem + 256u + 64u * b + lane_off + x * (kHalf / 2);
+                        if constexpr (kPieces) {
+#pragma unroll 1
+                            for (int q = 0; q < kHalf / 16; ++q) {
+                                float v[16];
+                                uint32_t pw[8];
+                                tc_ld16(ta + 16 * q, v);
+                                fill(v, pw, std::integral_constant<int, 16>{});
+                                tc_st8u(tp + 8 * q, pw);
+                            }
+                        } else {
+                        uint32_t pw[kHalf / 2];
+                        fill(sv, pw, std::integral_constant<int, kHalf>{});
+                        if constexpr (NODES) {
+                            if (sc == 0.f) {  // a masked score gave 0 x inf = NaN
+#pragma unroll
+                                for (int k = 0; k < 8; ++k)
+                                    l8[k] = 0.f;
+#pragma unroll
+                                for (int c = 0; c < kHalf / 2; ++c) {
+                                    pw[c] &= (vis[c >> 4] >> (2 * c & 31) & 1u ? 0xFFFFu : 0u) |
+                                             (vis[c >> 4] >> (2 * c + 1 & 31) & 1u ? 0xFFFF0000u : 0u);
+                                    l8[c & 7] = add_pair<kMmaBF16>(l8[c & 7], pw[c]);
+                                }
+                            }
+                        }
+                        tc_st32u(tp, pw);
+                        }
+                        l_run += ((l8[0] + l8[1]) + (l8[2] + l8[3])) + ((l8[4] + l8[5]) + (l8[6] + l8[7]));
+                    }
+                    if constexpr (NODES && !FP8) {
+                        // V rows past the sequence end become zeros, elements of the
+                        // tree's tokens that are not finite too (FP8: by the widening warps).
+                        const int vt = vbase + (j - j0), vs = vt % kVStages;
+                        if (!__all_sync(kFull, wait_or_fail(b_vf(vs), (vt / kVStages) & 1)))
+                            return false;
+                        const int tok = j * kN + r;
+                        if (tok >= context) {
+#pragma unroll 4
+                            for (int k = x * kChunks * 4; k < (x + 1) * kChunks * 4; ++k) {
+                                const uint32_t at = sV(vs) + (k >> 3) * kChunkBytes + r * 128 + (((k & 7) ^ (r & 7)) << 4);
+                                uint4 v = tok < w.L ? lds128(at) : make_uint4(0u, 0u, 0u, 0u);
+                                const bool bad = tok < w.L && drop_nonfinite<BF16>(v);
+                                if (bad)
+                                    *const_cast<volatile int *>(&poison[item % kPoisonSlots]) = item + 1;
+                                if (bad || tok >= w.L)
+                                    sts128(at, v.x, v.y, v.z, v.w);
+                            }
+                        }
+                        fence_proxy_async();
+                    }
+                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                    tc_fence_before();
+                    mbar_arrive(b_p(b));
+                    ++gx;
+                    return true;
+                };
+                int j = j0;
+                const int plain = min(j1, context / kN);  // tiles before the first that holds a node
+#pragma unroll 1
+                for (; alive && j < plain; ++j)
+                    alive = step(j, std::false_type{});
+#pragma unroll 1
+                for (; alive && j < j1; ++j)
+                    alive = step(j, std::true_type{});
+                if (!alive)
+                    break;
+                vbase += j1 - j0;
+                if (!__all_sync(kFull, wait_or_fail(b_pv(0), (gx - 1) & 1))) {
+                    alive = false;
+                    break;
+                }
+                tc_fence_after();
+                if (!active)
+                    continue;
+                // The row's sum: both halves', in their order.
+                coop_row[x * kM + r] = l_run;
+                if (!pair_sync()) {
+                    alive = false;
+                    break;
+                }
+                l_run = coop_row[r] + coop_row[kM + r];
+                if (!pair_sync()) {  // read, before anything else goes there
+                    alive = false;
+                    break;
+                }
+                if (blank)
+                    l_run = 1.f;  // O is 0: a row that sees nothing is zeros
+                const bool poisoned = valid && *const_cast<volatile int *>(&poison[item % kPoisonSlots]) == item + 1;
+                const bool whole = !SPLIT || it.clo == it.chi;
+                const int slot = SPLIT ? (((int)blockIdx.x * 2 + ((int)blockIdx.x == it.clo ? 1 : 0)) * 2) * kM + r : 0;
+                const float inv = p.v_scale / l_run;
+                uint16_t *out = static_cast<uint16_t *>(p.out) +
+                                ((long long)(w.q0 + w.t0[0] + t) * p.num_q_heads + w.h * p.group + w.ht * HPC + g) * D + x * kOut;
+#pragma unroll 1
+                for (int c = 0; c < kOut / 32; ++c) {
+                    float o[32];
+                    tc_ld32(tO1 + c * 32, o);
+                    if (poisoned)
+                        add_nonfinite<BF16, FP8, D>(p, w, mask_row, j0 * kN, j1 * kN, x * (kOut / 32) + c, o);
+                    if (!valid)
+                        continue;
+                    if (whole) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            uint4 e;
+                            e.x = pack2<BF16>(o[8 * q + 0] * inv, o[8 * q + 1] * inv);
+                            e.y = pack2<BF16>(o[8 * q + 2] * inv, o[8 * q + 3] * inv);
+                            e.z = pack2<BF16>(o[8 * q + 4] * inv, o[8 * q + 5] * inv);
+                            e.w = pack2<BF16>(o[8 * q + 6] * inv, o[8 * q + 7] * inv);
+                            reinterpret_cast<uint4 *>(out + c * 32)[q] = e;
+                        }
+                    } else {
+                        float4 *po = reinterpret_cast<float4 *>(p.part_o + (size_t)slot * D + x * kOut);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            po[c * 8 + q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+                    }
+                }
+                if (!whole && valid && x == 0)
+                    p.part_ml[slot] = make_float2(r_ref == none ? -INFINITY : __fmul_rn(r_ref, sc), l_run);
+                tc_fence_before();
+                continue;
             }
             float m_run = -INFINITY, l_run = 0.f;
             for (int j = jx; j < nx; j += kStep, ++gx) {
@@ -1644,7 +2313,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                         if (kb + r >= context && kb + r < w.L) {
 #pragma unroll 4
                             for (int k = 0; k < kChunks * 8; ++k) {
-                                const uint32_t at = sV(vs) + (k >> 3) * kChunkBytes + r * 128 + (k & 7) * 16;
+                                const uint32_t at = sV(vs) + (k >> 3) * kChunkBytes + r * 128 + (((k & 7) ^ (r & 7)) << 4);
                                 uint4 v = lds128(at);
                                 if (drop_nonfinite<BF16>(v)) {
                                     sts128(at, v.x, v.y, v.z, v.w);
@@ -1675,7 +2344,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                 tc_fence_after();
             }
             uint16_t *out = static_cast<uint16_t *>(p.out) +
-                            ((long long)(w.q0 + w.t0[SOLO ? 0 : x] + t) * p.num_q_heads + w.h * p.group + w.ht * HPC + g) * D;
+                            ((long long)(w.q0 + w.t0[SOLO || COOP ? 0 : x] + t) * p.num_q_heads + w.h * p.group + w.ht * HPC + g) * D;
             const uint32_t to = tO(x) + lane_off;
             float o[32];
             // Solo: B leaves its rows' states for A and waits until A has
