@@ -1875,10 +1875,16 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                 fence_proxy_async();  // the fp16 rows, for the score MMAs
                 mbar_arrive(b_qr);
             }
-            if constexpr (COOP) {
-                // Columns 64 x .. 64 x + 63 of every K/V tile, dimensions x D / 2 .. of O.
-                constexpr int kHalf = kN / 2, kOut = D / 2;
-                const uint32_t tO1 = tmem + 384u + lane_off + x * kOut;
+            if constexpr (TREE) {
+                // COOP: columns 64 x .. 64 x + 63 of every K/V tile, dimensions
+                // x D / 2 .. of O. Else all of query tile x's, as the other kinds.
+                constexpr int kCols = COOP ? kN / 2 : kN, kOut = COOP ? D / 2 : D;
+                const int col0 = COOP ? x * kCols : 0;
+                const uint32_t tO1 = COOP ? tmem + 384u + lane_off + x * kOut : tO(x) + lane_off;
+                if (!COOP && w.n[x] == 0) {  // the tile has no queries
+                    vbase += j1 - j0;
+                    continue;
+                }
                 // Meet the other half's warp: bounded, as every wait, and shared
                 // memory written before is visible after it.
                 auto pair_sync = [&] {
@@ -1902,25 +1908,26 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                     // by 32, 195 by 16 at 64 x 16 nodes over 4096 tokens, 32 / 8
                     // heads; at head size 64 it costs 10 %).
                     constexpr bool kPieces = kNative && D == 128 && !NODES;
-                    const int b = gx & 1;
-                    if (!__all_sync(kFull, wait_or_fail(b_s(b), (gx >> 1) & 1)))
+                    const int b = COOP ? gx & 1 : x;  // the scores' place
+                    if (!__all_sync(kFull, wait_or_fail(b_s(b), COOP ? (gx >> 1) & 1 : gx & 1)))
                         return false;
                     tc_fence_after();
                     if (active) {
-                        [[maybe_unused]] float sv[kPieces ? 1 : kHalf];
-                        const uint32_t ta = tmem + 128u * b + lane_off + x * kHalf;
+                        [[maybe_unused]] float sv[kPieces ? 1 : kCols];
+                        const uint32_t ta = tmem + 128u * b + lane_off + col0;
                         if constexpr (!kPieces) {
                             uint32_t *rv = reinterpret_cast<uint32_t *>(sv);
-                            tc_ld32_async(ta, rv);
-                            tc_ld32_async(ta + 32, rv + 32);
+#pragma unroll
+                            for (int c = 0; c < kCols; c += 32)
+                                tc_ld32_async(ta + c, rv + c);
                             tc_wait_ld();
                         }
                         [[maybe_unused]] uint32_t vis[kN / 32];
                         if constexpr (NODES) {
                             // Masked scores: neutral for the extremum, weight 0.
-                            tree_bits(mask_row, w.q_len, j * kN + x * kHalf - context, vis);
+                            tree_bits(mask_row, w.q_len, j * kN + col0 - context, vis);
 #pragma unroll
-                            for (int c = 0; c < kHalf; ++c)
+                            for (int c = 0; c < kCols; ++c)
                                 sv[c] = vis[c >> 5] >> (c & 31) & 1u ? sv[c] : none;
                         }
                         float e8[8];
@@ -1941,34 +1948,39 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                         };
                         if constexpr (kPieces) {
 #pragma unroll 1
-                            for (int q = 0; q < kHalf / 16; ++q) {
+                            for (int q = 0; q < kCols / 16; ++q) {
                                 float v[16];
                                 tc_ld16(ta + 16 * q, v);
                                 extrema(v, std::integral_constant<int, 16>{});
                             }
                         } else {
-                            extrema(sv, std::integral_constant<int, kHalf>{});
+                            extrema(sv, std::integral_constant<int, kCols>{});
                         }
                         float e = sc_pos ? max3(max3(e8[0], e8[1], e8[2]), max3(e8[3], e8[4], e8[5]), fmaxf(e8[6], e8[7]))
                                          : min3(min3(e8[0], e8[1], e8[2]), min3(e8[3], e8[4], e8[5]), fminf(e8[6], e8[7]));
-                        // The reference moves when a score of either half exceeds it
-                        // by more than kRescaleLog2, which is rare: the two warps tell
-                        // each other whether, and only then the extrema. (An infinite
-                        // extremum is no reference: the row's sum is NaN then.)
+                        // The reference moves when a score exceeds it by more than
+                        // kRescaleLog2, which is rare. COOP: of either half; the two
+                        // warps tell each other whether, and only then the extrema. (An
+                        // infinite extremum is no reference: the row's sum is NaN then.)
                         auto exceeds = [&](float raw) {
                             return fabsf(raw) != INFINITY && (r_ref == none || __fmul_rn(raw - r_ref, sc) > kRescaleLog2);
                         };
-                        const bool mine = __any_sync(kFull, exceeds(e));
-                        if (lane == 0)
-                            *const_cast<volatile uint8_t *>(&coop_grow[8 * b + warp]) = mine;
-                        if (!pair_sync())
-                            return false;
-                        if (mine || *const_cast<volatile uint8_t *>(&coop_grow[8 * b + (warp ^ 4)])) {
-                            coop_row[x * kM + r] = e;
+                        bool moves = __any_sync(kFull, exceeds(e));
+                        if constexpr (COOP) {
+                            if (lane == 0)
+                                *const_cast<volatile uint8_t *>(&coop_grow[8 * b + warp]) = moves;
                             if (!pair_sync())
                                 return false;
-                            const float other = coop_row[(x ^ 1) * kM + r];
-                            e = sc_pos ? fmaxf(e, other) : fminf(e, other);
+                            moves |= *const_cast<volatile uint8_t *>(&coop_grow[8 * b + (warp ^ 4)]) != 0;
+                        }
+                        if (moves) {
+                            if constexpr (COOP) {
+                                coop_row[x * kM + r] = e;
+                                if (!pair_sync())
+                                    return false;
+                                const float other = coop_row[(x ^ 1) * kM + r];
+                                e = sc_pos ? fmaxf(e, other) : fminf(e, other);
+                            }
                             float alpha = 1.f;
                             if (exceeds(e)) {
                                 alpha = r_ref == none ? 0.f : ex2(__fmul_rn(r_ref - e, sc));
@@ -1976,8 +1988,11 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                             }
                             l_run *= alpha;
                             if (j > j0) {
-                                // O, once the last tile's O += P V is done (it was issued
-                                // before this tile's scores).
+                                // O: the last tile's O += P V was issued before this
+                                // tile's scores (COOP: waited for).
+                                if (COOP && !__all_sync(kFull, wait_or_fail(b_pv(0), (gx - 1) & 1)))
+                                    return false;
+                                tc_fence_after();
 #pragma unroll 1
                                 for (int c = 0; c < kOut / 16; ++c) {
                                     float o[16];
@@ -1988,7 +2003,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                                     tc_st16(tO1 + c * 16, o);
                                 }
                             }
-                            if (!pair_sync())  // read, before anything else goes there
+                            if (COOP && !pair_sync())  // read, before anything else goes there
                                 return false;
                         }
                         // P = 2^((s - reference) scale), rounded to the element type, in
@@ -2010,12 +2025,12 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                                 l8[c & 7] = add_pair<kMmaBF16>(l8[c & 7], pw[c]);
                             }
                         };
-                        // P's place was read by the tile before last, whose O += P V
-                        // came before this tile's scores.
-                        const uint32_t tp = tmem + 256u + 64u * b + lane_off + x * (kHalf / 2);
+                        // COOP: P's place was read by the tile before last, whose O += P V
+                        // came before this tile's scores. Else P goes over the scores.
+                        const uint32_t tp = COOP ? tmem + 256u + 64u * b + lane_off + x * (kCols / 2) : ta;
                         if constexpr (kPieces) {
 #pragma unroll 1
-                            for (int q = 0; q < kHalf / 16; ++q) {
+                            for (int q = 0; q < kCols / 16; ++q) {
                                 float v[16];
                                 uint32_t pw[8];
                                 tc_ld16(ta + 16 * q, v);
@@ -2023,26 +2038,28 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                                 tc_st8u(tp + 8 * q, pw);
                             }
                         } else {
-                        uint32_t pw[kHalf / 2];
-                        fill(sv, pw, std::integral_constant<int, kHalf>{});
+                            uint32_t pw[kCols / 2];
+                            fill(sv, pw, std::integral_constant<int, kCols>{});
                         if constexpr (NODES) {
                             if (sc == 0.f) {  // a masked score gave 0 x inf = NaN
 #pragma unroll
                                 for (int k = 0; k < 8; ++k)
                                     l8[k] = 0.f;
 #pragma unroll
-                                for (int c = 0; c < kHalf / 2; ++c) {
+                                for (int c = 0; c < kCols / 2; ++c) {
                                     pw[c] &= (vis[c >> 4] >> (2 * c & 31) & 1u ? 0xFFFFu : 0u) |
                                              (vis[c >> 4] >> (2 * c + 1 & 31) & 1u ? 0xFFFF0000u : 0u);
                                     l8[c & 7] = add_pair<kMmaBF16>(l8[c & 7], pw[c]);
                                 }
                             }
                         }
-                        tc_st32u(tp, pw);
+#pragma unroll
+                            for (int c = 0; c < kCols / 2; c += 32)
+                                tc_st32u(tp + c, pw + c);
                         }
                         l_run += ((l8[0] + l8[1]) + (l8[2] + l8[3])) + ((l8[4] + l8[5]) + (l8[6] + l8[7]));
                     }
-                    if constexpr (NODES && !FP8) {
+                    if (NODES && !FP8 && (COOP || x == 0)) {
                         // V rows past the sequence end become zeros, elements of the
                         // tree's tokens that are not finite too (FP8: by the widening warps).
                         const int vt = vbase + (j - j0), vs = vt % kVStages;
@@ -2051,7 +2068,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                         const int tok = j * kN + r;
                         if (tok >= context) {
 #pragma unroll 4
-                            for (int k = x * kChunks * 4; k < (x + 1) * kChunks * 4; ++k) {
+                            for (int k = COOP ? x * kChunks * 4 : 0; k < (COOP ? x + 1 : 2) * kChunks * 4; ++k) {
                                 const uint32_t at = sV(vs) + (k >> 3) * kChunkBytes + r * 128 + (((k & 7) ^ (r & 7)) << 4);
                                 uint4 v = tok < w.L ? lds128(at) : make_uint4(0u, 0u, 0u, 0u);
                                 const bool bad = tok < w.L && drop_nonfinite<BF16>(v);
@@ -2080,38 +2097,40 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                 if (!alive)
                     break;
                 vbase += j1 - j0;
-                if (!__all_sync(kFull, wait_or_fail(b_pv(0), (gx - 1) & 1))) {
+                if (!__all_sync(kFull, wait_or_fail(b_pv(COOP ? 0 : x), (gx - 1) & 1))) {
                     alive = false;
                     break;
                 }
                 tc_fence_after();
                 if (!active)
                     continue;
-                // The row's sum: both halves', in their order.
-                coop_row[x * kM + r] = l_run;
-                if (!pair_sync()) {
-                    alive = false;
-                    break;
-                }
-                l_run = coop_row[r] + coop_row[kM + r];
-                if (!pair_sync()) {  // read, before anything else goes there
-                    alive = false;
-                    break;
+                if constexpr (COOP) {
+                    // The row's sum: both halves', in their order.
+                    coop_row[x * kM + r] = l_run;
+                    if (!pair_sync()) {
+                        alive = false;
+                        break;
+                    }
+                    l_run = coop_row[r] + coop_row[kM + r];
+                    if (!pair_sync()) {  // read, before anything else goes there
+                        alive = false;
+                        break;
+                    }
                 }
                 if (blank)
                     l_run = 1.f;  // O is 0: a row that sees nothing is zeros
                 const bool poisoned = valid && *const_cast<volatile int *>(&poison[item % kPoisonSlots]) == item + 1;
                 const bool whole = !SPLIT || it.clo == it.chi;
-                const int slot = SPLIT ? (((int)blockIdx.x * 2 + ((int)blockIdx.x == it.clo ? 1 : 0)) * 2) * kM + r : 0;
+                const int slot = SPLIT ? (((int)blockIdx.x * 2 + ((int)blockIdx.x == it.clo ? 1 : 0)) * 2 + (COOP ? 0 : x)) * kM + r : 0;
                 const float inv = p.v_scale / l_run;
                 uint16_t *out = static_cast<uint16_t *>(p.out) +
-                                ((long long)(w.q0 + w.t0[0] + t) * p.num_q_heads + w.h * p.group + w.ht * HPC + g) * D + x * kOut;
+                                ((long long)(w.q0 + w.t0[COOP ? 0 : x] + t) * p.num_q_heads + w.h * p.group + w.ht * HPC + g) * D + (COOP ? x * kOut : 0);
 #pragma unroll 1
                 for (int c = 0; c < kOut / 32; ++c) {
                     float o[32];
                     tc_ld32(tO1 + c * 32, o);
                     if (poisoned)
-                        add_nonfinite<BF16, FP8, D>(p, w, mask_row, j0 * kN, j1 * kN, x * (kOut / 32) + c, o);
+                        add_nonfinite<BF16, FP8, D>(p, w, mask_row, j0 * kN, j1 * kN, (COOP ? x * (kOut / 32) : 0) + c, o);
                     if (!valid)
                         continue;
                     if (whole) {
@@ -2125,13 +2144,13 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                             reinterpret_cast<uint4 *>(out + c * 32)[q] = e;
                         }
                     } else {
-                        float4 *po = reinterpret_cast<float4 *>(p.part_o + (size_t)slot * D + x * kOut);
+                        float4 *po = reinterpret_cast<float4 *>(p.part_o + (size_t)slot * D + (COOP ? x * kOut : 0));
 #pragma unroll
                         for (int q = 0; q < 8; ++q)
                             po[c * 8 + q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
                     }
                 }
-                if (!whole && valid && x == 0)
+                if (!whole && valid && (!COOP || x == 0))
                     p.part_ml[slot] = make_float2(r_ref == none ? -INFINITY : __fmul_rn(r_ref, sc), l_run);
                 tc_fence_before();
                 continue;
@@ -2159,19 +2178,11 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                 // the tile then runs the same branch-free code as a full one.
                 // Padding slots past the sequence end (whatever they hold,
                 // NaN included) are masked the same way.
-                [[maybe_unused]] uint32_t vis[kN / 32];
-                if (TREE ? kb + kN > context : kb + kN - 1 > pos) {
+                if (kb + kN - 1 > pos) {
                     const float masked = sc_pos ? -INFINITY : INFINITY;
-                    if constexpr (TREE) {
-                        tree_bits(mask_row, w.q_len, kb - context, vis);
 #pragma unroll
-                        for (int c = 0; c < kN; ++c)
-                            sv[c] = vis[c >> 5] >> (c & 31) & 1u ? sv[c] : masked;
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < kN; ++c)
-                            sv[c] = kb + c <= pos ? sv[c] : masked;
-                    }
+                    for (int c = 0; c < kN; ++c)
+                        sv[c] = kb + c <= pos ? sv[c] : masked;
                 }
                 // Row maximum in base 2: scale x the largest visible raw score
                 // (the smallest for a negative scale; rounding is monotone, so
@@ -2258,7 +2269,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                     fill(std::true_type{});
                 else
                     fill(std::false_type{});
-                if (sc == 0.f && (TREE ? kb + kN > context : kb + kN - 1 > pos)) {
+                if (sc == 0.f && kb + kN - 1 > pos) {
                     // Scale 0: a masked score gave 0 x inf = NaN; its weight
                     // is 0. The visible ones keep theirs, 2^-ref, or NaN
                     // where the score itself is infinite or NaN.
@@ -2267,11 +2278,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                         l8[i] = 0.f;
 #pragma unroll
                     for (int c = 0; c < kN / 2; ++c) {
-                        if constexpr (TREE)
-                            pw[c] &= (vis[c >> 4] >> (2 * c & 31) & 1u ? 0xFFFFu : 0u) |
-                                     (vis[c >> 4] >> (2 * c + 1 & 31) & 1u ? 0xFFFF0000u : 0u);
-                        else
-                            pw[c] &= (kb + 2 * c <= pos ? 0xFFFFu : 0u) | (kb + 2 * c + 1 <= pos ? 0xFFFF0000u : 0u);
+                        pw[c] &= (kb + 2 * c <= pos ? 0xFFFFu : 0u) | (kb + 2 * c + 1 <= pos ? 0xFFFF0000u : 0u);
                         l8[c & 7] = add_pair<kMmaBF16>(l8[c & 7], pw[c]);
                     }
                 }
@@ -2298,8 +2305,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                 m_run = m_new;
                 // The V rows past the sequence end hold whatever the pool's
                 // padding slots hold: zero them (P is 0 there) once V lands.
-                // Tree: so are the elements of the tree's tokens that are not finite.
-                if (TREE ? !FP8 && (SOLO || x == 0) && kb + kN > context : zeroes && j == jp) {
+                if (zeroes && j == jp) {
                     const int vt = vbase + (j - j0), vs = vt % kVStages;
                     if (!__all_sync(kFull, wait_or_fail(b_vf(vs), (vt / kVStages) & 1))) {
                         alive = false;
@@ -2309,19 +2315,6 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                         for (int c = 0; c < kChunks; ++c)
                             for (int i = 0; i < 8; ++i)
                                 sts128(sV(vs) + c * kChunkBytes + r * 128 + i * 16, 0u, 0u, 0u, 0u);
-                    if constexpr (TREE) {
-                        if (kb + r >= context && kb + r < w.L) {
-#pragma unroll 4
-                            for (int k = 0; k < kChunks * 8; ++k) {
-                                const uint32_t at = sV(vs) + (k >> 3) * kChunkBytes + r * 128 + (((k & 7) ^ (r & 7)) << 4);
-                                uint4 v = lds128(at);
-                                if (drop_nonfinite<BF16>(v)) {
-                                    sts128(at, v.x, v.y, v.z, v.w);
-                                    *const_cast<volatile int *>(&poison[item % kPoisonSlots]) = item + 1;
-                                }
-                            }
-                        }
-                    }
                     fence_proxy_async();
                 }
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -2344,7 +2337,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                 tc_fence_after();
             }
             uint16_t *out = static_cast<uint16_t *>(p.out) +
-                            ((long long)(w.q0 + w.t0[SOLO || COOP ? 0 : x] + t) * p.num_q_heads + w.h * p.group + w.ht * HPC + g) * D;
+                            ((long long)(w.q0 + w.t0[SOLO ? 0 : x] + t) * p.num_q_heads + w.h * p.group + w.ht * HPC + g) * D;
             const uint32_t to = tO(x) + lane_off;
             float o[32];
             // Solo: B leaves its rows' states for A and waits until A has
@@ -2372,12 +2365,6 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                 l_run = l_run * fa + b.y * fb;
                 m_run = m;
             }
-            [[maybe_unused]] bool poisoned = false;
-            if constexpr (TREE) {
-                if (blank)
-                    l_run = 1.f;  // O is 0: a row that sees nothing is zeros
-                poisoned = valid && *const_cast<volatile int *>(&poison[i % kPoisonSlots]) == i + 1;
-            }
             auto solo_read = [&] {  // A has read B's O
                 if constexpr (SOLO) {
                     tc_fence_before();
@@ -2393,10 +2380,6 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
                         o[i] = o[i] * fa + ob[i] * fb;  // a weight of 0 too: 0 * NaN is NaN
-                }
-                if constexpr (TREE) {
-                    if (poisoned)
-                        add_nonfinite<BF16, FP8, D>(p, w, mask_row, j0 * kN, j1 * kN, c, o);
                 }
             };
             auto store_row = [&](int c, const float *v, float inv) {
