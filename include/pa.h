@@ -727,8 +727,9 @@ int pa_verify_draft(int32_t *num_accepted, int32_t *path, int32_t *tokens_out,
  * PA_DEVERR_TREE; nothing of either moves, its length and blocks stay. A block
  * id outside the pool sets PA_DEVERR_BLOCK_ID, and its token is not moved; so do
  * a free count outside [0, num_blocks] and blocks returned beyond num_blocks,
- * which are dropped. Two launches, the second programmatic. Returns PA_OK or a
- * PA_ERR_* code.
+ * which are dropped. Two launches, the second programmatic. It writes lengths: a
+ * pa_decode enqueued right behind it must not claim PA_DECODE_LENS_READY. Returns
+ * PA_OK or a PA_ERR_* code.
  */
 int pa_commit_draft(void *const *kv_caches, int num_layers, const int32_t *block_tables,
                     int max_blocks_per_seq, const int32_t *cu_seqlens_q,

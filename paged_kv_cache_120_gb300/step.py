@@ -14,6 +14,11 @@ A pool of E4M3 codes (uint8) selects the FP8 cache calls instead
 (pa_reshape_and_cache_fp8, pa_decode_fp8) with the workload's per-tensor
 scales.
 
+``SpeculativeStep`` is a step that checks drafted trees of tokens:
+
+    pa_build_step -> pa_build_tree -> per layer pa_rope_and_cache,
+    pa_tree_attention -> pa_verify_draft -> pa_commit_draft
+
 Everything here is marshalling around libpa calls; no arithmetic of the
 method runs in Python.
 """
@@ -294,6 +299,93 @@ class ModelStep:
             self.graph.replay()
         else:
             self.run_eager(stream)
+
+
+class SpeculativeStep:
+    """One step of speculative decoding over a model's layer pools, on the GPU
+    from end to end: blocks and slots for every sequence's drafted tree, its
+    positions and masks, then layer after layer the rotary write of its keys and
+    values and the attention of its nodes, the verification against the target's
+    rows, and the accepted nodes' keys and values moved into place in all layers,
+    lengths cut and surplus blocks returned. The caller fills ``qkv`` (one layer's
+    projections for all nodes; a model writes them layer by layer), ``tokens``,
+    ``parents``, ``query_lens`` (nodes per sequence), ``target`` and, if it draws,
+    ``draft`` and ``uniforms``; ``count``, ``path`` and ``new_tokens`` hold the
+    outcome and ``seq_lens`` the new lengths. ``capture()`` records the step in a
+    CUDA graph that later steps replay.
+
+    tables [S, width], seq_lens [S] and free_list (a stack, the free blocks in
+    front, their number num_free) are int32 tensors of the running batch;
+    max_nodes bounds a sequence's tree."""
+
+    def __init__(self, pools, tables, seq_lens, free_list, num_free, num_q_heads, max_nodes, vocab, rope_plan, k_scale=1.0,
+                 v_scale=1.0, dtype=workloads.BF16, mode="draft", target_dtype=None):
+        import torch
+        if mode not in ("greedy", "sample", "draft"):
+            raise ValueError(f"mode must be 'greedy', 'sample' or 'draft', not {mode!r}")
+        self.pools, self.tables, self.seq_lens, self.free_list, self.num_free = pools, tables, seq_lens, free_list, num_free
+        self.plan, self.max_nodes, self.k_scale, self.v_scale = rope_plan, max_nodes, k_scale, v_scale
+        _, _, self.block_size, hkv, d = pools[0].shape
+        self.fp8 = pools[0].dtype in (torch.uint8, torch.float8_e4m3fn)
+        self.scale = d ** -0.5
+        s, dev = tables.shape[0], tables.device
+        total = s * max_nodes
+        td = workloads.torch_dtype(dtype)
+        i32 = lambda *n: torch.zeros(*n, dtype=torch.int32, device=dev)  # noqa: E731
+        self.query_lens, self.cu, self.slots, self.admitted = i32(s), i32(s + 1), i32(total), i32(1)
+        self.tokens, self.parents, self.positions = i32(total), i32(total), i32(total)
+        self.masks = i32(total, -(-max_nodes // 32))
+        self.count, self.path, self.new_tokens = i32(s), i32(total), i32(total)
+        self.qkv = torch.zeros(total, num_q_heads + 2 * hkv, d, dtype=td, device=dev)
+        self.q, self.k, self.v = self.qkv.split([num_q_heads, hkv, hkv], 1)
+        self.rotated = torch.zeros(total, num_q_heads, d, dtype=td, device=dev)
+        self.outs = [torch.zeros_like(self.rotated) for _ in pools]
+        rows = lambda: torch.zeros(total, vocab, dtype=target_dtype or torch.float32, device=dev)  # noqa: E731
+        self.target, self.draft = rows(), rows() if mode == "draft" else None
+        self.uniforms = None if mode == "greedy" else torch.zeros(total, 2, device=dev)
+        self.workspace = binding.tree_attention_workspace(self.rotated, pools[0], s, max_nodes)
+        self.graph = None
+
+    def run_eager(self) -> None:
+        b = binding
+        b.pa_build_step(self.tables, self.seq_lens, self.query_lens, self.free_list, self.num_free, self.seq_lens, self.num_free,
+                        self.cu, None, self.slots, self.admitted, self.block_size)
+        b.pa_build_tree(self.parents, self.cu, self.seq_lens, self.positions, self.masks)
+        for pool, out in zip(self.pools, self.outs):
+            write = (self.rotated, self.q, self.k, self.v, pool, self.slots, self.positions, self.plan)
+            read = (out, self.rotated, pool, self.tables, self.cu, self.seq_lens, self.masks, self.scale, self.max_nodes)
+            if self.fp8:
+                b.pa_rope_and_cache_fp8(*write, self.k_scale, self.v_scale)
+                b.pa_tree_attention_fp8(*read, self.k_scale, self.v_scale, self.workspace)
+            else:
+                b.pa_rope_and_cache(*write)
+                b.pa_tree_attention(*read, self.workspace)
+        b.pa_verify_draft(self.count, self.path, self.new_tokens, self.tokens, self.parents, self.cu, self.target, self.draft,
+                          self.uniforms)
+        b.pa_commit_draft(self.pools, self.tables, self.cu, self.seq_lens, self.count, self.path, self.seq_lens, self.free_list,
+                          self.num_free, self.num_free)
+
+    def capture(self) -> None:
+        """Record the step. Its calls are made once before, with no nodes, so that kernel attributes and tensor maps exist."""
+        import torch
+        nodes = self.query_lens.clone()
+        self.query_lens.zero_()
+        self.run_eager()
+        self.query_lens.copy_(nodes)
+        torch.cuda.synchronize()
+        graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        stream.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(stream):
+            with torch.cuda.graph(graph, stream=stream, capture_error_mode="relaxed"):
+                self.run_eager()
+        torch.cuda.current_stream().wait_stream(stream)
+        self.graph = graph
+
+    def run(self) -> None:
+        if self.graph is not None:
+            self.graph.replay()
+        else:
+            self.run_eager()
 
 
 def make_device_inputs(name: str, plan: StepPlan, seed: int, device, kv_cache: str = "16bit"):
