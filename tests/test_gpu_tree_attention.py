@@ -360,3 +360,65 @@ def test_binding_refuses(dev):
             binding.pa_tree_attention(**dict(good, **{name: value}))
     with pytest.raises((E, TypeError)):
         binding.pa_tree_attention_fp8(**good, k_scale=1.0, v_scale=1.0)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("counts,context,hq,hkv,d", [([4, 2], [37, 0], 4, 4, 128), ([16, 9], [300, 121], 8, 4, 128), ([25], [500], 6, 6, 64),
+                                                     ([70, 64], [90, 64], 8, 2, 128)])
+def test_queries_that_are_not_finite(dev, counts, context, hq, hkv, d, kind, fp8):
+    """A NaN or an infinity in a query makes that head's row of that node NaN; every other row keeps its bits."""
+    b = Batch(dev, 41, counts, context, hq, hkv, d, kind, fp8, 16)
+    for ws in (b.workspace(), None):
+        clean, query = b.run(ws), b.query
+        b.query = query.clone()
+        bad = {(0, 1): float("nan"), (1, 0): float("inf"), (b.total - 1, hq - 1): -float("inf"), (2, 2): float("nan")}
+        for (node, head), value in bad.items():
+            b.query[node, head, 5] = value
+        out = b.run(ws)
+        b.query = query
+        for (node, head) in bad:
+            assert out[node, head].isnan().all(), (node, head)
+            out[node, head] = clean[node, head]
+        assert (out == clean).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("kind,peak", [("f16", 60.0), ("bf16", 3e4)])
+def test_large_scores(dev, kind, peak, fp8):
+    """Scores of hundreds to 2^20 and more: one token takes the row (its neighbours are many units of the exponent away), in every
+    form of the kernels. The bound is that of rounding the output and V alone, for rows whose runner-up weighs less than 2^-40."""
+    import torch
+    for counts, context, hq, hkv, d in (([4], [60], 4, 4, 128), ([20], [300], 4, 4, 128), ([20], [300], 4, 4, 64), ([80], [300], 4, 2, 128)):
+        b = Batch(dev, 51, counts, context, hq, hkv, d, kind, fp8, 16)
+        b.query *= peak
+        q = b.query.double().cpu().numpy()
+        k, v = b.values(0)
+        seen = b.seen_of(0)
+        g = hq // hkv
+        for ws in (b.workspace(), None):
+            out = b.run(ws).double().cpu().numpy()
+            assert np.isfinite(out[:b.total]).all()
+            for i in range(b.total):
+                for h in range(hq):
+                    at = np.flatnonzero(seen[i])
+                    s = k[at, h // g] @ q[i, h] * b.scale * np.log2(np.e)
+                    top = np.argsort(-s)[:2]
+                    # fp32 scores of |q||k| D are off by 2^-24 of their terms' sum, and 8-bit terms of the queries by 2^-18 of
+                    # the largest element's.
+                    off = np.abs(k[at, h // g]).sum(1).max() * np.abs(q[i, h]).max() * b.scale * 2.0 ** (-17 if fp8 else -22)
+                    if s[top[0]] - s[top[1]] > 40 + 2 * off:
+                        want = v[at[top[0]], h // g]
+                        assert np.all(np.abs(out[i, h] - want) <= np.abs(want) * 2 * E_OUT[kind] + 2.0 ** -24), (i, h)
+
+
+def test_workspace_that_is_too_small(dev):
+    for counts, context, hq, hkv in (([4], [300], 4, 4), ([33], [9000], 8, 2)):
+        b = Batch(dev, 2, counts, context, hq, hkv, 128, "bf16", False, 16)
+        ws = b.workspace()
+        with pytest.raises(binding.PAError) as e:
+            b.run(ws[:ws.numel() - 256])
+        assert e.value.code == binding.PA_ERR_WORKSPACE
+        with pytest.raises(binding.PAError) as e:
+            b.run(ws[16:])
+        assert e.value.code in (binding.PA_ERR_WORKSPACE, binding.PA_ERR_INVALID_ARG)
