@@ -223,6 +223,19 @@ constexpr int decode_stages()
 }
 constexpr int kTile = 16;       // tokens per tile (the MMA's M)
 constexpr int kMinShare = 8;    // ragged: tiles of a share at least
+// A tree's few nodes: a warp takes its tiles one after another and a piece is
+// merged with the others of its segment, so a segment of L tiles in shares of s
+// waits about s * (a tile) + L / s * (a piece): s grows as the root of L.
+// Measured with shares of 8, of 1 and of this rule (us): 22 sequences of up to 44
+// tokens 28.3, 10.9, 11.2; 31 of up to 314 20.3, 12.9, 13.2; 4 of 1000 24.1, 35.6,
+// 22.9; one of 6000 26.3, 44.7, 29.0; with more than 8 for every warp all the same.
+__device__ __forceinline__ int tree_share(long long tiles)
+{
+    int share = 1;
+    while (share < kMinShare && 6 * (share + 1) * (share + 1) <= tiles)
+        ++share;
+    return share;
+}
 constexpr int kMaxSeqs = 4096;  // sequences per pa_decode call (prefix lives in smem)
 
 // One pipeline stage: a 16-token tile of one kv head, K rows then V rows.
@@ -491,7 +504,8 @@ __global__ void __launch_bounds__(decode_warps<D, NT, FP8, FORM != kOneQuery>() 
     // 2. This warp's contiguous share of the unit sequence.
     // Ragged: with few tiles fewer warps get a share, of kMinShare tiles at
     // least (fewer pieces to merge), and those spread over the SMs.
-    const int owners = RAGGED ? (int)max(1LL, min((long long)p.total_warps, N / kMinShare)) : p.total_warps;
+    const int min_share = TREE ? tree_share(N / ((long long)S * segs_per_seq)) : kMinShare;
+    const int owners = RAGGED ? (int)max(1LL, min((long long)p.total_warps, N / min_share)) : p.total_warps;
     const int gw = owners < p.total_warps ? warp * gridDim.x + blockIdx.x : blockIdx.x * kWarps + warp;
     const long long r0 = share_lo(N, gw, owners);
     const long long r1 = share_lo(N, gw + 1, owners);
@@ -595,6 +609,9 @@ __global__ void __launch_bounds__(decode_warps<D, NT, FP8, FORM != kOneQuery>() 
     // whether some V element of its nodes was not finite.
     [[maybe_unused]] long long seg_at = 0, nodes_at = 0;
     [[maybe_unused]] bool poisoned = false;
+    // The masks of this thread's score columns (a tile's columns are at most 16,
+    // so a sequence's nodes are too): all ones where the column is none.
+    [[maybe_unused]] uint32_t node_mask[NT][2];
 
     auto seg_coords = [&](int seg, int &s, int &segl, int &hq0) {
         s = seg / segs_per_seq;
@@ -616,12 +633,6 @@ __global__ void __launch_bounds__(decode_warps<D, NT, FP8, FORM != kOneQuery>() 
         }
     };
 
-    // Tree: the mask of column col's query; null if it is none of s's.
-    [[maybe_unused]] auto mask_of = [&](int s, int col) -> const uint32_t * {
-        const int q = col / p.tile_heads;
-        return q < rows[s].y ? p.tree_masks + (long long)(rows[s].x + q) * p.mask_words : nullptr;
-    };
-
     auto begin_segment = [&](int seg) {
         int s, segl, hq0;
         seg_coords(seg, s, segl, hq0);
@@ -629,6 +640,15 @@ __global__ void __launch_bounds__(decode_warps<D, NT, FP8, FORM != kOneQuery>() 
             seg_at = prefix[s] + (long long)segl * ((lens[s] + kTile - 1) / kTile);
             nodes_at = seg_at + (lens[s] - rows[s].y) / kTile;
             poisoned = false;
+            const int n = rows[s].y;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int q = (nt * 8 + 2 * tig + e) / p.tile_heads;
+                    node_mask[nt][e] = q < n ? __ldg(p.tree_masks + (long long)(rows[s].x + q) * p.mask_words) & ((1u << n) - 1u)
+                                             : ~0u;
+                }
         }
         const uint16_t *qbase = p.query + ((long long)(RAGGED ? rows[s].x : s) * p.num_q_heads + hq0) * D;
 #pragma unroll
@@ -727,14 +747,9 @@ __global__ void __launch_bounds__(decode_warps<D, NT, FP8, FORM != kOneQuery>() 
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const uint32_t *mask = mask_of(s, nt * 8 + 2 * tig + e);
-                        uint32_t any = mask ? 0u : 1u;
-                        for (int k = 0; mask && 32 * k < n; ++k)
-                            any |= n - 32 * k >= 32 ? mask[k] : mask[k] & ((1u << (n - 32 * k)) - 1u);
-                        if (any == 0u)
+                    for (int e = 0; e < 2; ++e)
+                        if (node_mask[nt][e] == 0u)
                             lsum[nt][e] = 1.f;
-                    }
             }
             if (poisoned) {
                 // The elements of V zeroed below, to the columns that see them.
@@ -760,8 +775,7 @@ __global__ void __launch_bounds__(decode_warps<D, NT, FP8, FORM != kOneQuery>() 
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const uint32_t *mask = mask_of(s, nt * 8 + 2 * tig + e);
-                            if (mask && (mask[node >> 5] >> (node & 31) & 1u)) {
+                            if (node_mask[nt][e] >> node & 1u) {
 #pragma unroll
                                 for (int mt = 0; mt < KS; ++mt) {
                                     acc[mt][nt][e] += extra(FP8 ? VB * g + 2 * mt : 16 * mt + g);
@@ -904,23 +918,20 @@ __global__ void __launch_bounds__(decode_warps<D, NT, FP8, FORM != kOneQuery>() 
                 const int first = (int)(i - seg_at) * kTile - (lens[s] - n);  // node of the tile's first token
                 seen = 0u;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int h = 0; h < 2; ++h) {
+                    const int node = first + g + 8 * h;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const uint32_t *mask = mask_of(s, nt * 8 + 2 * tig + e);
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int node = first + g + 8 * h;
-                            if (node < 0 || (node < n && (!mask || (__ldg(mask + (node >> 5)) >> (node & 31) & 1u))))
+                        for (int e = 0; e < 2; ++e)
+                            if (node < 0 || (node < n && (node_mask[nt][e] >> node & 1u)))
                                 seen |= 1u << (4 * nt + 2 * h + e);
-                        }
-                    }
+                }
                 constexpr int CPR = Geo::kRowBytes / 16;
+                const int r0n = max(0, -first), count = (min(kTile, n - first) - r0n) * CPR;  // the nodes' chunks
                 bool found = false;
-                for (int z = lane; z < kTile * CPR * Geo::kBoxes; z += 32) {
-                    const int bx = z / (kTile * CPR), rem = z - bx * (kTile * CPR), r = rem / CPR;
-                    if (first + r < 0 || first + r >= n)
-                        continue;
+                for (int z = lane; z < count * Geo::kBoxes; z += 32) {
+                    const int bx = z >= count ? 1 : 0, rem = z - bx * count, r = r0n + rem / CPR;
                     const uint32_t at = sbuf + bx * Geo::kBoxBytes + Geo::kVOffset + r * Geo::kRowBytes + (rem % CPR) * 16;
                     const uint4 v = lds128(at);
                     const uint32_t x[4] = {v.x, v.y, v.z, v.w};

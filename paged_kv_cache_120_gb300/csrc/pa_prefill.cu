@@ -233,10 +233,16 @@ int check_call(const char *who, const void *out, const void *query, const void *
 // units an SM over 400 / 1404 / 6404 states 35 / 51 / 117 and 18 / 31 / 118 us
 // (78 and 102 over 1 .. 6404), 0.1 an SM 20 / 23 / 33 and 17 / 29 / 100, 2.1 an
 // SM 57 / 91 / 262 and 45 / 87 / 336.
-bool cross_splits(long long units, int sms, long long max_len)
+// Trees: 9 + 12 u, as a tile of theirs takes less than one of a cross batch
+// beside what a cut unit costs. Shared against whole: 0.1 units an SM over
+// 23371 tokens 33 and 194, 0.2 over 4425 37 and 54, 0.7 over 1 .. 5935 55 and
+// 72, 3.4 over 4096 267 and 273; 1.05 over 57 .. 1139 26 and 18, 3.9 over 1 ..
+// 4801 (FP8) 176 and 160 us. (2.5 over 0 .. 8191, FP8: 163 and 153, shared:
+// were all of the longest, whole units would take three rounds for 2.5.)
+bool cross_splits(long long units, int sms, long long max_len, bool tree)
 {
     const double u = (double)units / sms, tiles = (double)((max_len + kN - 1) / kN) + 2.0;
-    return (std::ceil(u) - 0.75 * u) * tiles > 9.0 + 5.0 * u;
+    return (std::ceil(u) - 0.75 * u) * tiles > 9.0 + (tree ? 12.0 : 5.0) * u;
 }
 
 // What a call's queries see.
@@ -279,7 +285,7 @@ int prefill_impl(const char *who, void *out, const void *query, const void *kv_c
         return set_error(PA_ERR_WORKSPACE, "%s: workspace of %zu bytes at %p (need %zu, 256-byte aligned)", who,
                          workspace_bytes, workspace, lp.split_bytes);
     if (sees != Sees::kCausal)
-        split = split && cross_splits(lp.units, sms, (long long)max_blocks_per_seq * block_size);
+        split = split && cross_splits(lp.units, sms, (long long)max_blocks_per_seq * block_size, sees == Sees::kTree);
 
     TreeParams prm;  // the other kinds take its first part
     prm.out = out;
