@@ -50,6 +50,10 @@
 //    sequences first, that running CTAs take over (cluster launch control); if
 //    no chunk passes one query tile, both halves of the tensor memory work on
 //    that tile (SOLO).
+//  * Tree attention (pa_tree_attention) runs as cross attention does, with a
+//    softmax loop of its own for the tiles that hold nodes, whose masks decide
+//    there; one query tile is worked on by both softmax warpgroups, half of a
+//    tile's columns each, and an FP8 cache's K is not widened (see the kinds).
 //  * Every wait is bounded; K/V rows past a sequence's end (padding slots,
 //    possibly NaN) are zeroed before P V reads them.
 #pragma once

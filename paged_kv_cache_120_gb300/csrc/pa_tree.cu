@@ -917,9 +917,6 @@ using namespace pa;
 
 namespace {
 
-// Attributes of the verify kernels and of pa_build_tree's, set once per
-// device, so that a call being captured into a CUDA graph makes no such call;
-// the SM count with them.
 template <typename T>
 const void *verify_fn(int mode)
 {
@@ -938,7 +935,8 @@ const void *verify_kernel(int dtype, int mode)
     return dtype == PA_F32 ? verify_fn<float>(mode) : dtype == PA_BF16 ? verify_fn<__nv_bfloat16>(mode) : verify_fn<__half>(mode);
 }
 
-int tree_setup(const char *who, int *sms_out)
+// The current device's SM count, asked for once per device.
+int sm_count_of(const char *who, int *sms_out)
 {
     static std::mutex mu;
     static int sm_count[64] = {};
@@ -951,7 +949,7 @@ int tree_setup(const char *who, int *sms_out)
     if (sms == 0) {
         e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
         if (e != cudaSuccess)
-            return set_error(PA_ERR_CUDA, "%s: kernel attributes: %s", who, cudaGetErrorString(e));
+            return set_error(PA_ERR_CUDA, "%s: SM count: %s", who, cudaGetErrorString(e));
         if (dev < 64)
             sm_count[dev] = sms;
     }
@@ -1011,7 +1009,7 @@ extern "C" int pa_verify_draft(int32_t *num_accepted, int32_t *path, int32_t *to
         !aligned(cu_seqlens_q, 4) || !aligned(uniforms, 4) || !aligned(target, elem) || !aligned(draft, elem))
         return set_error(PA_ERR_INVALID_ARG, "%s: misaligned pointer (4 B, rows their element's size)", who);
     int sms = 0;
-    const int rc = tree_setup(who, &sms);
+    const int rc = sm_count_of(who, &sms);
     if (rc != PA_OK)
         return rc;
     // CTAs a sequence: as many as run at once, up to those that leave a warp one
@@ -1100,7 +1098,7 @@ extern "C" int pa_commit_draft(void *const *kv_caches, int num_layers, const int
     if (columns > 0x3fffffffLL)
         return set_error(PA_ERR_UNSUPPORTED, "%s: %d layers of rows of %lld bytes are too many columns", who, num_layers, row_bytes);
     int sms = 0;
-    const int rc = tree_setup(who, &sms);
+    const int rc = sm_count_of(who, &sms);
     if (rc != PA_OK)
         return rc;
     // A CTA looks its sequence's slots up once and then takes several columns a
