@@ -945,6 +945,27 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    if constexpr (!SPLIT && CROSS) {
+        // Longest sequences first, so that no long unit is left for the
+        // end (40 x up to 224 queries over 1 .. 1500 states, 20 heads of
+        // 64: 91 us as they come, 79 us so; 39 x 243 over up to 16941: 685
+        // and 539 us): a sequence's place is the number of longer ones, counted
+        // by two threads each (75 sequences, 8 heads, a K/V tile each: 25.2 us by one
+        // warp behind this barrier, 18.3 so).
+        static_assert(kOrderedSeqs * 2 <= 256, "two threads a sequence");
+        if (p.num_seqs <= kOrderedSeqs && tid < 2 * kOrderedSeqs && (tid & ~31) < 2 * p.num_seqs) {
+            const int s = tid >> 1, len = s < p.num_seqs ? p.seq_lens[s] : 0;
+            int place = 0;
+#pragma unroll 4
+            for (int k = tid & 1; k < p.num_seqs; k += 2) {
+                const int other = p.seq_lens[k];
+                place += other > len || (other == len && k < s);
+            }
+            place += __shfl_xor_sync(kFull, place, 1);
+            if (s < p.num_seqs && (tid & 1) == 0)
+                order[place] = (uint8_t)s;
+        }
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -1062,31 +1083,6 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                 }
                 done += __shfl_sync(kFull, incl, 31);
             }
-        }
-        if (!SPLIT && CROSS && p.num_seqs <= kOrderedSeqs) {
-            // Longest sequences first, so that no long unit is left for the
-            // end (40 x up to 224 queries over 1 .. 1500 states, 20 heads of
-            // 64: 91 us as they come, 79 us so; 39 x 243 over up to 16941: 685
-            // and 539 us): a sequence's place is the number of longer ones.
-            int len[kOrderedSeqs / 32], place[kOrderedSeqs / 32];
-#pragma unroll
-            for (int k = 0; k < kOrderedSeqs / 32; ++k) {
-                len[k] = 32 * k + lane < p.num_seqs ? p.seq_lens[32 * k + lane] : 0;
-                place[k] = 0;
-            }
-#pragma unroll
-            for (int b = 0; b < kOrderedSeqs / 32; ++b)
-                for (int i = 0; i < min(32, p.num_seqs - 32 * b); ++i) {
-                    const int other = __shfl_sync(kFull, len[b], i);
-#pragma unroll
-                    for (int k = 0; k < kOrderedSeqs / 32; ++k)
-                        place[k] += other > len[k] || (other == len[k] && 32 * b + i < 32 * k + lane);
-                }
-#pragma unroll
-            for (int k = 0; k < kOrderedSeqs / 32; ++k)
-                if (32 * k + lane < p.num_seqs)
-                    order[place[k]] = (uint8_t)(32 * k + lane);
-            __syncwarp();
         }
         if (lane == 0) {
             // Whole units: the grid has a CTA per unit; this one starts with
