@@ -370,46 +370,10 @@ __device__ __forceinline__ float add_pair(float acc, uint32_t w)
     return acc;
 }
 
-// 2^x0, 2^x1 on the FMA pipe, without the MUFU unit that ex2 uses: x = j + f
-// with j = round(x) (adding and subtracting 1.5 * 2^23 rounds to an integer
-// in fp32 for |x| < 2^22) and f in [-1/2, 1/2] exact, then p(f) ~ 2^f by the
-// minimax polynomial of degree DEG (coefficients from a Remez exchange fit of
-// the relative error, printed by paged_kv_cache_120_gb300/exp2_poly.py; max
-// relative error 7.5e-5 at degree 3, 2.7e-6 at degree 4), then j added to
-// p's exponent field. Inputs below -126 are clamped there (2^-126 or less
-// rounds to zero or to a negligible subnormal in the 16-bit P); NaN stays
-// NaN (max.NaN keeps it, and the exponent add leaves NaN bits NaN).
+// 2^x0, 2^x1 on the FMA pipe; used by the causal and cross kinds alone, and
+// defined beside them (pa_prefill.cu).
 template <int DEG>
-__device__ __forceinline__ void exp2_poly2(uint64_t x2, float &y0, float &y1)
-{
-    float x0, x1;
-    unpk2(x2, x0, x1);
-    asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(x0));  // -126
-    asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(x1));
-    const uint64_t xv = pk2(x0, x1);
-    const uint64_t magic = pk2(12582912.f, 12582912.f), nmagic = pk2(-12582912.f, -12582912.f);
-    const uint64_t j = add2(xv, magic);           // round(x) in the low mantissa bits
-    const uint64_t t = add2(j, nmagic);           // round(x) as a float
-    uint64_t f;
-    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(f) : "l"(xv), "l"(t));
-    uint64_t p;
-    if constexpr (DEG == 4) {
-        p = fma2(pk2(0x1.3997d6p-7f, 0x1.3997d6p-7f), f, pk2(0x1.ca1440p-5f, 0x1.ca1440p-5f));
-        p = fma2(p, f, pk2(0x1.ec06dap-3f, 0x1.ec06dap-3f));
-        p = fma2(p, f, pk2(0x1.62e0dcp-1f, 0x1.62e0dcp-1f));
-        p = fma2(p, f, pk2(0x1.ffffe8p-1f, 0x1.ffffe8p-1f));
-    } else {
-        static_assert(DEG == 3, "degree 3 or 4");
-        p = fma2(pk2(0x1.c3f760p-5f, 0x1.c3f760p-5f), f, pk2(0x1.f0de1ap-3f, 0x1.f0de1ap-3f));
-        p = fma2(p, f, pk2(0x1.62f31ap-1f, 0x1.62f31ap-1f));
-        p = fma2(p, f, pk2(0x1.fff692p-1f, 0x1.fff692p-1f));
-    }
-    float p0, p1, j0, j1;
-    unpk2(p, p0, p1);
-    unpk2(j, j0, j1);
-    y0 = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(j0) << 23));
-    y1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(j1) << 23));
-}
+__device__ __forceinline__ void exp2_poly2(uint64_t x2, float &y0, float &y1);
 
 // 32 consecutive 32-bit columns of this thread's TMEM lane from raw words.
 __device__ __forceinline__ void tc_st32u(uint32_t taddr, const uint32_t *v)
@@ -2243,9 +2207,13 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                         for (int c = 0; c < kN / 2; ++c) {
                             const uint64_t x2 = fma2(pk2(sv[2 * c], sv[2 * c + 1]), sc2, nref2);
                             float p0, p1;
-                            if (kPolyEvery > 0 && c % (kPolyEvery > 0 ? kPolyEvery : 1) == kPolyEvery - 1) {
-                                exp2_poly2<kMmaBF16 ? 3 : 4>(x2, p0, p1);
-                            } else {
+                            bool poly = false;
+                            if constexpr (kPolyEvery > 0 && !TREE) {
+                                poly = c % (kPolyEvery > 0 ? kPolyEvery : 1) == kPolyEvery - 1;
+                                if (poly)
+                                    exp2_poly2<kMmaBF16 ? 3 : 4>(x2, p0, p1);
+                            }
+                            if (!poly) {
                                 float x0, x1;
                                 unpk2(x2, x0, x1);
                                 p0 = ex2(x0);
