@@ -422,3 +422,24 @@ def test_workspace_that_is_too_small(dev):
         with pytest.raises(binding.PAError) as e:
             b.run(ws[16:])
         assert e.value.code in (binding.PA_ERR_WORKSPACE, binding.PA_ERR_INVALID_ARG)
+
+
+@pytest.mark.parametrize("seqs", [33, 128, 129])
+@pytest.mark.parametrize("values", [(7,), (0, 5, 130, 131, 290)])
+def test_many_sequences_of_equal_and_unequal_lengths(dev, seqs, values):
+    """Whole units are taken longest sequence first, up to 128 of them; every row is there once."""
+    rng = np.random.default_rng(seqs)
+    counts, context = rng.integers(0, 12, seqs), rng.choice(values, seqs)
+    b = Batch(dev, seqs, counts.tolist(), context.tolist(), 4, 2, 64, "f16", False, 16)
+    b.check(b.run())
+
+
+@pytest.mark.parametrize("seqs, longest", [(1, 0), (1, 500), (1, 7000), (3, 1100), (9, 60), (40, 1500)])
+@pytest.mark.parametrize("fp8", [False, True], ids=["16", "fp8"])
+def test_few_rows_shared_out_by_length(dev, seqs, longest, fp8):
+    """Few rows: a warp's share grows with the segments' lengths."""
+    rng = np.random.default_rng(longest + seqs)
+    counts = rng.integers(1, 5, seqs)
+    context = rng.integers(longest // 2, longest + 1, seqs)
+    b = Batch(dev, seqs, counts.tolist(), context.tolist(), 8, 2, 128, "bf16", fp8, 16)
+    b.check(b.run(b.workspace()))
