@@ -811,6 +811,13 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
     constexpr int kTerms = native_terms(BF16), kNativeStg = native_staging(COOP);
     __shared__ uint64_t native_k[kNative ? 2 * kNativeKMax : 1];                 // K stages full, then empty
     __shared__ uint64_t native_stg[kNative ? 4 * kNativeStagingMax : 1];         // a widening warp's buffer has landed
+    // Two query tiles, native: tile B's terms are there (q_ready: tile A's). A barrier
+    // each, because nothing but a tile's own scores holds its threads back: those of a
+    // tile B without queries run up to kUnitSlots items ahead, and arrivals of theirs on
+    // one barrier for both would complete tile A's phase in its place. A tile's threads
+    // arrive only for items in which it has queries, once each, and write an item's terms
+    // only after their tile's last P V of the item before, when its scores are done too.
+    __shared__ uint64_t native_qb[1];
     __shared__ uint64_t coop_q[COOP ? 4 : 1];       // Q of an even / odd item has landed, is no longer read
     __shared__ uint64_t coop_pair[COOP ? 4 : 1];    // the two warps of a quarter of the rows meet
     __shared__ float coop_row[COOP ? 2 * kM : 1];   // a row's extremum or sum, of either half
@@ -846,6 +853,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
     auto sV = [&](int st) { return base + kOffV + st * kTileBytes; };
     const uint32_t b_q = smem_addr(&bars.q_full), b_qe = smem_addr(&bars.q_empty);
     const uint32_t b_qr = smem_addr(&bars.q_ready);
+    [[maybe_unused]] const uint32_t b_qrb = smem_addr(&native_qb[0]);
     auto b_kf = [&](int st) { return smem_addr(kNative ? &native_k[st] : &bars.k_full[st]); };
     auto b_ke = [&](int st) { return smem_addr(kNative ? &native_k[kNativeKMax + st] : &bars.k_empty[st]); };
     auto b_vf = [&](int st) { return smem_addr(&bars.v_full[st]); };
@@ -858,7 +866,9 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
 
     if (tid == 0) {
         mbar_init(b_q, 1);
-        mbar_init(b_qr, 256);  // the 8 softmax warps
+        mbar_init(b_qr, kNative && !COOP ? 128 : 256);  // the softmax threads that bring Q
+        if constexpr (kNative && !COOP)
+            mbar_init(b_qrb, 128);
         mbar_init(b_qe, 1);
         if constexpr (!SPLIT)
             mbar_init(smem_addr(&claim_bar), 1);
@@ -1497,6 +1507,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                 commit(b_s(x));
             };
             int kc = 0, vc = 0, ui = 0;  // K tiles, V tiles and units consumed so far
+            [[maybe_unused]] int ub = 0;  // units with a tile B among them
             int gx[2] = {0, 0};          // P V of tile x issued so far
             bool go = true;
             for (int i = 0; go; ++i) {
@@ -1517,6 +1528,10 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                         break;
                 } else if (!all_ok(wait_or_fail(kQToF16 || kNative ? b_qr : b_q, ui & 1)))
                     break;
+                if constexpr (kNative && !COOP) {
+                    if (w.n[1] > 0 && !all_ok(wait_or_fail(b_qrb, ub++ & 1)))
+                        break;
+                }
                 ++ui;
                 tc_fence_after();
                 if constexpr (COOP) {
@@ -1726,6 +1741,10 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
             [[maybe_unused]] const uint32_t *mask_row = nullptr;
             [[maybe_unused]] bool blank = false;
             if constexpr (TREE) {
+                if (!COOP && w.n[x] == 0) {  // the tile has no queries: nothing to bring, nobody waits for it
+                    vbase += j1 - j0;
+                    continue;
+                }
                 if (valid) {
                     mask_row = p.tree_masks + (long long)(w.q0 + w.t0[SOLO || COOP ? 0 : x] + t) * p.mask_words;
                     if (context == 0) {
@@ -1796,7 +1815,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                                    code[term][1], code[term][2], code[term][3]);
                     }
                     fence_proxy_async();  // the terms, for the score MMAs
-                    mbar_arrive(b_qr);
+                    mbar_arrive(!COOP && x == 1 ? b_qrb : b_qr);
                 }
             }
             if constexpr (kQToF16) {
@@ -1845,10 +1864,6 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                 constexpr int kCols = COOP ? kN / 2 : kN, kOut = COOP ? D / 2 : D;
                 const int col0 = COOP ? x * kCols : 0;
                 const uint32_t tO1 = COOP ? tmem + 384u + lane_off + x * kOut : tO(x) + lane_off;
-                if (!COOP && w.n[x] == 0) {  // the tile has no queries
-                    vbase += j1 - j0;
-                    continue;
-                }
                 // Meet the other half's warp: bounded, as every wait, and shared
                 // memory written before is visible after it.
                 auto pair_sync = [&] {
