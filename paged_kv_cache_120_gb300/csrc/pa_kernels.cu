@@ -950,6 +950,8 @@ __global__ void __launch_bounds__(decode_warps<D, NT, FP8, FORM != kOneQuery>() 
                         found = true;
                     }
                 }
+                if (found)
+                    fence_proxy_async();  // every lane's own stores, ahead of the stage's next TMA write
                 poisoned |= __any_sync(kFull, found);
                 __syncwarp();
             }
