@@ -1972,6 +1972,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                                 if (COOP && !__all_sync(kFull, wait_or_fail(b_pv(0), (gx - 1) & 1)))
                                     return false;
                                 tc_fence_after();
+                                __syncwarp();
 #pragma unroll 1
                                 for (int c = 0; c < kOut / 16; ++c) {
                                     float o[16];
@@ -2019,19 +2020,20 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                         } else {
                             uint32_t pw[kCols / 2];
                             fill(sv, pw, std::integral_constant<int, kCols>{});
-                        if constexpr (NODES) {
-                            if (sc == 0.f) {  // a masked score gave 0 x inf = NaN
+                            if constexpr (NODES) {
+                                if (sc == 0.f) {  // a masked score gave 0 x inf = NaN
 #pragma unroll
-                                for (int k = 0; k < 8; ++k)
-                                    l8[k] = 0.f;
+                                    for (int k = 0; k < 8; ++k)
+                                        l8[k] = 0.f;
 #pragma unroll
-                                for (int c = 0; c < kCols / 2; ++c) {
-                                    pw[c] &= (vis[c >> 4] >> (2 * c & 31) & 1u ? 0xFFFFu : 0u) |
-                                             (vis[c >> 4] >> (2 * c + 1 & 31) & 1u ? 0xFFFF0000u : 0u);
-                                    l8[c & 7] = add_pair<kMmaBF16>(l8[c & 7], pw[c]);
+                                    for (int c = 0; c < kCols / 2; ++c) {
+                                        pw[c] &= (vis[c >> 4] >> (2 * c & 31) & 1u ? 0xFFFFu : 0u) |
+                                                 (vis[c >> 4] >> (2 * c + 1 & 31) & 1u ? 0xFFFF0000u : 0u);
+                                        l8[c & 7] = add_pair<kMmaBF16>(l8[c & 7], pw[c]);
+                                    }
                                 }
+                                __syncwarp();  // the store below is the whole warp's
                             }
-                        }
 #pragma unroll
                             for (int c = 0; c < kCols / 2; c += 32)
                                 tc_st32u(tp + c, pw + c);
@@ -2058,6 +2060,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                             }
                         }
                         fence_proxy_async();
+                        __syncwarp();  // rows of nodes took longer
                     }
                     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                     tc_fence_before();
@@ -2107,12 +2110,11 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
 #pragma unroll 1
                 for (int c = 0; c < kOut / 32; ++c) {
                     float o[32];
+                    __syncwarp();  // the load is the whole warp's: lanes part below, and in add_nonfinite
                     tc_ld32(tO1 + c * 32, o);
                     if (poisoned)
                         add_nonfinite<BF16, FP8, D>(p, w, mask_row, j0 * kN, j1 * kN, (COOP ? x * (kOut / 32) : 0) + c, o);
-                    if (!valid)
-                        continue;
-                    if (whole) {
+                    if (valid && whole) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             uint4 e;
@@ -2122,13 +2124,14 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                             e.w = pack2<BF16>(o[8 * q + 6] * inv, o[8 * q + 7] * inv);
                             reinterpret_cast<uint4 *>(out + c * 32)[q] = e;
                         }
-                    } else {
+                    } else if (valid) {
                         float4 *po = reinterpret_cast<float4 *>(p.part_o + (size_t)slot * D + (COOP ? x * kOut : 0));
 #pragma unroll
                         for (int q = 0; q < 8; ++q)
                             po[c * 8 + q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
                     }
                 }
+                __syncwarp();
                 if (!whole && valid && (!COOP || x == 0))
                     p.part_ml[slot] = make_float2(r_ref == none ? -INFINITY : __fmul_rn(r_ref, sc), l_run);
                 tc_fence_before();

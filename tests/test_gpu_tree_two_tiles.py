@@ -3,6 +3,7 @@ tile has no queries. The bounds are those of test_gpu_tree_attention.py."""
 import numpy as np
 import pytest
 
+import test_gpu_tree_attention as single
 from test_gpu_tree_attention import Batch, dev  # noqa: F401
 
 from paged_kv_cache_120_gb300 import binding
@@ -49,3 +50,14 @@ def test_second_tiles_that_come_and_go(dev, kind):  # noqa: F811
     for _ in range(8):
         assert (b.run() == out).all(), "two runs differ"
     assert binding.pa_get_device_error() == 0
+
+
+@pytest.mark.parametrize("fp8", [True, False], ids=["fp8", "16"])
+@pytest.mark.parametrize("hq,hkv,d", [(16, 2, 128), (12, 2, 64), (32, 8, 128)])
+def test_nonfinite_nodes_in_warps_of_uneven_rows(dev, hq, hkv, d, fp8):  # noqa: F811
+    """The rows of a warp see different numbers of nodes whose V is not finite, and some rows are nobody's: lanes part while those
+    are added, and the warp meets again before its next read of tensor memory."""
+    rng = np.random.default_rng(hq + d)
+    for most in (9, 45):  # one query tile, and two
+        counts = rng.integers(2, most + 1, 80)
+        single.test_nonfinite_nodes_reach_only_who_sees_them(dev, counts.tolist(), rng.integers(0, 150, 80).tolist(), hq, hkv, d, "bf16", fp8)
