@@ -145,7 +145,8 @@ __device__ __forceinline__ Sum running(Sum s)
     return s;
 }
 
-// max(p - a q, 0) as a pair, a >= 0: the product's and the difference's
+// max(p - a q, 0) as a pair, a >= 0, q >= 0 (the callers make entries that are not
+// above 0, NaN among them, 0: they would add to what is left): the product's and the difference's
 // rounding errors are kept ((p - d) - m is the latter's where p >= m, and only
 // there it counts). Anything not above 0 (NaN too) is 0.
 __device__ __forceinline__ Sum weight(float p, float q, const Sum &a)
@@ -328,7 +329,7 @@ __global__ void __launch_bounds__(kVerifyThreads, verify_ctas(MODE)) verify_draf
             // The numbers that decide on this node.
             const bool in = has && (unsigned)x < (unsigned)V;
             s_p[i] = in ? to_float(target[(q0 + a) * p.target_stride + x]) : 0.f;
-            s_q[i] = in ? to_float(draft[(q0 + a) * p.draft_stride + x]) : 0.f;
+            s_q[i] = in ? fmaxf(to_float(draft[(q0 + a) * p.draft_stride + x]), 0.f) : 0.f;
             s_u[i] = p.uniforms[2 * (q0 + i)];
         }
         if (rank == 0) {
@@ -391,7 +392,7 @@ __global__ void __launch_bounds__(kVerifyThreads, verify_ctas(MODE)) verify_draf
             widen<T>(vq, y);
 #pragma unroll
             for (int k = 0; k < VEC; ++k)
-                w[k] = weight(x[k], y[k], a);
+                w[k] = weight(x[k], fmaxf(y[k], 0.f), a);
         } else {
 #pragma unroll
             for (int k = 0; k < VEC; ++k)
@@ -444,7 +445,7 @@ __global__ void __launch_bounds__(kVerifyThreads, verify_ctas(MODE)) verify_draf
             for (int k = 0; k < VEC; ++k) {
                 Sum2 w;
                 if (with_q)
-                    w = weight(pk2(x0[k], x1[k]), pk2(y0[k], y1[k]), a2, minus);
+                    w = weight(pk2(x0[k], x1[k]), pk2(fmaxf(y0[k], 0.f), fmaxf(y1[k], 0.f)), a2, minus);
                 else
                     w = Sum2{pk2(fmaxf(x0[k], 0.f), fmaxf(x1[k], 0.f)), 0ull};
                 if (k == 0)
