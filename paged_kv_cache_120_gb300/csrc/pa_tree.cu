@@ -601,8 +601,13 @@ __global__ void __launch_bounds__(kVerifyThreads, verify_ctas(MODE)) verify_draf
                 const Sum all = shfl(upto, 31);
                 add(run, all.hi, all.lo);
             }
-            if (found < 0) {  // rounding: the part's last positive entry
-                for (int v = r.v0 + lane; v < r.v1; v += 32) {
+            if (found < 0) {
+                // Rounding: a sum passed t that another order of its terms does not
+                // pass. The border is at the end of what was found last, the group of
+                // tiles or the part: its last positive entry.
+                const int lo = at >= 0 ? r.v0 + 32 * at * group : r.v0;
+                const int hi = at >= 0 ? min(r.v1, lo + 32 * group) : r.v1;
+                for (int v = lo + lane; v < hi; v += 32) {
                     Sum e[VEC];
                     weights(load(r.p, r.mis, v, true), with_q ? load(r.q, r.mis, v, r.q_vec) : none, a, e);
 #pragma unroll
