@@ -406,6 +406,7 @@ __global__ void __launch_bounds__(decode_warps<D, NT, FP8, FORM != kOneQuery>() 
 
     extern __shared__ uint8_t smem_raw[];
     __shared__ long long warp_sums[kWarps];
+    __shared__ int warp_live[TREE ? kWarps : 1];  // sequences with rows
 
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -432,6 +433,7 @@ __global__ void __launch_bounds__(decode_warps<D, NT, FP8, FORM != kOneQuery>() 
         const int per = (S + blockDim.x - 1) / blockDim.x;
         const int s0 = min(S, tid * per), s1 = min(S, s0 + per);
         long long local = 0;
+        [[maybe_unused]] int live = 0;
         for (int s = s0; s < s1; ++s) {
             int L = p.seq_lens[s];
             if constexpr (RAGGED) {
@@ -450,6 +452,13 @@ __global__ void __launch_bounds__(decode_warps<D, NT, FP8, FORM != kOneQuery>() 
             }
             lens[s] = L;
             local += (long long)((L + kTile - 1) / kTile) * segs_per_seq;
+            if constexpr (TREE)
+                live += L > 0;
+        }
+        if constexpr (TREE) {
+            live = __reduce_add_sync(kFull, live);
+            if (lane == 0)
+                warp_live[warp] = live;
         }
         long long incl = local;
 #pragma unroll
@@ -503,8 +512,15 @@ __global__ void __launch_bounds__(decode_warps<D, NT, FP8, FORM != kOneQuery>() 
 
     // 2. This warp's contiguous share of the unit sequence.
     // Ragged: with few tiles fewer warps get a share, of kMinShare tiles at
-    // least (fewer pieces to merge), and those spread over the SMs.
-    const int min_share = TREE ? tree_share(N / ((long long)S * segs_per_seq)) : kMinShare;
+    // least (fewer pieces to merge; tree: by the mean tiles of the segments that have
+    // any, as idle rows of a batch have none), and those spread over the SMs.
+    int min_share = kMinShare;
+    if constexpr (TREE) {
+        int live = 0;
+        for (int w = 0; w < kWarps; ++w)
+            live += warp_live[w];
+        min_share = tree_share(N / ((long long)max(1, live) * segs_per_seq));
+    }
     const int owners = RAGGED ? (int)max(1LL, min((long long)p.total_warps, N / min_share)) : p.total_warps;
     const int gw = owners < p.total_warps ? warp * gridDim.x + blockIdx.x : blockIdx.x * kWarps + warp;
     const long long r0 = share_lo(N, gw, owners);
