@@ -756,7 +756,8 @@ struct PrefillBars {
     uint64_t q_ready;  // FP8 cache, bf16 queries: the softmax threads have moved Q to fp16
     uint64_t stg_full[2][2];  // FP8 cache: K / V staging half 0 / 1 has landed
     // Per query tile x: s_full[x] its S is in TMEM, p_full[x] its P is,
-    // pv_done[x] its O += P V is done (one phase per K/V tile).
+    // pv_done[x] its O += P V is done (one phase per K/V tile). kTreeSolo: x is
+    // the K/V tile's number, even or odd.
     uint64_t s_full[2], p_full[2], pv_done[2];
     uint64_t unit_full[kUnitSlots], unit_empty[kUnitSlots];
     int unit_ring[kUnitSlots];  // unit index, or -1 once the launch's units are all taken
@@ -1563,7 +1564,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                         for (int k = 0; k < kN / 16; ++k)
                             mma_ts(tmem + 384u, tmem + 256u + 64u * b + k * 8, dv + (uint64_t)(k * (2048 >> 4)), id_o,
                                       (j > j0 || k > 0) ? 1u : 0u);
-                        commit(b_pv(0));
+                        commit(b_pv(b));
                         commit(b_ve(vs));
                         ++vc;
                         if (j + 2 < j1)
@@ -1872,6 +1873,13 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                         mbar_arrive(smem_addr(&coop_pair[quarter]));
                     return __all_sync(kFull, wait_or_fail(smem_addr(&coop_pair[quarter]), met++ & 1));
                 };
+                // Tile gx - 1's O += P V is done. COOP: scores run two tiles ahead of it,
+                // so that of tile gx - 2 may still be on its way here, and one barrier's
+                // parity could not tell the two apart: even and odd tiles have one each.
+                auto last_pv_done = [&] {
+                    return (bool)__all_sync(kFull, COOP ? wait_or_fail(b_pv((gx - 1) & 1), (gx - 1) >> 1 & 1)
+                                                        : wait_or_fail(b_pv(x), (gx - 1) & 1));
+                };
                 const bool active = __any_sync(kFull, valid);  // a warp without rows only keeps in step: its P may be anything
                 const float none = sc_pos ? -INFINITY : INFINITY;
                 float r_ref = none, l_run = 0.f;  // reference: a raw score (none yet: of no finite one)
@@ -1969,7 +1977,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                             if (j > j0) {
                                 // O: the last tile's O += P V was issued before this
                                 // tile's scores (COOP: waited for).
-                                if (COOP && !__all_sync(kFull, wait_or_fail(b_pv(0), (gx - 1) & 1)))
+                                if (COOP && !last_pv_done())
                                     return false;
                                 tc_fence_after();
                                 __syncwarp();
@@ -2079,7 +2087,7 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                 if (!alive)
                     break;
                 vbase += j1 - j0;
-                if (!__all_sync(kFull, wait_or_fail(b_pv(COOP ? 0 : x), (gx - 1) & 1))) {
+                if (!last_pv_done()) {
                     alive = false;
                     break;
                 }

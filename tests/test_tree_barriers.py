@@ -1,8 +1,10 @@
-"""A host model of how the chunk kernel's roles hand an item's queries on when trees of two query tiles attend over an FP8 cache:
-the softmax threads of tiles A and B write their tile's query terms and arrive, the MMA warp waits and multiplies. Barriers behave
-as mbarriers do (a phase ends with its count's arrival, a waiter sees the phase's parity), roles run in random order, and tile B's
-threads pass items in which B has no queries without waiting for anything but the ring that hands items on. Right is: every
-multiplication finds its own item's terms in place, and no term is overwritten that is still to be read."""
+"""Host models of waits in the chunk kernel's tree kinds. Barriers behave as mbarriers do (a phase ends with its count's arrival, a
+waiter sees the phase's parity), roles run in random order at random speeds.
+
+Trees of two query tiles over an FP8 cache: the softmax threads of tiles A and B write their tile's query terms and arrive, the MMA
+warp waits and multiplies; tile B's threads pass items in which B has no queries without waiting for anything but the ring that
+hands items on. Every multiplication has to find its own item's terms in place, and no term may be overwritten that is still to be
+read. Trees of one query tile: an item's O may be read only when its last P V is done."""
 import random
 
 import pytest
@@ -140,3 +142,87 @@ def test_the_model_with_queries_in_both_tiles():
     """Where both tiles always have queries one barrier would have been enough: both wait for the item's scores."""
     for seed in range(30):
         run(*patterns(random.Random(seed), "all"), one_barrier=True, seed=seed)
+
+
+def run_one_tile(tiles, alternate, seed):
+    """Trees of one query tile: scores run two K/V tiles ahead, so that a thread may have handed on its last weights while the P V of
+    the tile before is still waiting for slower threads. An item's O is read behind a wait for its last P V. alternate: even and odd
+    tiles' P V complete on a barrier each; else all on one."""
+    rng = random.Random(seed)
+    scores, weights = [Barrier(1), Barrier(1)], [Barrier(THREADS), Barrier(THREADS)]
+    done = [Barrier(1), Barrier(1)]
+    finished = [0]       # P V complete, in order
+    issued = []          # P V on their way
+    total = sum(tiles)
+
+    def softmax(_):
+        g = 0
+        for n in tiles:
+            for _ in range(n):
+                while not scores[g & 1].passed(g >> 1):
+                    yield
+                weights[g & 1].arrive()
+                g += 1
+                yield
+            last = g - 1
+            bar, parity = (done[last & 1], last >> 1) if alternate else (done[0], last)
+            while not bar.passed(parity):
+                yield
+            if finished[0] < g:
+                raise Fault(f"O is read before the P V of tile {last}: {finished[0]} are done")
+
+    def mma():
+        g = 0  # K/V tiles whose P V is issued
+        for n in tiles:
+            for _ in range(min(2, n)):
+                scores[(g + _) & 1].arrive()
+                yield
+            for j in range(n):
+                while not weights[g & 1].passed(g >> 1):
+                    yield
+                issued.append(g)
+                yield
+                if j + 2 < n:
+                    while finished[0] <= g:  # scores complete behind the P V issued before them
+                        yield
+                    scores[g & 1].arrive()
+                g += 1
+
+    def tensor_core():
+        while finished[0] < total:
+            if issued:
+                g = issued.pop(0)
+                finished[0] += 1
+                done[g & 1 if alternate else 0].arrive()
+            yield
+
+    roles = [softmax(t) for t in range(THREADS)] + [mma(), tensor_core()]
+    speed = [rng.random() ** 2 + 0.01 for _ in roles]
+    live, left = set(range(len(roles))), 200000
+    while live:
+        left -= 1
+        if left == 0:
+            raise Fault("nobody moves")
+        k = rng.choices(sorted(live), [speed[r] for r in sorted(live)])[0]
+        try:
+            next(roles[k])
+        except StopIteration:
+            live.discard(k)
+
+
+def test_the_last_p_v_is_waited_for():
+    for seed in range(150):
+        rng = random.Random(seed)
+        run_one_tile([rng.randint(1, 4) for _ in range(6)], True, seed)
+
+
+def test_one_barrier_for_all_p_v_would_not_do():
+    """Its parity takes the P V two tiles back for the last one's."""
+    faults = 0
+    for seed in range(150):
+        rng = random.Random(seed)
+        try:
+            run_one_tile([rng.randint(2, 4) for _ in range(6)], False, seed)
+        except Fault:
+            faults += 1
+    assert faults > 0
