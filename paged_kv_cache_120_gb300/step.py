@@ -307,22 +307,37 @@ class SpeculativeStep:
     positions and masks, then layer after layer the rotary write of its keys and
     values and the attention of its nodes, the verification against the target's
     rows, and the accepted nodes' keys and values moved into place in all layers,
-    lengths cut and surplus blocks returned. The caller fills ``qkv`` (one layer's
-    projections for all nodes; a model writes them layer by layer), ``tokens``,
-    ``parents``, ``query_lens`` (nodes per sequence), ``target`` and, if it draws,
-    ``draft`` and ``uniforms``; ``count``, ``path`` and ``new_tokens`` hold the
-    outcome and ``seq_lens`` the new lengths. ``capture()`` records the step in a
-    CUDA graph that later steps replay.
+    lengths cut and surplus blocks returned.
+
+    Before a step the caller fills ``tokens``, ``parents`` and ``query_lens``
+    (nodes per sequence, whose rows follow one another) and, if it draws,
+    ``draft`` and ``uniforms``. The model runs inside the step, at two points:
+
+    - ``project(step, layer)`` is called before each layer's rotary write and
+      fills ``step.qkv``, the layer's projections of all nodes, from
+      ``step.outs[layer - 1]``, the attention of the layer before (from
+      ``step.tokens`` at layer 0);
+    - ``head(step)`` is called behind the last layer's attention and fills
+      ``step.target``, the next token's distribution (logits if greedy) behind
+      each node.
+
+    Both enqueue their work on the current stream, and nothing that a CUDA graph
+    cannot hold if the step is captured. Where one is None, its buffer is what the
+    caller has put there before the step, one ``qkv`` for all layers (recorded
+    inputs). ``count``, ``path`` and ``new_tokens`` hold the outcome and ``seq_lens``
+    the new lengths. ``capture()`` records the step in a CUDA graph that later
+    steps replay.
 
     tables [S, width], seq_lens [S] and free_list (a stack, the free blocks in
     front, their number num_free) are int32 tensors of the running batch;
     max_nodes bounds a sequence's tree."""
 
     def __init__(self, pools, tables, seq_lens, free_list, num_free, num_q_heads, max_nodes, vocab, rope_plan, k_scale=1.0,
-                 v_scale=1.0, dtype=workloads.BF16, mode="draft", target_dtype=None):
+                 v_scale=1.0, dtype=workloads.BF16, mode="draft", target_dtype=None, project=None, head=None):
         import torch
         if mode not in ("greedy", "sample", "draft"):
             raise ValueError(f"mode must be 'greedy', 'sample' or 'draft', not {mode!r}")
+        self.project, self.head = project, head
         self.pools, self.tables, self.seq_lens, self.free_list, self.num_free = pools, tables, seq_lens, free_list, num_free
         self.plan, self.max_nodes, self.k_scale, self.v_scale = rope_plan, max_nodes, k_scale, v_scale
         _, _, self.block_size, hkv, d = pools[0].shape
@@ -351,7 +366,9 @@ class SpeculativeStep:
         b.pa_build_step(self.tables, self.seq_lens, self.query_lens, self.free_list, self.num_free, self.seq_lens, self.num_free,
                         self.cu, None, self.slots, self.admitted, self.block_size)
         b.pa_build_tree(self.parents, self.cu, self.seq_lens, self.positions, self.masks)
-        for pool, out in zip(self.pools, self.outs):
+        for layer, (pool, out) in enumerate(zip(self.pools, self.outs)):
+            if self.project is not None:
+                self.project(self, layer)
             write = (self.rotated, self.q, self.k, self.v, pool, self.slots, self.positions, self.plan)
             read = (out, self.rotated, pool, self.tables, self.cu, self.seq_lens, self.masks, self.scale, self.max_nodes)
             if self.fp8:
@@ -360,6 +377,8 @@ class SpeculativeStep:
             else:
                 b.pa_rope_and_cache(*write)
                 b.pa_tree_attention(*read, self.workspace)
+        if self.head is not None:
+            self.head(self)
         b.pa_verify_draft(self.count, self.path, self.new_tokens, self.tokens, self.parents, self.cu, self.target, self.draft,
                           self.uniforms)
         b.pa_commit_draft(self.pools, self.tables, self.cu, self.seq_lens, self.count, self.path, self.seq_lens, self.free_list,
