@@ -637,7 +637,15 @@ int pa_tree_attention(void *out, const void *query, const void *kv_cache,
                       void *workspace, size_t workspace_bytes, unsigned flags,
                       pa_stream_t stream);
 
-/* pa_tree_attention over an FP8 pool, with pa_prefill_fp8's conventions. */
+/*
+ * pa_tree_attention over an FP8 pool, with pa_prefill_fp8's conventions but for
+ * the queries of the tcgen05 tiles: their MMAs take K's codes as they are, and a
+ * head's row of a query as a sum of 8-bit terms under a power of two, two terms
+ * for bf16, three for fp16. What lies 2^-18 (bf16) or 2^-25 (fp16) below the row's
+ * largest element is lost: a score is off by at most that much of the largest
+ * |q| times the sum of |k|. Few rows hold bf16 queries as pa_decode_fp8 does and
+ * fp16 ones as they are, so the bound max_seqlen_q decides on this too.
+ */
 int pa_tree_attention_fp8(void *out, const void *query, const void *kv_cache,
                           const int32_t *block_tables, int max_blocks_per_seq,
                           const int32_t *cu_seqlens_q, const int32_t *seq_lens,
@@ -660,7 +668,7 @@ int pa_tree_attention_workspace_size(int num_seqs, int max_seqlen_q, int num_q_h
  * token that follows, from given random numbers. From the root on, at a node
  * with the target's row p (the next token's distribution after it):
  *   greedy  (uniforms NULL): y is p's largest entry (the first of equals; NaN
- *           is passed over). The first child holding y is accepted, else y is
+ *           is passed over; 0 if none is above -inf). The first child holding y is accepted, else y is
  *           the sequence's new token. p may hold logits.
  *   sample  (uniforms, draft NULL): y is drawn from p with the node's second
  *           number; then as above. For children that were chosen, not drawn:
@@ -687,7 +695,8 @@ int pa_tree_attention_workspace_size(int num_seqs, int max_seqlen_q, int num_q_h
  *   target, draft device, rows of vocab_size entries, one per node, target_stride
  *                 and draft_stride elements apart (>= vocab_size); row i is the
  *                 distribution behind node i. Probabilities are taken as given:
- *                 finite, summing to about 1. Entries not above 0 weigh 0.
+ *                 finite, summing to about 1. Entries not above 0 (NaN among them)
+ *                 weigh 0, in both.
  *   dtype         PA_F16, PA_BF16 or PA_F32, of both
  *   uniforms      device, [total_q][2] fp32 in [0, 1), or NULL
  * num_seqs <= 4096, at most PA_MAX_TREE_NODES nodes a sequence. Outputs overlap

@@ -1995,9 +1995,12 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                                 return false;
                         }
                         // P = 2^((s - reference) scale), rounded to the element type, in
-                        // pairs; the row sum adds the rounded values. The difference comes
-                        // first, so that the largest score's argument is small however
-                        // large the scores.
+                        // pairs: an MMA takes both operands in one 16-bit type, and P in
+                        // two terms would be twice its P V. Against 64 bits the rows are
+                        // off by 0.0023 rms in bf16 (0.0017 by the output's rounding alone)
+                        // and 0.00026 in fp16 (0.00021). The row sum adds the rounded
+                        // values, in 32 bits. The difference comes first, so that the
+                        // largest score's argument is small however large the scores.
                         const float ref = r_ref == none ? 0.f : r_ref;
                         const uint64_t sc2 = pk2(sc, sc), nref2 = pk2(-ref, -ref);
                         float l8[8];
