@@ -1968,11 +1968,9 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                                 const float other = coop_row[(x ^ 1) * kM + r];
                                 e = sc_pos ? fmaxf(e, other) : fminf(e, other);
                             }
-                            float alpha = 1.f;
-                            if (exceeds(e)) {
-                                alpha = r_ref == none ? 0.f : ex2(__fmul_rn(r_ref - e, sc));
-                                r_ref = e;
-                            }
+                            const bool up = exceeds(e);  // selects: lanes stay together for the loads below
+                            const float alpha = !up ? 1.f : r_ref == none ? 0.f : ex2(__fmul_rn(r_ref - e, sc));
+                            r_ref = up ? e : r_ref;
                             l_run *= alpha;
                             if (j > j0) {
                                 // O: the last tile's O += P V was issued before this
@@ -1980,7 +1978,6 @@ __global__ void __launch_bounds__(threads_for(FP8), 1)
                                 if (COOP && !last_pv_done())
                                     return false;
                                 tc_fence_after();
-                                __syncwarp();
 #pragma unroll 1
                                 for (int c = 0; c < kOut / 16; ++c) {
                                     float o[16];
